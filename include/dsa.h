@@ -463,6 +463,128 @@ int dsa_topk_merge(const float* scores, int64_t scores_ld, const int32_t* idx,
 int dsa_topk_noalloc(const float* logits, int64_t ld, const int32_t* row_ends,
                      int64_t rows, int64_t width, int64_t k, int32_t* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention beside the indexer: a paged key/value cache, the append that
+ * writes it with the position rotation on the way, and the attention that
+ * reads it, over all keys of a request (with a prefix the batch may share) or
+ * over the keys the indexer selected.  The indexer pages name this path
+ * ("scoring and top-k", then the attention core) without printing it.
+ */
+
+/* 16-bit element types of the attention calls. */
+typedef enum { DSA_BF16 = 0, DSA_FP16 = 1 } dsa_dtype;
+
+/*
+ * A paged key/value cache: two pools of num_pages pages of 64 tokens.  Element
+ * c of head h of token t of page p is at
+ *   k[p * k_page_stride + t * k_token_stride + h * k_head_stride + c]
+ * and likewise in v (strides in elements, so token-major and head-major pages,
+ * and pools that interleave layers, are all views).  Pools 16-byte aligned;
+ * strides multiples of 8 elements.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int64_t num_pages;
+    int64_t heads;   /* key/value heads */
+    int64_t dim;     /* columns per head, a multiple of 16 */
+    int32_t dtype;   /* dsa_dtype */
+} dsa_kv_cache;
+
+/*
+ * dsa_kv_append - write new keys and values into their cache slots, rotating
+ * the keys (and optionally the queries) to their positions on the way.
+ *
+ *   k, v         [n][cache->heads][dim], token and head strides in elements.
+ *   q            optional queries [n][q_heads][dim] (NULL: keys and values only).
+ *   q_out        rotated queries, same shape, may be q itself; NULL iff q is.
+ *   slots        int64 [n]: slot = page * 64 + offset; < 0 = padding (nothing is
+ *                cached; its query is still rotated); >= num_pages * 64 is skipped
+ *                and flagged DSA_STATUS_BAD_SLOT.  Equal slots race.
+ *   positions    int64 [n], row of the angle table of each token.  A position
+ *                outside [0, max_pos) is clamped and, unless the token is padding,
+ *                flagged DSA_STATUS_BAD_GEOMETRY.
+ *   cos_sin      FP32 [max_pos][cs_stride >= rot_dim]: row p holds rot_dim / 2
+ *                cosines, then rot_dim / 2 sines.
+ *   rot_dim      columns that turn, 0 (no rotation: positions and cos_sin unused) or
+ *                a multiple of 16 up to dim; the other columns are copied.
+ *   interleaved  0: column i pairs with i + rot_dim / 2; 1: column 2i with 2i + 1.
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin): FP32 products, one FP32
+ * add, then rounded once to the cache's type.  Pointers of k, v, q, q_out 16-byte
+ * aligned, their strides multiples of 8; cos_sin 16-byte aligned, cs_stride a
+ * multiple of 4.  dim a multiple of 16 up to 512.
+ */
+int dsa_kv_append(const dsa_kv_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                  const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                  const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                  void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int64_t n,
+                  const int64_t* slots, const int64_t* positions, const float* cos_sin, int64_t cs_stride,
+                  int64_t max_pos, int64_t rot_dim, int interleaved, int32_t* status, void* stream);
+
+/*
+ * dsa_attend_workspace_size - bytes of scratch dsa_attend_paged (k = 0) or
+ * dsa_attend_selected (k = list length) needs for these sizes; 0 for sizes the
+ * calls refuse.  Zero-fill the workspace before its first use; every completed
+ * call leaves it ready for the next, of any sizes that fit.
+ */
+size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
+                                 int64_t max_query_len, int64_t k);
+
+/*
+ * dsa_attend_paged - attention of grouped decode rows over the paged cache.
+ *
+ * Row r of request j attends to the shared prefix, key positions 0 .. prefix_len - 1
+ * in the pages prefix_pages[0 .. ceil(prefix_len / 64) - 1], and to its own keys,
+ * positions t < row_ends[r] in the pages block_table[j]:
+ *   out[r][h] = sum_t softmax_t(scale * q[r][h] . k_t) v_t,
+ * query head h reading key/value head h / (heads / kv_heads).  The prefix's keys
+ * are read once for the rows of the whole batch.
+ *
+ *   q             [rows][heads][dim] of the cache's type (strides in elements).
+ *   heads         a multiple of cache->heads, at most 128 per key/value head.
+ *   block_table, bt_stride, max_pages, starts, row_ends, num_requests, rows
+ *                 as dsa_score_paged.  Rows outside every request see no keys.
+ *   max_query_len largest row count of a request (>= 0; a hint that sizes the
+ *                 tiles, any value gives the same results; the one the workspace
+ *                 was sized with).
+ *   scale         > 0 and finite.
+ *   out           [rows][heads][dim] of the cache's type; a row that sees no key
+ *                 gets zeros.
+ *   lse           optional FP32 [rows][heads]: log(sum_t exp(scale * q . k_t)),
+ *                 -inf for a row that sees no key.
+ *   workspace     dsa_attend_workspace_size(...) bytes, 256-byte aligned.
+ * Keys a row may not see do not reach its output, whatever their bits (the cache
+ * past a request's end may hold NaN).  A page outside the pool is not read
+ * (DSA_STATUS_BAD_PAGE; rows that see it are unspecified).  Products accumulate in
+ * FP32; the softmax weights are rounded to the cache's type before they meet the
+ * values.  dim a multiple of 16 up to 128, else DSA_ERR_UNSUPPORTED.
+ */
+int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                     int64_t heads, const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                     const int32_t* starts, const int32_t* row_ends, int64_t num_requests, int64_t rows,
+                     int64_t max_query_len, const int32_t* prefix_pages, int64_t prefix_len, float scale, void* out,
+                     int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                     size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * dsa_attend_selected - attention of decode rows over the keys the indexer chose.
+ *
+ * As dsa_attend_paged without a prefix, but row r sees only the key positions
+ * topk[r][0 .. k - 1] of its request (dsa_score_paged's or dsa_topk_merge's
+ * output): negative entries are empty and may sit anywhere; an entry at or past
+ * row_ends[r] (or the block table's end) is skipped and flagged
+ * DSA_STATUS_BAD_GEOMETRY; a position listed twice counts twice.
+ *   topk          int32 [rows][topk_stride >= k].
+ */
+int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                        int64_t heads, const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                        const int32_t* starts, const int32_t* row_ends, int64_t num_requests, int64_t rows,
+                        const int32_t* topk, int64_t topk_stride, int64_t k, float scale, void* out,
+                        int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t* status, void* stream);
+
 /*
  * dsa_set_score_timing - profiling hook: when both events are non-NULL,
  * dsa_score_paged records `before` just ahead of its scoring kernel and

@@ -8,8 +8,12 @@ device memory and streams.
 from . import dsa  # noqa: F401
 from .dsa import (  # noqa: F401
     FORMATS,
+    attend_paged,
+    attend_selected,
+    attend_workspace_size,
     decode_layout,
     insert_key,
+    kv_append,
     quantize_queries_rg,
     quantize_query,
     score_paged,

@@ -58,7 +58,27 @@ _SIGS = {
     "dsa_timing_elapsed_ms": (_c.c_int, [_P, _P, _c.POINTER(_c.c_float)]),
     "dsa_version": (_c.c_char_p, []),
     "dsa_probe_mma": (_c.c_int, [_c.c_int, _I64, _P, _P]),
+    "dsa_kv_append": (_c.c_int, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P,
+                                 _P, _P, _I64, _I64, _I64, _c.c_int, _P, _P]),
+    "dsa_attend_workspace_size": (_c.c_size_t, [_I64] * 7),
+    "dsa_attend_paged": (_c.c_int, [_P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64,
+                                    _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
+    "dsa_attend_selected": (_c.c_int, [_P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I64,
+                                       _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
 }
+
+
+class KvCache(_c.Structure):
+    """``dsa_kv_cache``: the two pools with their strides in elements."""
+
+    _fields_ = [("k", _P), ("v", _P),
+                ("k_page_stride", _I64), ("k_token_stride", _I64), ("k_head_stride", _I64),
+                ("v_page_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64),
+                ("num_pages", _I64), ("heads", _I64), ("dim", _I64), ("dtype", _c.c_int32)]
+
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+PAGE_TOKENS = 64
 
 
 def lib():
@@ -398,6 +418,145 @@ def topk(logits: torch.Tensor, row_ends: torch.Tensor, k: int, width: Optional[i
                         _ptr(workspace), workspace.numel(), _stream(logits.device))
     _check(rc, "dsa_topk")
     return out
+
+
+def _kv_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> KvCache:
+    shape = k_cache.shape
+    if k_cache.dtype not in DTYPES or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be BF16 or both FP16")
+    if len(shape) != 4 or shape[1] != PAGE_TOKENS or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [pages, 64, heads, dim]")
+    kp, kt, kh, kc = k_cache.stride()
+    vp, vt, vh, vc = v_cache.stride()
+    if kc != 1 or vc != 1:
+        raise ValueError("cache columns must be contiguous")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), kp, kt, kh, vp, vt, vh, shape[0], shape[2], shape[3],
+                   DTYPES[k_cache.dtype])
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+              status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Writes keys and values [n, heads, dim] into the slots (int64 [n]; < 0 is
+    padding) of the paged caches [pages, 64, heads, dim].  With ``cos_sin``
+    (FP32 [positions, rot]: cosines, then sines) keys and the optional queries
+    [n, q_heads, dim] are rotated to ``positions`` (int64 [n]) on the way.
+    Returns the rotated queries (``q_out``, which may be ``q``), or None."""
+    c = _kv_cache(k_cache, v_cache)
+    n = k.shape[0]
+    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype or k.dim() != 3 or k.shape != v.shape \
+            or k.shape[1] != c.heads or k.shape[2] != c.dim or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must be [n, heads, dim] of the cache's type with contiguous columns")
+    if slots.dtype != torch.int64 or slots.shape != (n,) or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int64 [n], one per key")
+    rot = max_pos = cs_stride = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or (cos_sin.shape[1] and cos_sin.stride(1) != 1):
+            raise ValueError("cos_sin must be FP32 [positions, rot] with contiguous rows")
+        if positions is None or positions.dtype != torch.int64 or positions.shape != (n,) \
+                or not positions.is_contiguous():
+            raise ValueError("positions must be contiguous int64 [n]")
+        (max_pos, rot), cs_stride = cos_sin.shape, cos_sin.stride(0)
+    qs = os_ = (0, 0, 0)
+    heads = 0
+    if q is not None:
+        if q.dtype != k_cache.dtype or q.dim() != 3 or q.shape[0] != n or q.shape[2] != c.dim or q.stride(2) != 1:
+            raise ValueError("q must be [n, q_heads, dim] of the cache's type with contiguous columns")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.dtype != q.dtype or q_out.shape != q.shape or q_out.stride(2) != 1:
+            raise ValueError("q_out must match q")
+        heads, qs, os_ = q.shape[1], q.stride(), q_out.stride()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    ks, vs = k.stride(), v.stride()
+    rc = lib().dsa_kv_append(_c.addressof(c), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _ptr(q), qs[0],
+                             qs[1], heads, _ptr(q_out), os_[0], os_[1], n, slots.data_ptr(), _ptr(positions),
+                             _ptr(cos_sin), cs_stride, max_pos, rot, int(interleaved), _ptr(status),
+                             _stream(k_cache.device))
+    _check(rc, "dsa_kv_append")
+    return q_out
+
+
+def attend_workspace_size(rows: int, num_requests: int, heads: int, kv_heads: int, dim: int, max_query_len: int,
+                          k: int = 0) -> int:
+    """Bytes of scratch of ``attend_paged`` (k = 0) or ``attend_selected``."""
+    return int(lib().dsa_attend_workspace_size(rows, num_requests, heads, kv_heads, dim, max_query_len, k))
+
+
+def _attend_args(q, k_cache, v_cache, block_table, starts, row_ends, scale, out, want_lse):
+    c = _kv_cache(k_cache, v_cache)
+    if q.dtype != k_cache.dtype or q.dim() != 3 or q.shape[2] != c.dim or q.stride(2) != 1:
+        raise ValueError("q must be [rows, heads, dim] of the cache's type with contiguous columns")
+    if block_table.dtype != torch.int32 or starts.dtype != torch.int32 or row_ends.dtype != torch.int32:
+        raise ValueError("block_table, starts and row_ends must be int32")
+    if block_table.dim() != 2 or (block_table.numel() and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [requests, pages] with contiguous rows")
+    rows, requests = q.shape[0], starts.numel() - 1
+    if starts.dim() != 1 or block_table.shape[0] != requests or not starts.is_contiguous():
+        raise ValueError("starts must be contiguous, one entry per request and one more")
+    if row_ends.shape != (rows,) or not row_ends.is_contiguous():
+        raise ValueError("row_ends must hold one bound per query row")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or out.stride(2) != 1:
+        raise ValueError("out must match q")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
+    return c, rows, requests, float(c.dim ** -0.5 if scale is None else scale), out, lse
+
+
+def attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                 starts: torch.Tensor, row_ends: torch.Tensor, max_query_len: int,
+                 prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0, scale: Optional[float] = None,
+                 out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Attention of decode rows [rows, heads, dim] over the paged caches
+    [pages, 64, kv_heads, dim]: row r sees the ``prefix_len`` keys in
+    ``prefix_pages`` (int32), shared by the batch, and keys t < row_ends[r] of
+    its request.  scale defaults to dim ** -0.5.  Returns (out, lse FP32
+    [rows, heads] or None)."""
+    c, rows, requests, scale, out, lse = _attend_args(q, k_cache, v_cache, block_table, starts, row_ends, scale, out,
+                                                      want_lse)
+    if prefix_len and (prefix_pages is None or prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous()
+                       or prefix_pages.numel() * PAGE_TOKENS < prefix_len):
+        raise ValueError("prefix_pages must be contiguous int32 and hold prefix_len keys")
+    heads = q.shape[1]
+    if workspace is None:
+        workspace = new_workspace(attend_workspace_size(rows, requests, heads, c.heads, c.dim, max_query_len),
+                                  q.device)
+    qs, os_ = q.stride(), out.stride()
+    rc = lib().dsa_attend_paged(_c.addressof(c), q.data_ptr(), qs[0], qs[1], heads, block_table.data_ptr(),
+                                block_table.stride(0), block_table.shape[1], starts.data_ptr(), row_ends.data_ptr(),
+                                requests, rows, int(max_query_len), _ptr(prefix_pages), int(prefix_len), scale,
+                                out.data_ptr(), os_[0], os_[1], _ptr(lse), workspace.data_ptr(), workspace.numel(),
+                                _ptr(status), _stream(q.device))
+    _check(rc, "dsa_attend_paged")
+    return out, lse
+
+
+def attend_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    starts: torch.Tensor, row_ends: torch.Tensor, topk: torch.Tensor, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                    workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Attention of decode rows over the key positions of ``topk`` (int32
+    [rows, k], the indexer's selection; negative entries are empty).  Other
+    arguments and results as ``attend_paged``."""
+    c, rows, requests, scale, out, lse = _attend_args(q, k_cache, v_cache, block_table, starts, row_ends, scale, out,
+                                                      want_lse)
+    if topk.dtype != torch.int32 or topk.dim() != 2 or topk.shape[0] != rows or (topk.numel() and topk.stride(1) != 1):
+        raise ValueError("topk must be int32 [rows, k] with contiguous rows")
+    heads, k = q.shape[1], topk.shape[1]
+    if workspace is None:
+        workspace = new_workspace(attend_workspace_size(rows, requests, heads, c.heads, c.dim, 1, k), q.device)
+    qs, os_ = q.stride(), out.stride()
+    rc = lib().dsa_attend_selected(_c.addressof(c), q.data_ptr(), qs[0], qs[1], heads, block_table.data_ptr(),
+                                   block_table.stride(0), block_table.shape[1], starts.data_ptr(),
+                                   row_ends.data_ptr(), requests, rows, topk.data_ptr(), topk.stride(0), k, scale,
+                                   out.data_ptr(), os_[0], os_[1], _ptr(lse), workspace.data_ptr(),
+                                   workspace.numel(), _ptr(status), _stream(q.device))
+    _check(rc, "dsa_attend_selected")
+    return out, lse
 
 
 class TimingEvent:
