@@ -1,9 +1,13 @@
 // dsa_attend_paged and dsa_attend_selected: decode attention over the paged
-// key/value cache.
+// key/value cache, on the tensor cores.
 //
-// First form: one CTA per (row, query head), one pass over the row's keys with
-// the running maximum and sum of the softmax.  Each warp takes every fourth
-// key (four columns a lane), and the four partial results are joined at the end.
+//   o = sum_t softmax_t(c q . k_t) v_t over the keys a row sees, in one pass:
+//   per tile of 128 keys S = Q K^T, p = 2^(s c' - m), l += sum p, O += P V with a
+//   running reference m of the row; pieces of a row's keys taken by different
+//   CTAs are joined by their (m, l, O).
+//
+// Launches: a plan (segments of rows that share keys, tiles of all segments on
+// one axis), the attention kernel over equal shares of that axis, and the join.
 #include <math.h>
 
 #include "elem16.cuh"
@@ -13,123 +17,1020 @@ namespace dsa {
 
 int check_kv_cache(const dsa_kv_cache* c);
 
-struct AttendArgs {
-    dsa_kv_cache c;
-    const uint16_t* q;
-    int64_t qr, qh;
-    const int32_t* bt;
-    int64_t bt_stride, max_pages;
-    const int32_t* starts;
-    const int32_t* row_ends;
-    int R, rows, heads, group;
-    const int32_t* prefix_pages;
-    int64_t prefix_len;
-    const int32_t* topk;
-    int64_t topk_stride, k;
-    float scale;
-    uint16_t* out;
-    int64_t orow, oh;
-    float* lse;
-    int32_t* status;
+constexpr int kTile = 128;          // keys per tile: two pages, or 128 listed keys
+constexpr int kMaxCtas = 192;       // workspace and tables are sized for at most this many CTAs
+constexpr int kMaxWorkers = 2 * kMaxCtas;
+constexpr int kAttThreads = 384;    // 2 producer warps, 2 MMA warps, 2 x 4 softmax warps
+constexpr int kMaxStages = 12;
+constexpr int kPieces = 8;          // piece records in flight per slot
+constexpr int kPlanThreads = 512;
+constexpr int kListThreads = 256;
+constexpr int kPrefixSmem = 2048;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The reference m of a row is raised when a tile's maximum passes it by more
+// than this many powers of two; until then weights up to 2^8 are kept as they
+// are, and O and l need no rescaling.
+constexpr float kSlack = 8.0f;
+
+// A run of a segment's tiles of one key/value head, taken by one worker.
+struct Piece {
+    int row0, nrows;      // query rows
+    int kvh, req;         // key/value head; request, -1 for the shared prefix
+    int keys, minb;       // largest and smallest key bound of the rows
+    int tile0, ntiles;
+    int slot;             // where its partial result goes
+    int direct;           // no other piece sees these rows: write the output itself
+    int poison;           // a value that some of the rows must not see is not finite
+    int pad;
 };
 
-template <typename T, bool kSelected>
-__global__ void __launch_bounds__(128) attend_simple_kernel(const AttendArgs a) {
-    const int row = blockIdx.x, head = blockIdx.y, kvh = head / a.group;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ int s_req;
-    __shared__ float sm[4], sl[4], so[4][128];
+// Workspace regions, 256-byte aligned.
+struct AttLayout {
+    size_t ticket;    // int: zero on entry, zero again on return
+    size_t info;      // int64[2]: tiles on the axis, segments
+    size_t seg;       // int4[S]: first row, rows, request, largest bound
+    size_t minb;      // int[S]: smallest bound
+    size_t prefix;    // int64[S + 1]: tiles of all key heads before the segment
+    size_t worker;    // int[kMaxWorkers]: segment of the worker's first tile
+    size_t row_seg;   // int[rows]: the row's segment, -1 outside every request
+    size_t ends;      // int[rows]: validated bounds
+    size_t list;      // int[rows][kpad]: slots of the selected keys, packed
+    size_t po, pml;   // float[pieces][rows_cap][dim], float2[pieces][rows_cap]: partial results
+    size_t xo, xml;   // the same of the prefix's row-tile pairs (2 x 128 rows a piece)
+    size_t total;
+    int64_t max_segs, kpad, rows_cap;
+};
+
+struct AttParams {
+    int64_t* info;
+    int* ticket;
+    int4* seg;
+    int* minb;
+    int64_t* prefix;
+    int* worker;
+    int* row_seg;
+    int* ends;
+    int* list;
+    float* po;
+    float2* pml;
+    float* xo;
+    float2* xml;
+    const int32_t* bt;
+    int64_t bt_stride;
+    const int32_t* starts;
+    const int32_t* row_ends;
+    const int32_t* prefix_pages;
+    const int32_t* topk;
+    int64_t topk_stride;
+    const uint16_t* v;
+    int64_t vp, vt, vh;                    // value strides (elements), for the rare plain reads
+    uint16_t* out;
+    int64_t orow, ohead;
+    float* lse;
+    int32_t* status;
+    int R, rows, heads, group, kv_heads, dim, max_keys, num_pages;
+    int k, kpad;
+    int prefix_len;                        // shared keys; prefix_mode says who computes them
+    int prefix_mode;                       // 0 none, 1 a segment of the axis, 2 the paired kernel
+    int rps, rows_cap;                     // query rows per segment, tile rows (group * rps)
+    int q_half, nqb, nst;                  // Q bytes per 64 columns, Q buffers and ring stages per slot
+    int max_segs, workers;                 // workers: 2 per CTA of the axis' kernel
+    int x_rps, x_pairs, x_workers;         // paired kernel: query rows per row tile, row-tile pairs, workers
+    int kpu, ktu, khu, vpu, vtu, vhu;      // gather: row numbers per page, token, head
+    int k_none, v_none;                    // gather: a row outside the map
+    float scale_log2;
+};
+
+// ----------------------------------------------------------------- the axis
+// Worker w of W takes tiles [w T / W, (w + 1) T / W).
+__host__ __device__ __forceinline__ int64_t share_start(int64_t w, int64_t T, int64_t W) { return w * T / W; }
+__device__ __forceinline__ int worker_of(int64_t t, int64_t T, int64_t W) {
+    return static_cast<int>(((t + 1) * W - 1) / T);
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+
+// Inclusive scan of one int64 per thread; total in *total (shared).
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* warp_tmp, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += o;
+    }
+    if (lane == 31) warp_tmp[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = lane < nwarps ? warp_tmp[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+            if (lane >= d) s += o;
+        }
+        warp_tmp[lane] = s;
+        if (lane == 31) *total = s;
+    }
+    __syncthreads();
+    if (warp > 0) v += warp_tmp[warp - 1];
+    __syncthreads();
+    return v;
+}
+
+// Tile prefix of S segments and every worker's first segment (whole block).
+__device__ void finish_plan(const AttParams& p, int S) {
+    __shared__ int64_t tmp[32], total;
+    __shared__ int64_t sp[kPrefixSmem + 1];
+    int64_t carry = 0;
+    for (int base = 0; base < S; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        const int64_t n = i < S ? static_cast<int64_t>(tiles_of(__ldcg(&p.seg[i].w))) * p.kv_heads : 0;
+        const int64_t before = carry + block_scan64(n, tmp, &total) - n;
+        if (i < S) {
+            p.prefix[i] = before;
+            if (i < kPrefixSmem) sp[i] = before;
+        }
+        carry += total;
+        __syncthreads();
+    }
+    const int64_t T = carry;
+    if (threadIdx.x == 0) {
+        p.prefix[S] = T;
+        p.info[0] = T;
+        p.info[1] = S;
+    }
+    __syncthreads();
+    const int64_t W = p.workers < T ? p.workers : T;
+    for (int w = threadIdx.x; w < W; w += blockDim.x) {
+        const int64_t t = share_start(w, T, W);
+        int lo = 0, hi = S - 1;   // the last segment that starts at or before t and has tiles
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            const int64_t b = mid < kPrefixSmem ? sp[mid] : p.prefix[mid];
+            if (b <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        p.worker[w] = lo;
+    }
+}
+
+__device__ __forceinline__ int checked_bound(int e, int max_keys, bool& bad) {
+    if (e < 0 || e > max_keys) bad = true;
+    return min(max(e, 0), max_keys);
+}
+
+// Segments of the dense call: up to rps rows of one request each, behind the
+// prefix's one where the axis carries it.  One CTA.
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ int64_t tmp[32], total;
+    for (int r = threadIdx.x; r < p.rows; r += blockDim.x) {
+        p.row_seg[r] = -1;
+        p.ends[r] = 0;
+    }
+    int carry = 0;
+    if (p.prefix_mode == 1) {
+        if (threadIdx.x == 0) {
+            p.seg[0] = make_int4(0, p.rows, -1, p.prefix_len);
+            p.minb[0] = p.prefix_len;
+        }
+        carry = 1;
+    }
+    __syncthreads();
+    bool bad = false;
+    for (int base = 0; base < p.R; base += blockDim.x) {
+        const int q = base + threadIdx.x;
+        int s0 = 0, s1 = 0;
+        if (q < p.R) {
+            const int a = p.starts[q], b = p.starts[q + 1];
+            if (a < 0 || b < a || b > p.rows) bad = true;
+            s0 = min(max(a, 0), p.rows);
+            s1 = min(max(b, s0), p.rows);
+        }
+        const int nseg = (s1 - s0 + p.rps - 1) / p.rps;
+        const int at = carry + static_cast<int>(block_scan64(nseg, tmp, &total)) - nseg;
+        for (int i = 0; i < nseg; ++i) {
+            if (at + i >= p.max_segs) {   // overlapping requests
+                bad = true;
+                break;
+            }
+            const int row0 = s0 + i * p.rps, nr = min(p.rps, s1 - row0);
+            int most = 0, least = 0x7FFFFFFF;
+            for (int r = row0; r < row0 + nr; ++r) {
+                const int e = checked_bound(p.row_ends[r], p.max_keys, bad);
+                p.ends[r] = e;
+                p.row_seg[r] = at + i;
+                most = max(most, e);
+                least = min(least, e);
+            }
+            p.seg[at + i] = make_int4(row0, nr, q, most);
+            p.minb[at + i] = least;
+        }
+        carry += static_cast<int>(total < 0x3FFFFFFF ? total : 0x3FFFFFFF);
+        if (carry > p.max_segs) carry = p.max_segs;
+        __syncthreads();
+    }
+    if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    __threadfence_block();
+    __syncthreads();
+    finish_plan(p, carry);
+}
+
+// Segments of the selected call: one row each.  A CTA packs its row's listed
+// keys into slots (page * 64 + token; -1 for a page outside the pool); the last
+// CTA lays out the axis.
+__global__ void __launch_bounds__(kListThreads) attend_list_kernel(const AttParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ int64_t tmp[32], total;
+    __shared__ int s_req, s_last;
+    const int row = blockIdx.x;
     if (threadIdx.x == 0) s_req = -1;
     __syncthreads();
-    for (int j = threadIdx.x; j < a.R; j += 128) {
-        const int s0 = a.starts[j], s1 = a.starts[j + 1];
-        if ((s0 < 0 || s1 < s0 || s1 > a.rows) && a.status) atomicOr(a.status, DSA_STATUS_BAD_GEOMETRY);
-        if (s0 <= row && row < s1) atomicMax(&s_req, j);
+    bool bad = false, bad_page = false;
+    for (int j = threadIdx.x; j < p.R; j += blockDim.x) {
+        const int a = p.starts[j], b = p.starts[j + 1];
+        if (a < 0 || b < a || b > p.rows) bad = true;
+        if (a <= row && row < b) atomicMax(&s_req, j);
     }
     __syncthreads();
     const int req = s_req;
-    int64_t own = 0;
+    int count = 0;
     if (req >= 0) {
-        own = a.row_ends[row];
-        if (own < 0 || own > a.max_pages * kPage) {
-            if (threadIdx.x == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_GEOMETRY);
-            own = own < 0 ? 0 : a.max_pages * kPage;
-        }
-    }
-    const int dim = static_cast<int>(a.c.dim);
-    const bool on = lane * 4 < dim;
-    float q[4] = {0, 0, 0, 0};
-    if (on) {
-        const uint2 w = *reinterpret_cast<const uint2*>(a.q + row * a.qr + head * a.qh + lane * 4);
-        const float2 x = T::unpack(w.x), y = T::unpack(w.y);
-        q[0] = x.x, q[1] = x.y, q[2] = y.x, q[3] = y.y;
-    }
-    float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
-    const int64_t prefix = !kSelected && req >= 0 ? a.prefix_len : 0;
-    const int64_t total = req < 0 ? 0 : kSelected ? a.k : prefix + own;
-    for (int64_t i = warp; i < total; i += 4) {
-        int page;
-        int64_t t;
-        if (kSelected) {
-            t = a.topk[row * a.topk_stride + i];
-            if (t < 0) continue;
-            if (t >= own) {
-                if (lane == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_GEOMETRY);
-                continue;
+        const int bound = checked_bound(p.row_ends[row], p.max_keys, bad);
+        const int32_t* src = p.topk + row * p.topk_stride;
+        int* dst = p.list + static_cast<int64_t>(row) * p.kpad;
+        for (int base = 0; base < p.k; base += 4 * kListThreads) {
+            int slot[4], n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = base + threadIdx.x * 4 + i;
+                const int t = at < p.k ? src[at] : -1;
+                if (t >= bound) bad = true;
+                const bool on = t >= 0 && t < bound;
+                if (on) {
+                    const int page = p.bt[req * p.bt_stride + t / kPage];
+                    const bool ok = page >= 0 && page < p.num_pages;
+                    bad_page |= !ok;
+                    slot[n++] = ok ? page * kPage + t % kPage : -1;
+                }
             }
-            page = a.bt[req * a.bt_stride + t / kPage];
-        } else if (i < prefix) {
-            t = i;
-            page = a.prefix_pages[t / kPage];
-        } else {
-            t = i - prefix;
-            page = a.bt[req * a.bt_stride + t / kPage];
+            int o = count + static_cast<int>(block_scan64(n, tmp, &total)) - n;
+            for (int i = 0; i < n; ++i) dst[o + i] = slot[i];
+            count += static_cast<int>(total);
         }
-        if (page < 0 || page >= a.c.num_pages) {
-            if (lane == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_PAGE);
-            continue;
-        }
-        const uint16_t* kp = static_cast<const uint16_t*>(a.c.k) + page * a.c.k_page_stride +
-                             (t % kPage) * a.c.k_token_stride + kvh * a.c.k_head_stride;
-        const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + page * a.c.v_page_stride +
-                             (t % kPage) * a.c.v_token_stride + kvh * a.c.v_head_stride;
-        float s = 0.0f, v[4] = {0, 0, 0, 0};
-        if (on) {
-            const uint2 kw = *reinterpret_cast<const uint2*>(kp + lane * 4);
-            const uint2 vw = *reinterpret_cast<const uint2*>(vp + lane * 4);
-            const float2 x = T::unpack(kw.x), y = T::unpack(kw.y), z = T::unpack(vw.x), w = T::unpack(vw.y);
-            s = q[0] * x.x + q[1] * x.y + q[2] * y.x + q[3] * y.y;
-            v[0] = z.x, v[1] = z.y, v[2] = w.x, v[3] = w.y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - mn), p = expf(s - mn);
-        l = l * keep + p;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = o[d] * keep + p * v[d];
-        m = mn;
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) so[warp][lane * 4 + d] = o[d];
+    if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    if (bad_page && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
     __syncthreads();
-    const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < 4; ++w) {
-        const float f = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - top);
-        sum += sl[w] * f;
-        acc += so[w][threadIdx.x] * f;
+    if (threadIdx.x == 0) {
+        p.seg[row] = make_int4(row, 1, req, count);
+        p.minb[row] = count;
+        p.row_seg[row] = req >= 0 ? row : -1;
+        __threadfence();
+        s_last = atomicAdd(p.ticket, 1) == p.rows - 1;
+        if (s_last) *p.ticket = 0;
     }
-    if (threadIdx.x < dim)
-        a.out[row * a.orow + head * a.oh + threadIdx.x] =
-            static_cast<uint16_t>(T::pack(sum == 0.0f ? 0.0f : acc / sum, 0.0f));
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[static_cast<int64_t>(row) * a.heads + head] = sum == 0.0f ? -INFINITY : top + logf(sum);
+    __syncthreads();
+    if (s_last) {
+        __threadfence();
+        finish_plan(p, p.rows);
+    }
 }
 
+// ----------------------------------------------------------------- attention
+struct AttShared {
+    uint64_t full[2][kMaxStages], empty[2][kMaxStages];
+    uint64_t qfull[2][2], qempty[2][2];
+    uint64_t sfull[2], pfull[2], ofull[2], ofree[2], drain[2];
+    Piece piece[2][kPieces];
+    int abort;
+    uint32_t tmem;
+};
+constexpr int kAttMeta = (sizeof(AttShared) + 127) / 128 * 128;
+
+template <int DH>
+__host__ __device__ constexpr int stage_bytes() { return DH * kTile * 128; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Per-type facts: MMA type code, the exponent bits that mark a value that is
+// not finite, and a shift of the weights.  FP16 weights are kept 2^7 larger (at
+// most 2^15 with the slack) so that small ones stay out of the subnormals.
+template <typename T>
+struct Facts;
+template <>
+struct Facts<Bf16> {
+    static constexpr uint32_t mma = 1, expo = 0x7F80u;
+    static constexpr float shift = 0.0f;
+};
+template <>
+struct Facts<Fp16> {
+    static constexpr uint32_t mma = 0, expo = 0x7C00u;
+    static constexpr float shift = 7.0f;
+};
+
+template <typename T>
+__device__ __forceinline__ bool half_wild(uint32_t h) {
+    return (h & Facts<T>::expo) == Facts<T>::expo;
+}
+
+// A whole warp's wait; the warp's answer, so that its lanes stay together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+    const bool ok = mbar_wait(bar, parity, abort, status);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Where a role stands on the axis, and the ring position it is at.
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int nst) {
+        if (++st == nst) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// One CTA runs two slots, each a pipeline of its own: a producer warp (TMA), an
+// MMA warp and four softmax warps with one tile row per thread.  Independent
+// slots take two shares of the axis, each with its own ring of key and value
+// stages; paired slots take two row tiles of one share and read the same ring
+// (the prefix of a large batch: each key tile is loaded once for 256 rows).
+template <typename T, bool kPaired, bool kSelected, int DH>
+__global__ void __launch_bounds__(kAttThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const AttParams p) {
+    extern __shared__ uint8_t dyn[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q_bytes = DH * p.q_half;                                  // one Q buffer
+    uint8_t* const ring0 = smem + 2 * p.nqb * q_bytes;
+    const int rings = kPaired ? 1 : 2;
+    AttShared& sh = *reinterpret_cast<AttShared*>(ring0 + rings * p.nst * stage_bytes<DH>());
+    volatile int* const abort = &sh.abort;
+    const int active = (p.rows_cap + 31) / 32;                          // softmax warps with rows, per slot
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            for (int i = 0; i < p.nst; ++i) {
+                mbar_init(&sh.full[s][i], 1);
+                mbar_init(&sh.empty[s][i], kPaired ? 2 : 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh.qfull[s][i], 1);
+                mbar_init(&sh.qempty[s][i], 1);
+            }
+            mbar_init(&sh.sfull[s], 2);
+            mbar_init(&sh.pfull[s], active);
+            mbar_init(&sh.ofull[s], 2);
+            mbar_init(&sh.ofree[s], active);
+            mbar_init(&sh.drain[s], 1);
+        }
+        sh.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch(&qmap);
+            tma_prefetch(&kmap);
+            tma_prefetch(&vmap);
+        }
+        tc_alloc(&sh.tmem, 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int slot = warp < 4 ? (warp & 1) : (warp >> 2) - 1;
+    const int rs = kPaired ? 0 : slot;                                  // whose ring
+    const int x_tiles = tiles_of(p.prefix_len);
+    const int64_t T_all = kPaired ? static_cast<int64_t>(p.x_pairs) * p.kv_heads * x_tiles : p.info[0];
+    const int64_t W_most = kPaired ? p.x_workers : p.workers;
+    const int64_t W = W_most < T_all ? W_most : T_all;
+    const int worker = kPaired ? blockIdx.x : slot * gridDim.x + blockIdx.x;
+    const bool works = worker < W;
+    const int64_t t0 = works ? share_start(worker, T_all, W) : 0;
+    const int64_t t1 = works ? share_start(worker + 1, T_all, W) : 0;
+    const int rps = kPaired ? p.x_rps : p.rps;
+    uint8_t* const ring = ring0 + rs * p.nst * stage_bytes<DH>();
+
+    if (warp < 2) {
+        // ------------------------------------------------- producer
+        if (kPaired && slot == 1) goto done;
+        Ring at;
+        int64_t issued = 0;
+        int npiece = 0;
+        bool ok = true;
+        int s = works && !kPaired ? p.worker[worker] : 0;
+        int sb = -64;                                                   // first of 32 segments held by the lanes
+        int4 rec = {0, 0, 0, 0};
+        int rec_min = 0;
+        int64_t rec_pre = 0, rec_next = 0;
+        int64_t t = t0;
+        while (t < t1 && ok) {
+            Piece pc;
+            pc.poison = 0;
+            if (kPaired) {
+                const int64_t item = t / x_tiles;
+                const int pairs = p.x_pairs;
+                pc.kvh = static_cast<int>(item / pairs);
+                pc.row0 = static_cast<int>(item % pairs) * 2 * rps;
+                pc.req = -1;
+                pc.keys = pc.minb = p.prefix_len;
+                pc.tile0 = static_cast<int>(t % x_tiles);
+                pc.ntiles = static_cast<int>(min(static_cast<int64_t>(x_tiles - pc.tile0), t1 - t));
+                pc.slot = static_cast<int>(item + worker);
+                pc.direct = 0;
+            } else {
+                int64_t pre, nxt;
+                for (;;) {
+                    if (s < sb || s >= sb + 32) {
+                        sb = s;
+                        const int i = s + lane;
+                        if (i < p.max_segs && i < static_cast<int>(p.info[1])) {
+                            rec = p.seg[i];
+                            rec_min = p.minb[i];
+                            rec_pre = p.prefix[i];
+                            rec_next = p.prefix[i + 1];
+                        } else {
+                            rec_pre = rec_next = T_all;
+                        }
+                    }
+                    pre = __shfl_sync(0xFFFFFFFFu, rec_pre, s - sb);
+                    nxt = __shfl_sync(0xFFFFFFFFu, rec_next, s - sb);
+                    if (nxt > t) break;
+                    ++s;
+                }
+                pc.row0 = __shfl_sync(0xFFFFFFFFu, rec.x, s - sb);
+                pc.nrows = __shfl_sync(0xFFFFFFFFu, rec.y, s - sb);
+                pc.req = __shfl_sync(0xFFFFFFFFu, rec.z, s - sb);
+                pc.keys = __shfl_sync(0xFFFFFFFFu, rec.w, s - sb);
+                pc.minb = __shfl_sync(0xFFFFFFFFu, rec_min, s - sb);
+                const int tph = tiles_of(pc.keys);
+                const int local = static_cast<int>(t - pre);
+                pc.kvh = local / tph;
+                pc.tile0 = local - pc.kvh * tph;
+                pc.ntiles = static_cast<int>(min(static_cast<int64_t>(tph - pc.tile0), t1 - t));
+                pc.slot = s * p.kv_heads + pc.kvh + worker;
+                pc.direct = p.prefix_mode == 0 && pc.ntiles == tph;
+            }
+            // The piece's record; consumers see it through the Q barrier.
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
+                    const int to = kPaired ? x : slot;
+                    Piece w = pc;
+                    if (kPaired) {
+                        w.row0 = pc.row0 + x * rps;
+                        w.nrows = max(0, min(rps, p.rows - w.row0));
+                    }
+                    sh.piece[to][npiece % kPieces] = w;
+                }
+            }
+            const int32_t* pages = pc.req < 0 ? p.prefix_pages : p.bt + pc.req * p.bt_stride;
+            const int npages = (pc.keys + kPage - 1) / kPage;
+            int held = 0, held_next = 0;                                // 32 page ids, one per lane
+            for (int i = 0; i < pc.ntiles && ok; ++i) {
+                const int tile = pc.tile0 + i;
+                int4 krow, vrow;
+                int pg0 = 0, pg1 = 0;
+                if (kSelected) {
+                    const int* list = p.list + static_cast<int64_t>(pc.row0) * p.kpad + tile * kTile + lane * 4;
+                    const int4 e = *reinterpret_cast<const int4*>(list);   // kpad is a multiple of 128
+                    const int left = pc.keys - tile * kTile - lane * 4;
+                    auto kr = [&](int slot_id, int j) {
+                        return j < left && slot_id >= 0
+                                   ? (slot_id >> 6) * p.kpu + (slot_id & 63) * p.ktu + pc.kvh * p.khu
+                                   : p.k_none;
+                    };
+                    auto vr = [&](int slot_id, int j) {
+                        return j < left && slot_id >= 0
+                                   ? (slot_id >> 6) * p.vpu + (slot_id & 63) * p.vtu + pc.kvh * p.vhu
+                                   : p.v_none;
+                    };
+                    krow = make_int4(kr(e.x, 0), kr(e.y, 1), kr(e.z, 2), kr(e.w, 3));
+                    vrow = make_int4(vr(e.x, 0), vr(e.y, 1), vr(e.z, 2), vr(e.w, 3));
+                } else {
+                    auto fetch = [&](int first) {
+                        const int j = first + lane;
+                        int id = p.num_pages;                           // outside the map: zeros
+                        if (j < npages) {
+                            id = pages[j];
+                            if (id < 0 || id >= p.num_pages) {
+                                if (p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
+                                id = p.num_pages;
+                            }
+                        }
+                        return id;
+                    };
+                    if ((i & 15) == 0) {
+                        held = i == 0 ? fetch(2 * tile) : held_next;
+                        held_next = pc.ntiles - i > 16 ? fetch(2 * tile + 32) : 0;
+                    }
+                    pg0 = __shfl_sync(0xFFFFFFFFu, held, 2 * (i & 15));
+                    pg1 = __shfl_sync(0xFFFFFFFFu, held, 2 * (i & 15) + 1);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = warp_wait(&sh.empty[rs][at.st], at.ph ^ 1, abort, p.status);
+                    if (!ok) break;
+                    uint64_t* bar = &sh.full[rs][at.st];
+                    uint8_t* dst = ring + at.st * stage_bytes<DH>();
+                    const CUtensorMap* map = kv ? &vmap : &kmap;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, stage_bytes<DH>());
+                    ++issued;
+                    if (kSelected) {
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < DH; ++h)
+                            tma_gather4(dst + h * kTile * 128 + lane * 512, map, h * 64, kv ? vrow : krow, bar);
+                    } else if (lane == 0) {
+#pragma unroll
+                        for (int h = 0; h < DH; ++h) {
+                            tma_load_4d(dst + h * kTile * 128, map, h * 64, 0, pc.kvh, pg0, bar);
+                            tma_load_4d(dst + h * kTile * 128 + kPage * 128, map, h * 64, 0, pc.kvh, pg1, bar);
+                        }
+                    }
+                    at.next(p.nst);
+                    if (i == 0 && kv == 0) {
+                        // Q of the piece, behind its first key tile: the buffer is free once the products of
+                        // the piece before last (or the last, with one buffer) are done.
+                        const int b = npiece % p.nqb;
+                        const uint32_t ph = (npiece / p.nqb) & 1;
+#pragma unroll
+                        for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
+                            const int to = kPaired ? x : slot;
+                            ok = ok && warp_wait(&sh.qempty[to][b], ph ^ 1, abort, p.status);
+                            if (ok && lane == 0) {
+                                uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
+                                mbar_arrive_expect_tx(&sh.qfull[to][b], DH * 128 * p.group * rps);
+#pragma unroll
+                                for (int h = 0; h < DH; ++h)
+                                    tma_load_3d(qdst + h * p.q_half, &qmap, h * 64, pc.kvh * p.group,
+                                                pc.row0 + (kPaired ? x * rps : 0), &sh.qfull[to][b]);
+                            }
+                        }
+                        ++npiece;
+                        if (!ok) break;
+                    }
+                }
+            }
+            t += pc.ntiles;
+        }
+        // Every stage and Q buffer has been released: no arrival is still on its way when the CTA exits.
+        for (int64_t i = issued > p.nst ? issued - p.nst : 0; i < issued && ok; ++i)
+            ok = warp_wait(&sh.empty[rs][i % p.nst], (i / p.nst) & 1, abort, p.status);
+        for (int x = 0; x < (kPaired ? 2 : 1); ++x)
+            for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece && ok; ++i)
+                ok = warp_wait(&sh.qempty[kPaired ? x : slot][i % p.nqb], (i / p.nqb) & 1, abort, p.status);
+        if (!ok) {
+            // The copies in flight land before the CTA exits.
+            const unsigned long long deadline = globaltimer() + kWaitLimitNs;
+            const int64_t first = issued > p.nst ? issued - p.nst : 0;
+            for (int64_t i = first; i < issued; ++i)
+                if (!mbar_drain(&sh.full[rs][i % p.nst], (i / p.nst) & 1, deadline, p.status)) break;
+            for (int x = 0; x < (kPaired ? 2 : 1); ++x)
+                for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece; ++i)
+                    // (a buffer whose copy was not issued after a failed wait is one phase behind: already past)
+                    if (mbar_test_wait(&sh.qempty[kPaired ? x : slot][i % p.nqb], ((i / p.nqb) & 1) ^ 1))
+                        mbar_drain(&sh.qfull[kPaired ? x : slot][i % p.nqb], (i / p.nqb) & 1, deadline, p.status);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------- MMA issuer
+        const uint32_t id_s = idesc_f16(Facts<T>::mma, 128, kTile, 0);
+        const uint32_t id_o = idesc_f16(Facts<T>::mma, 128, p.dim, 1);
+        const uint32_t d_s = tmem + slot * 128, d_o = tmem + 256 + slot * 128;
+        const int ksteps = p.dim / 16;
+        Ring at;
+        uint32_t ph_p = 0, ph_of = 0;
+        int npiece = 0;
+        bool ok = true, any = false;
+        int64_t t = t0;
+        while (t < t1 && ok) {
+            const int b = npiece % p.nqb;
+            ok = warp_wait(&sh.qfull[slot][b], (npiece / p.nqb) & 1, abort, p.status);
+            if (!ok) break;
+            Piece& pc = sh.piece[slot][npiece % kPieces];
+            const int ntiles = pc.ntiles, tile0 = pc.tile0, keys = pc.keys, minb = pc.minb;
+            const uint32_t qa = smem_u32(smem + (slot * p.nqb + b) * q_bytes);
+            for (int i = 0; i < ntiles; ++i) {
+                ok = warp_wait(&sh.full[rs][at.st], at.ph, abort, p.status);
+                if (!ok) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint32_t ka = smem_u32(ring + at.st * stage_bytes<DH>());
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const int h = DH == 1 ? 0 : kk >> 2, c = kk & 3;
+                        tc_mma_f16(d_s, desc_sw128(qa + h * p.q_half) + 2 * c,
+                                   desc_sw128(ka + h * kTile * 128) + 2 * c, id_s, kk > 0);
+                    }
+                    tc_commit(&sh.sfull[slot]);
+                    mbar_arrive(&sh.sfull[slot]);      // passes the piece's record on
+                    tc_commit(&sh.empty[rs][at.st]);
+                    if (i == ntiles - 1) tc_commit(&sh.qempty[slot][b]);
+                }
+                any = true;
+                at.next(p.nst);
+                ok = warp_wait(&sh.full[rs][at.st], at.ph, abort, p.status);
+                if (!ok) break;
+                uint8_t* va = ring + at.st * stage_bytes<DH>();
+                if (!kSelected) {
+                    // Values no row may see are zeroed (0 x NaN is NaN); values only some rows may see
+                    // are searched for such, which the softmax warps then add by hand.
+                    const int left = keys - (tile0 + i) * kTile;       // keys of this tile
+                    const int all = minb - (tile0 + i) * kTile;        // ... that every row sees
+                    if (left < kTile || all < left) {
+                        const int from = min(max(all, 0), min(left, kTile));
+                        for (int x = lane; x < (kTile - from) * DH * 8; x += 32) {
+                            const int r = from + x / (DH * 8), c = x % (DH * 8);
+                            uint4* at16 = reinterpret_cast<uint4*>(va + (c >> 3) * kTile * 128 + r * 128 + (c & 7) * 16);
+                            if (r >= left) {
+                                *at16 = make_uint4(0, 0, 0, 0);
+                            } else {
+                                uint4 v = *at16;
+                                uint32_t* w = &v.x;
+                                bool wild = false;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if (half_wild<T>(w[j])) w[j] &= 0xFFFF0000u, wild = true;
+                                    if (half_wild<T>(w[j] >> 16)) w[j] &= 0x0000FFFFu, wild = true;
+                                }
+                                if (wild) {
+                                    *at16 = v;
+                                    pc.poison = 1;
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                ok = warp_wait(&sh.pfull[slot], ph_p, abort, p.status);
+                if (!ok) break;
+                ph_p ^= 1;
+                if (i == 0) {   // the accumulator is free once the piece before has been read out
+                    ok = warp_wait(&sh.ofree[slot], ph_of ^ 1, abort, p.status);
+                    if (!ok) break;
+                    ph_of ^= 1;
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t vd = desc_mn_sw128(smem_u32(va), kTile * 128);
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc_mma_f16_ta(d_o, d_s + 8 * kk, vd + 128 * kk, id_o, i > 0 || kk > 0);
+                    tc_commit(&sh.empty[rs][at.st]);
+                    if (i == ntiles - 1) {
+                        tc_commit(&sh.ofull[slot]);
+                        mbar_arrive(&sh.ofull[slot]);   // passes the record's poison mark on
+                    }
+                }
+                at.next(p.nst);
+            }
+            t += ntiles;
+            ++npiece;
+        }
+        if (any && (!ok || *abort) && lane == 0) {
+            // The products in flight end before the CTA exits.
+            tc_commit(&sh.drain[slot]);
+            mbar_drain(&sh.drain[slot], 0, globaltimer() + kWaitLimitNs, p.status);
+        }
+    } else {
+        // ------------------------------------------------- softmax, one row per thread
+        const int quarter = warp & 3;
+        if (quarter >= active) goto done;
+        const int m = quarter * 32 + lane;                              // tile row
+        const int mi = m / p.group, mg = m - mi * p.group;              // query row of the piece, head of the group
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t a_s = tmem + lanes + slot * 128, a_o = tmem + lanes + 256 + slot * 128;
+        const float c = p.scale_log2;
+        uint32_t ph_s = 0, ph_o = 0;
+        int npiece = 0;
+        bool ok = true;
+        int64_t t = t0;
+        while (t < t1 && ok) {
+            float m_ref = -INFINITY, l = 0.0f;
+            int ntiles = 1, tile0 = 0, bound = 0;
+            bool on = false, warp_on = false;
+            const Piece& pc = sh.piece[slot][npiece % kPieces];
+            for (int i = 0; i < ntiles; ++i) {
+                ok = warp_wait(&sh.sfull[slot], ph_s, abort, p.status);
+                if (!ok) break;
+                ph_s ^= 1;
+                tc_fence_after();
+                if (i == 0) {
+                    ntiles = pc.ntiles, tile0 = pc.tile0;
+                    on = mi < pc.nrows && m < p.group * rps;
+                    warp_on = quarter * 32 < pc.nrows * p.group;
+                    bound = pc.keys;
+                    if (on && pc.minb != pc.keys) bound = p.ends[pc.row0 + mi];
+                }
+                if (warp_on) {
+                    uint32_t w[128];
+                    uint32_t(&lo)[64] = *reinterpret_cast<uint32_t(*)[64]>(w);
+                    uint32_t(&hi)[64] = *reinterpret_cast<uint32_t(*)[64]>(w + 64);
+                    tc_ld_32x32b_x64(a_s, lo);
+                    tc_ld_32x32b_x64(a_s + 64, hi);
+                    tc_wait_ld_regs<128>(w);
+                    const int left = bound - (tile0 + i) * kTile;
+                    if (left < kTile) {
+#pragma unroll
+                        for (int j = 0; j < kTile; ++j)
+                            if (j >= left) w[j] = 0xFF800000u;
+                    }
+                    float mx = __uint_as_float(w[0]);
+#pragma unroll
+                    for (int j = 1; j < kTile; ++j) mx = fmaxf(mx, __uint_as_float(w[j]));
+                    mx *= c;
+                    const bool up = mx > m_ref + kSlack;
+                    if (__any_sync(0xFFFFFFFFu, up)) {
+                        const float nm = up ? mx : m_ref;
+                        const float f = up ? ex2(m_ref - nm) : 1.0f;
+                        m_ref = nm;
+                        l *= f;
+                        if (i > 0) {
+                            // every product of this slot so far is done (they precede this tile's scores)
+                            for (int x = 0; x < p.dim; x += 16) {
+                                uint32_t o[16];
+                                tc_ld_32x32b_x16(a_o + x, o);
+                                tc_wait_ld16(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tc_st_32x32b_x16(a_o + x, o);
+                            }
+                        }
+                    }
+                    const float base = m_ref == -INFINITY ? 0.0f : Facts<T>::shift - m_ref;
+                    const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
+                    uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+                    for (int j = 0; j < kTile; j += 2) {
+                        const float2 e = unpack2(fma2(pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), c2, b2));
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        if (j & 2) s1 = add2(s1, pack2(p0, p1));
+                        else s0 = add2(s0, pack2(p0, p1));
+                        w[j / 2] = T::pack(p0, p1);
+                    }
+                    const float2 sum = unpack2(add2(s0, s1));
+                    l += sum.x + sum.y;
+                    tc_st_32x32b_x32(a_s, w);
+                    tc_st_32x32b_x32(a_s + 32, w + 32);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.pfull[slot]);
+            }
+            if (!ok) break;
+            ok = warp_wait(&sh.ofull[slot], ph_o, abort, p.status);
+            if (!ok) break;
+            ph_o ^= 1;
+            tc_fence_after();
+            if (warp_on) {
+                const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
+                const float ref = m_ref == -INFINITY ? -INFINITY : m_ref - Facts<T>::shift;
+                const int row = pc.row0 + mi, head = pc.kvh * p.group + mg;
+                const bool direct = pc.direct;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t* out = p.out + row * p.orow + head * p.ohead;
+                float* part;
+                if (kPaired) {
+                    const int64_t at = (static_cast<int64_t>(pc.slot) * 2 + slot) * 128 + m;
+                    part = p.xo + at * p.dim;
+                    if (on) p.xml[at] = make_float2(ref, l);
+                } else {
+                    const int64_t at = static_cast<int64_t>(pc.slot) * p.rows_cap + m;
+                    part = p.po + at * p.dim;
+                    if (on && !direct) p.pml[at] = make_float2(ref, l);
+                }
+                if (on && direct && p.lse)
+                    p.lse[static_cast<int64_t>(row) * p.heads + head] =
+                        l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                for (int x = 0; x < p.dim; x += 16) {
+                    uint32_t o[16];
+                    tc_ld_32x32b_x16(a_o + x, o);
+                    tc_wait_ld16(o);
+                    if (!kSelected && poison && on) {
+                        // the values that were taken out of the products, for the rows that see them
+                        const int from = max(pc.minb, tile0 * kTile), to = min(bound, (tile0 + ntiles) * kTile);
+                        for (int k = from; k < to; ++k) {
+                            const int page = p.bt[pc.req * p.bt_stride + k / kPage];
+                            if (page < 0 || page >= p.num_pages) continue;
+                            const uint16_t* v = p.v + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (half_wild<T>(v[j]))
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) + T::unpack(v[j]).x);
+                        }
+                    }
+                    if (on && direct) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            h[j] = T::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        *reinterpret_cast<uint4*>(out + x) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+                    } else if (on) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4*>(part + x + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.ofree[slot]);
+            t += ntiles;
+            ++npiece;
+        }
+    }
+done:
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// ----------------------------------------------------------------- join
+// Joins the pieces of a (row, head): kWarps warps take every kWarps-th piece,
+// four columns a lane.
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_kernel(const AttParams p) {
+    constexpr int kItems = kWarps == 1 ? 4 : 1;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + (kWarps == 1 ? warp : 0);
+    if (item >= static_cast<int64_t>(p.rows) * p.heads) return;
+    const int row = static_cast<int>(item / p.heads), head = static_cast<int>(item % p.heads);
+    const int kvh = head / p.group, g = head - kvh * p.group;
+    const int s = p.row_seg[row];
+    // two runs of pieces: the row's own keys and the prefix
+    const float2* ml[2] = {nullptr, nullptr};
+    const float* po[2] = {nullptr, nullptr};
+    int64_t step[2] = {0, 0};   // tile rows from one piece to the next
+    int n[2] = {0, 0};
+    if (s >= 0) {
+        const int64_t T_all = p.info[0];
+        const int64_t W = p.workers < T_all ? p.workers : T_all;
+        for (int x = 0; x < (p.prefix_mode == 1 ? 2 : 1); ++x) {
+            const int sx = x == 0 ? s : 0;
+            const int4 rec = p.seg[sx];
+            const int tph = tiles_of(rec.w);
+            if (tph == 0) continue;
+            const int64_t first = p.prefix[sx] + static_cast<int64_t>(kvh) * tph;
+            const int wa = worker_of(first, T_all, W), wb = worker_of(first + tph - 1, T_all, W);
+            const int64_t at = (static_cast<int64_t>(sx) * p.kv_heads + kvh + wa) * p.rows_cap + (row - rec.x) * p.group + g;
+            ml[x] = p.pml + at;
+            po[x] = p.po + at * p.dim;
+            step[x] = p.rows_cap;
+            n[x] = wb - wa + 1;
+        }
+        if (p.prefix_mode == 0 && n[0] == 1) return;   // written by the attention kernel
+        if (p.prefix_mode == 2) {
+            const int tph = tiles_of(p.prefix_len);
+            const int64_t T_x = static_cast<int64_t>(p.x_pairs) * p.kv_heads * tph;
+            const int64_t W_x = p.x_workers < T_x ? p.x_workers : T_x;
+            const int pair = row / (2 * p.x_rps), in = row - pair * 2 * p.x_rps;
+            const int64_t it = static_cast<int64_t>(kvh) * p.x_pairs + pair;
+            const int wa = worker_of(it * tph, T_x, W_x), wb = worker_of(it * tph + tph - 1, T_x, W_x);
+            const int half = in >= p.x_rps;
+            const int64_t at = ((it + wa) * 2 + half) * 128 + (in - half * p.x_rps) * p.group + g;
+            ml[1] = p.xml + at;
+            po[1] = p.xo + at * p.dim;
+            step[1] = 256;
+            n[1] = wb - wa + 1;
+        }
+    }
+    const bool on = lane * 4 < p.dim;
+    float top = -INFINITY;
+    for (int x = 0; x < 2; ++x)
+        for (int i = lane; i < n[x]; i += 32) top = fmaxf(top, ml[x][i * step[x]].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float l = 0.0f;
+    float4 o = {0, 0, 0, 0};
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll 4
+        for (int i = kWarps == 1 ? 0 : warp; i < n[x]; i += kWarps) {
+            const float2 e = ml[x][i * step[x]];
+            float4 v = {0, 0, 0, 0};
+            if (on) v = *reinterpret_cast<const float4*>(po[x] + i * step[x] * p.dim + lane * 4);
+            const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - top);
+            l += e.y * f;
+            o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+        }
+    }
+    if (kWarps > 1) {
+        __shared__ float sl[kWarps];
+        __shared__ float4 so[kWarps][32];
+        if (lane == 0) sl[warp] = l;
+        so[warp][lane] = o;
+        __syncthreads();
+        if (warp > 0) return;
+        l = 0.0f;
+        o = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 v = so[w][lane];
+            l += sl[w];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (on)
+        *reinterpret_cast<uint2*>(p.out + row * p.orow + head * p.ohead + lane * 4) =
+            make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
+    if (lane == 0 && p.lse)
+        p.lse[item] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// ----------------------------------------------------------------- host
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Query rows per segment: what fits a tile of 128 rows, no more than a request
+// is said to have, but all rows where they fit one tile (a prefix then is one segment).
+static int64_t rows_per_segment(int64_t rows, int64_t group, int64_t max_query_len, int64_t k) {
+    if (k > 0) return 1;
+    const int64_t most = 128 / group;
+    return rows <= most ? (rows > 0 ? rows : 1) : clamp64(max_query_len, 1, most);
+}
+
+static AttLayout attend_layout(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
+                               int64_t max_query_len, int64_t k) {
+    AttLayout L = {};
+    const int64_t group = heads / kv_heads;
+    const int64_t rps = rows_per_segment(rows, group, max_query_len, k);
+    // every request starts a segment of its own; one more for the prefix
+    const int64_t full = rows / rps + num_requests;
+    L.max_segs = k > 0 ? rows : (rows < full ? rows : full) + 1;
+    L.rows_cap = group * rps;
+    L.kpad = (k + kTile - 1) / kTile * kTile;
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
+        return here;
+    };
+    L.ticket = take(256);
+    L.info = take(16);
+    L.seg = take(L.max_segs * 16);
+    L.minb = take(L.max_segs * 4);
+    L.prefix = take((L.max_segs + 1) * 8);
+    L.worker = take(kMaxWorkers * 4);
+    L.row_seg = take(rows * 4);
+    L.ends = take(rows * 4);
+    L.list = take(rows * L.kpad * 4);
+    const int64_t slots = (L.max_segs * kv_heads + kMaxWorkers) * L.rows_cap;
+    L.po = take(slots * dim * 4);
+    L.pml = take(slots * 8);
+    if (k == 0 && rows * group > 128) {
+        const int64_t x_rps = 128 / group, pairs = (rows + 2 * x_rps - 1) / (2 * x_rps);
+        const int64_t xslots = (pairs * kv_heads + kMaxCtas) * 256;
+        L.xo = take(xslots * dim * 4);
+        L.xml = take(xslots * 8);
+    }
+    L.total = at;
+    return L;
+}
+
+static bool sizes_ok(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim) {
+    return rows <= (1 << 24) && num_requests <= (1 << 24) && heads <= 65535 && dim >= 16 && dim <= 128 &&
+           dim % 16 == 0 && heads / kv_heads <= 128;
+}
 
 // The checks both calls share.
 static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -141,10 +1042,10 @@ static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_
     if (rc != DSA_OK) return rc;
     if (heads < 1 || rows < 0 || num_requests < 0 || max_pages < 0) return DSA_ERR_INVALID;
     if (heads % cache->heads) return DSA_ERR_INVALID;
-    if (cache->dim > 128 || heads / cache->heads > 128 || heads > 65535) return DSA_ERR_UNSUPPORTED;
+    if (!sizes_ok(rows, num_requests, heads, cache->heads, cache->dim)) return DSA_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !isfinite(scale)) return DSA_ERR_INVALID;
     if (rows == 0) return DSA_OK;
-    if (rows > (1 << 24) || num_requests > (1 << 30) || max_pages > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
+    if (max_pages > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
     if (!q || !out || !row_ends || !starts || !workspace) return DSA_ERR_INVALID;
     if (max_pages > 0 && num_requests > 0 && (!block_table || bt_stride < max_pages)) return DSA_ERR_INVALID;
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255)) return DSA_ERR_INVALID;
@@ -154,26 +1055,184 @@ static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_
     return DSA_OK;
 }
 
+// TMA strides are positive; a dimension of extent 1 may come with any.
+static bool fix_stride(int64_t& s, int64_t extent, int64_t instead) {
+    if (s > 0) return true;
+    s = instead;
+    return extent <= 1;
+}
+
+static int64_t gcd64(int64_t a, int64_t b) {
+    while (b) {
+        const int64_t t = a % b;
+        a = b;
+        b = t;
+    }
+    return a;
+}
+
+struct AttCall {
+    AttParams p;
+    AttLayout L;
+    CUtensorMap q, k, v;
+    int ctas;
+};
+
+static CUtensorMapDataType map_type(int dtype) {
+    return dtype == DSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+static int query_map(CUtensorMap* map, const dsa_kv_cache* c, const void* q, int64_t row_stride, int64_t head_stride,
+                     int64_t rows, int64_t heads, int64_t box_rows) {
+    if (!fix_stride(head_stride, heads, c->dim) || !fix_stride(row_stride, rows, heads * c->dim))
+        return DSA_ERR_UNSUPPORTED;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->dim), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads / c->heads), static_cast<cuuint32_t>(box_rows)};
+    return encode_tiled(map, map_type(c->dtype), 3, const_cast<void*>(q), dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS
+               ? DSA_OK
+               : DSA_ERR_CUDA;
+}
+
+// The cache the maps describe: a pool without pages (no key can be visible then)
+// gets a page of the workspace that nothing loads.
+static dsa_kv_cache mapped_cache(const dsa_kv_cache* cache, void* workspace) {
+    dsa_kv_cache c = *cache;
+    if (c.num_pages > 0) return c;
+    c.k = c.v = workspace;
+    c.k_head_stride = c.v_head_stride = c.dim;
+    c.k_token_stride = c.v_token_stride = c.dim * c.heads;
+    c.k_page_stride = c.v_page_stride = c.dim * c.heads * kPage;
+    c.num_pages = 1;
+    return c;
+}
+
+// A pool as pages of 64 tokens.
+static int page_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t ps, int64_t ts, int64_t hs) {
+    if (!fix_stride(ps, c->num_pages, c->dim) || !fix_stride(ts, kPage, c->dim) || !fix_stride(hs, c->heads, c->dim))
+        return DSA_ERR_UNSUPPORTED;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->dim), kPage, static_cast<cuuint64_t>(c->heads),
+                                static_cast<cuuint64_t>(c->num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ts) * 2, static_cast<cuuint64_t>(hs) * 2,
+                                   static_cast<cuuint64_t>(ps) * 2};
+    const cuuint32_t box[4] = {64, kPage, 1, 1};
+    return encode_tiled(map, map_type(c->dtype), 4, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+                   CUDA_SUCCESS
+               ? DSA_OK
+               : DSA_ERR_CUDA;
+}
+
+// A pool as rows of dim columns that start every `unit` elements, the unit a
+// common divisor of its strides, so that every (page, token, head) is one row.
+static int row_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t ps, int64_t ts, int64_t hs, int* pu,
+                   int* tu, int* hu, int* none) {
+    if (!fix_stride(ps, c->num_pages, 0) || !fix_stride(ts, kPage, 0) || !fix_stride(hs, c->heads, 0))
+        return DSA_ERR_UNSUPPORTED;
+    int64_t unit = gcd64(gcd64(ps, ts), hs);
+    if (unit == 0) unit = c->dim;
+    const int64_t n = ((c->num_pages - 1) * ps + (kPage - 1) * ts + (c->heads - 1) * hs) / unit + 1;
+    if (n > 0x7FFFFF00) return DSA_ERR_UNSUPPORTED;
+    *pu = static_cast<int>(ps / unit), *tu = static_cast<int>(ts / unit), *hu = static_cast<int>(hs / unit);
+    *none = static_cast<int>(n);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->dim), static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(unit) * 2};
+    const cuuint32_t box[2] = {64, 1};
+    return encode_tiled(map, map_type(c->dtype), 2, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+                   CUDA_SUCCESS
+               ? DSA_OK
+               : DSA_ERR_CUDA;
+}
+
+constexpr int kSmemMost = 232448;   // 227 KB
+
+// Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
+static int fit_shared(int rows, int halves, bool paired, AttParams& p) {
+    p.q_half = (rows * 128 + 1023) / 1024 * 1024;
+    p.nqb = !paired && rows <= 32 ? 2 : 1;
+    const int stage = halves * kTile * 128, fixed = 2 * p.nqb * halves * p.q_half + kAttMeta + 1024;
+    int n = (kSmemMost - fixed) / stage;
+    if (!paired) n /= 2;
+    p.nst = n > kMaxStages ? kMaxStages : n;
+    return fixed + (paired ? 1 : 2) * p.nst * stage;
+}
+
+template <typename T, bool kPaired, bool kSelected, int DH>
+static int launch_attention(const AttCall& a, int grid, int smem, cudaStream_t stream) {
+    auto* kernel = attend_kernel<T, kPaired, kSelected, DH>;
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess)
+            return DSA_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    return launch_pdl(kernel, dim3(grid), dim3(kAttThreads), smem, stream, a.q, a.k, a.v, a.p) == cudaSuccess
+               ? DSA_OK
+               : DSA_ERR_CUDA;
+}
+
+template <bool kPaired, bool kSelected>
+static int launch_attention(const AttCall& a, int dtype, int grid, int smem, cudaStream_t stream) {
+    if (a.p.dim > 64)
+        return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, 2>(a, grid, smem, stream)
+                                 : launch_attention<Fp16, kPaired, kSelected, 2>(a, grid, smem, stream);
+    return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, 1>(a, grid, smem, stream)
+                             : launch_attention<Fp16, kPaired, kSelected, 1>(a, grid, smem, stream);
+}
+
+template <typename T>
+static int launch_join(const AttParams& p, int ctas, cudaStream_t stream) {
+    const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
+    if (items > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
+    // few rows: their many pieces are shared by the warps of a CTA
+    const cudaError_t e = items <= 16 * ctas
+                              ? launch_pdl(attend_join_kernel<T, 8>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
+                                           stream, p)
+                              : launch_pdl(attend_join_kernel<T, 1>, dim3(static_cast<unsigned>((items + 3) / 4)),
+                                           dim3(128), 0, stream, p);
+    return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
+    AttParams& p = a.p;
+    const AttLayout& L = a.L;
+    p.ticket = reinterpret_cast<int*>(ws + L.ticket);
+    p.info = reinterpret_cast<int64_t*>(ws + L.info);
+    p.seg = reinterpret_cast<int4*>(ws + L.seg);
+    p.minb = reinterpret_cast<int*>(ws + L.minb);
+    p.prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
+    p.worker = reinterpret_cast<int*>(ws + L.worker);
+    p.row_seg = reinterpret_cast<int*>(ws + L.row_seg);
+    p.ends = reinterpret_cast<int*>(ws + L.ends);
+    p.list = reinterpret_cast<int*>(ws + L.list);
+    p.po = reinterpret_cast<float*>(ws + L.po);
+    p.pml = reinterpret_cast<float2*>(ws + L.pml);
+    p.xo = reinterpret_cast<float*>(ws + L.xo);
+    p.xml = reinterpret_cast<float2*>(ws + L.xml);
+    p.max_segs = static_cast<int>(L.max_segs);
+    p.rows_cap = static_cast<int>(L.rows_cap);
+    p.kpad = static_cast<int>(L.kpad);
+    p.group = p.heads / p.kv_heads;
+    const int sms = device_sm_count();
+    a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    p.workers = 2 * a.ctas;
+    p.v = static_cast<const uint16_t*>(c->v);
+    p.vp = c->v_page_stride, p.vt = c->v_token_stride, p.vh = c->v_head_stride;
+}
+
 }  // namespace dsa
 
 using namespace dsa;
 
 extern "C" size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads,
                                             int64_t dim, int64_t max_query_len, int64_t k) {
-    if (rows < 0 || num_requests < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 16 || dim % 16 ||
-        dim > 128 || heads / kv_heads > 128 || max_query_len < 0 || k < 0)
+    if (rows < 0 || num_requests < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || max_query_len < 0 || k < 0 ||
+        k > (1 << 24) || !sizes_ok(rows, num_requests, heads, kv_heads, dim))
         return 0;
-    return 256;
-}
-
-template <bool kSelected>
-static int launch_simple(const AttendArgs& a, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>(a.heads));
-    if (a.c.dtype == DSA_BF16)
-        attend_simple_kernel<Bf16, kSelected><<<grid, 128, 0, stream>>>(a);
-    else
-        attend_simple_kernel<Fp16, kSelected><<<grid, 128, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return attend_layout(rows, num_requests, heads, kv_heads, dim, max_query_len, k).total;
 }
 
 extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -181,21 +1240,54 @@ extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_
                                 const int32_t* starts, const int32_t* row_ends, int64_t num_requests, int64_t rows,
                                 int64_t max_query_len, const int32_t* prefix_pages, int64_t prefix_len, float scale,
                                 void* out, int64_t out_row_stride, int64_t out_head_stride, float* lse,
-                                void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
-    const int rc = check_attend(cache, q, q_row_stride, q_head_stride, heads, block_table, bt_stride, max_pages, starts,
-                                row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
+                                void* workspace, size_t workspace_bytes, int32_t* status, void* stream_) {
+    int rc = check_attend(cache, q, q_row_stride, q_head_stride, heads, block_table, bt_stride, max_pages, starts,
+                          row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
     if (rc != DSA_OK) return rc;
-    if (max_query_len < 0 || prefix_len < 0 || (prefix_len > 0 && !prefix_pages)) return DSA_ERR_INVALID;
+    if (max_query_len < 0 || prefix_len < 0 || (prefix_len > 0 && (!prefix_pages || cache->num_pages == 0)))
+        return DSA_ERR_INVALID;
     if (prefix_len > (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
     if (rows == 0) return DSA_OK;
-    if (workspace_bytes <
-        dsa_attend_workspace_size(rows, num_requests, heads, cache->heads, cache->dim, max_query_len, 0))
-        return DSA_ERR_INVALID;
-    const AttendArgs a{*cache, static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, block_table, bt_stride,
-                       max_pages, starts, row_ends, static_cast<int>(num_requests), static_cast<int>(rows),
-                       static_cast<int>(heads), static_cast<int>(heads / cache->heads), prefix_pages, prefix_len,
-                       nullptr, 0, 0, scale, static_cast<uint16_t*>(out), out_row_stride, out_head_stride, lse, status};
-    return launch_simple<false>(a, static_cast<cudaStream_t>(stream));
+    AttCall a = {};
+    a.L = attend_layout(rows, num_requests, heads, cache->heads, cache->dim, max_query_len, 0);
+    if (workspace_bytes < a.L.total) return DSA_ERR_INVALID;
+    AttParams& p = a.p;
+    p.bt = block_table, p.bt_stride = bt_stride, p.starts = starts, p.row_ends = row_ends;
+    p.prefix_pages = prefix_pages;
+    p.out = static_cast<uint16_t*>(out), p.orow = out_row_stride, p.ohead = out_head_stride;
+    p.lse = lse, p.status = status;
+    p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
+    p.kv_heads = static_cast<int>(cache->heads), p.dim = static_cast<int>(cache->dim);
+    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0, p.num_pages = static_cast<int>(cache->num_pages);
+    p.prefix_len = static_cast<int>(prefix_len);
+    p.scale_log2 = scale * kLog2e;
+    fill_params(a, cache, static_cast<uint8_t*>(workspace));
+    p.rps = static_cast<int>(rows_per_segment(rows, p.group, max_query_len, 0));
+    p.prefix_mode = prefix_len == 0 ? 0 : rows * p.group <= 128 ? 1 : 2;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const dsa_kv_cache c = mapped_cache(cache, workspace);
+    rc = page_map(&a.k, &c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride);
+    if (rc == DSA_OK) rc = page_map(&a.v, &c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride);
+    if (rc != DSA_OK) return rc;
+    const int halves = p.dim > 64 ? 2 : 1;
+    if (launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return DSA_ERR_CUDA;
+    if (p.prefix_mode == 2) {
+        AttCall x = a;
+        p.x_rps = 128 / p.group;
+        p.x_pairs = static_cast<int>((rows + 2 * p.x_rps - 1) / (2 * p.x_rps));
+        p.x_workers = a.ctas;
+        x.p = p;
+        x.p.rows_cap = p.group * p.x_rps;
+        const int smem = fit_shared(x.p.rows_cap, halves, true, x.p);
+        rc = query_map(&x.q, cache, q, q_row_stride, q_head_stride, rows, heads, p.x_rps);
+        if (rc == DSA_OK) rc = launch_attention<true, false>(x, cache->dtype, a.ctas, smem, stream);
+        if (rc != DSA_OK) return rc;
+    }
+    const int smem = fit_shared(p.rows_cap, halves, false, p);
+    rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, p.rps);
+    if (rc == DSA_OK) rc = launch_attention<false, false>(a, cache->dtype, a.ctas, smem, stream);
+    if (rc != DSA_OK) return rc;
+    return cache->dtype == DSA_BF16 ? launch_join<Bf16>(p, a.ctas, stream) : launch_join<Fp16>(p, a.ctas, stream);
 }
 
 extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -204,18 +1296,43 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
                                    int64_t num_requests, int64_t rows, const int32_t* topk, int64_t topk_stride,
                                    int64_t k, float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
                                    float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
-                                   void* stream) {
-    const int rc = check_attend(cache, q, q_row_stride, q_head_stride, heads, block_table, bt_stride, max_pages, starts,
-                                row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
+                                   void* stream_) {
+    int rc = check_attend(cache, q, q_row_stride, q_head_stride, heads, block_table, bt_stride, max_pages, starts,
+                          row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
     if (rc != DSA_OK) return rc;
     if (k < 0 || (k > 0 && rows > 0 && (!topk || topk_stride < k))) return DSA_ERR_INVALID;
-    if (k > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
+    if (k > (int64_t(1) << 24) || cache->num_pages > (1 << 25)) return DSA_ERR_UNSUPPORTED;
     if (rows == 0) return DSA_OK;
-    if (workspace_bytes < dsa_attend_workspace_size(rows, num_requests, heads, cache->heads, cache->dim, 1, k))
-        return DSA_ERR_INVALID;
-    const AttendArgs a{*cache, static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, block_table, bt_stride,
-                       max_pages, starts, row_ends, static_cast<int>(num_requests), static_cast<int>(rows),
-                       static_cast<int>(heads), static_cast<int>(heads / cache->heads), nullptr, 0, topk, topk_stride,
-                       k, scale, static_cast<uint16_t*>(out), out_row_stride, out_head_stride, lse, status};
-    return launch_simple<true>(a, static_cast<cudaStream_t>(stream));
+    AttCall a = {};
+    // (an empty list is one key long in the workspace: the rows still need their zeros)
+    a.L = attend_layout(rows, num_requests, heads, cache->heads, cache->dim, 1, k > 0 ? k : 1);
+    if (workspace_bytes < a.L.total) return DSA_ERR_INVALID;
+    AttParams& p = a.p;
+    p.bt = block_table, p.bt_stride = bt_stride, p.starts = starts, p.row_ends = row_ends;
+    p.topk = topk, p.topk_stride = topk_stride, p.k = static_cast<int>(k);
+    p.out = static_cast<uint16_t*>(out), p.orow = out_row_stride, p.ohead = out_head_stride;
+    p.lse = lse, p.status = status;
+    p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
+    p.kv_heads = static_cast<int>(cache->heads), p.dim = static_cast<int>(cache->dim);
+    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0, p.num_pages = static_cast<int>(cache->num_pages);
+    p.scale_log2 = scale * kLog2e;
+    fill_params(a, cache, static_cast<uint8_t*>(workspace));
+    p.rps = 1;
+    rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, 1);
+    const dsa_kv_cache c = mapped_cache(cache, workspace);
+    if (rc == DSA_OK)
+        rc = row_map(&a.k, &c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride, &p.kpu, &p.ktu, &p.khu,
+                     &p.k_none);
+    if (rc == DSA_OK)
+        rc = row_map(&a.v, &c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride, &p.vpu, &p.vtu, &p.vhu,
+                     &p.v_none);
+    if (rc != DSA_OK) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const int smem = fit_shared(p.rows_cap, p.dim > 64 ? 2 : 1, false, p);
+    if (launch_pdl(attend_list_kernel, dim3(static_cast<unsigned>(rows)), dim3(kListThreads), 0, stream, p) !=
+        cudaSuccess)
+        return DSA_ERR_CUDA;
+    rc = launch_attention<false, true>(a, cache->dtype, a.ctas, smem, stream);
+    if (rc != DSA_OK) return rc;
+    return cache->dtype == DSA_BF16 ? launch_join<Bf16>(p, a.ctas, stream) : launch_join<Fp16>(p, a.ctas, stream);
 }

@@ -481,7 +481,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: to
 
 def attend_workspace_size(rows: int, num_requests: int, heads: int, kv_heads: int, dim: int, max_query_len: int,
                           k: int = 0) -> int:
-    """Bytes of scratch of ``attend_paged`` (k = 0) or ``attend_selected``."""
+    """Bytes of scratch of ``attend_paged`` (k = 0) or ``attend_selected`` (k =
+    the list length, 1 for empty lists)."""
     return int(lib().dsa_attend_workspace_size(rows, num_requests, heads, kv_heads, dim, max_query_len, k))
 
 
@@ -548,7 +549,8 @@ def attend_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("topk must be int32 [rows, k] with contiguous rows")
     heads, k = q.shape[1], topk.shape[1]
     if workspace is None:
-        workspace = new_workspace(attend_workspace_size(rows, requests, heads, c.heads, c.dim, 1, k), q.device)
+        workspace = new_workspace(attend_workspace_size(rows, requests, heads, c.heads, c.dim, 1, max(k, 1)),
+                                  q.device)
     qs, os_ = q.stride(), out.stride()
     rc = lib().dsa_attend_selected(_c.addressof(c), q.data_ptr(), qs[0], qs[1], heads, block_table.data_ptr(),
                                    block_table.stride(0), block_table.shape[1], starts.data_ptr(),
