@@ -20,9 +20,9 @@ int check_kv_cache(const dsa_kv_cache* c);
 constexpr int kTile = 128;          // keys per tile: two pages, or 128 listed keys
 constexpr int kMaxCtas = 192;       // workspace and tables are sized for at most this many CTAs
 constexpr int kMaxWorkers = 2 * kMaxCtas;
-constexpr int kAttThreads = 384;    // 2 producer warps, 2 MMA warps, 2 x 4 softmax warps
+constexpr int kAttThreads = 640;    // 2 producer warps, 2 MMA warps, 2 x 8 softmax warps
 constexpr int kMaxStages = 12;
-constexpr int kPieces = 8;          // piece records in flight per slot
+constexpr int kPieces = 4;          // piece records in flight per slot: two with Q buffers, one in use, one being read out
 constexpr int kPlanThreads = 512;
 constexpr int kListThreads = 256;
 constexpr int kPrefixSmem = 2048;
@@ -83,8 +83,9 @@ struct AttParams {
     const int32_t* prefix_pages;
     const int32_t* topk;
     int64_t topk_stride;
-    const uint16_t* v;
-    int64_t vp, vt, vh;                    // value strides (elements), for the rare plain reads
+    const uint16_t* kbase;                 // the pools (element strides), where keys are listed
+    const uint16_t* vbase;                 // and where a value is not finite
+    int64_t kp, kt, kh, vp, vt, vh;
     uint16_t* out;
     int64_t orow, ohead;
     float* lse;
@@ -97,8 +98,6 @@ struct AttParams {
     int q_half, nqb, nst;                  // Q bytes per 64 columns, Q buffers and ring stages per slot
     int max_segs, workers;                 // workers: 2 per CTA of the axis' kernel
     int x_rps, x_pairs, x_workers;         // paired kernel: query rows per row tile, row-tile pairs, workers
-    int kpu, ktu, khu, vpu, vtu, vhu;      // gather: row numbers per page, token, head
-    int k_none, v_none;                    // gather: a row outside the map
     float scale_log2;
 };
 
@@ -106,6 +105,8 @@ struct AttParams {
 // Worker w of W takes tiles [w T / W, (w + 1) T / W).
 __host__ __device__ __forceinline__ int64_t share_start(int64_t w, int64_t T, int64_t W) { return w * T / W; }
 __device__ __forceinline__ int worker_of(int64_t t, int64_t T, int64_t W) {
+    if (T * W < (int64_t(1) << 32))   // (a 64-bit division takes about five times the instructions)
+        return static_cast<int>((static_cast<uint32_t>(t + 1) * static_cast<uint32_t>(W) - 1) / static_cast<uint32_t>(T));
     return static_cast<int>(((t + 1) * W - 1) / T);
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
@@ -303,11 +304,13 @@ struct AttShared {
     uint64_t full[2][kMaxStages], empty[2][kMaxStages];
     uint64_t qfull[2][2], qempty[2][2];
     uint64_t sfull[2], pfull[2], ofull[2], ofree[2], drain[2];
+    float half[2][2][128];            // maxima (then sums) of the two halves of each row
     Piece piece[2][kPieces];
     int abort;
     uint32_t tmem;
 };
 constexpr int kAttMeta = (sizeof(AttShared) + 127) / 128 * 128;
+static_assert(kAttMeta <= 3072, "five stages of 32 KB and two Q tiles leave 3 KB");
 
 template <int DH>
 __host__ __device__ constexpr int stage_bytes() { return DH * kTile * 128; }
@@ -365,6 +368,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// The two warps that share 32 tile rows meet (a warp that gives up arrives
+// once, so that the other does not wait for it).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void pair_leave(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+// The barrier counts this thread once its copies so far are in shared memory.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Where a role stands on the axis, and the ring position it is at.
 struct Ring {
     int st = 0;
@@ -378,7 +390,8 @@ struct Ring {
 };
 
 // One CTA runs two slots, each a pipeline of its own: a producer warp (TMA), an
-// MMA warp and four softmax warps with one tile row per thread.  Independent
+// MMA warp and eight softmax warps; two threads share a tile row, half of the
+// tile's keys each.  Independent
 // slots take two shares of the axis, each with its own ring of key and value
 // stages; paired slots take two row tiles of one share and read the same ring
 // (the prefix of a large batch: each key tile is loaded once for 256 rows).
@@ -386,20 +399,21 @@ template <typename T, bool kPaired, bool kSelected, int DH>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const AttParams p) {
-    extern __shared__ uint8_t dyn[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q_bytes = DH * p.q_half;                                  // one Q buffer
     uint8_t* const ring0 = smem + 2 * p.nqb * q_bytes;
     const int rings = kPaired ? 1 : 2;
     AttShared& sh = *reinterpret_cast<AttShared*>(ring0 + rings * p.nst * stage_bytes<DH>());
     volatile int* const abort = &sh.abort;
-    const int active = (p.rows_cap + 31) / 32;                          // softmax warps with rows, per slot
+    const int active = (p.rows_cap + 31) / 32;                          // 32-row quarters with rows
+    // Listed keys are copied by the producer warp and by the softmax warps without rows.
+    const int copiers = kSelected ? 1 + 2 * (4 - active) : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             for (int i = 0; i < p.nst; ++i) {
-                mbar_init(&sh.full[s][i], 1);
+                mbar_init(&sh.full[s][i], kSelected ? 32 * copiers : 1);
                 mbar_init(&sh.empty[s][i], kPaired ? 2 : 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -407,9 +421,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 mbar_init(&sh.qempty[s][i], 1);
             }
             mbar_init(&sh.sfull[s], 2);
-            mbar_init(&sh.pfull[s], active);
+            mbar_init(&sh.pfull[s], 2 * active);
             mbar_init(&sh.ofull[s], 2);
-            mbar_init(&sh.ofree[s], active);
+            mbar_init(&sh.ofree[s], 2 * active);
             mbar_init(&sh.drain[s], 1);
         }
         sh.abort = 0;
@@ -430,7 +444,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    const int slot = warp < 4 ? (warp & 1) : (warp >> 2) - 1;
+    const int slot = warp < 4 ? (warp & 1) : (warp - 4) >> 3;
+    const int half = ((warp - 4) >> 2) & 1, quarter = warp & 3;         // softmax: keys of the tile, rows (TMEM lanes)
     const int rs = kPaired ? 0 : slot;                                  // whose ring
     const int x_tiles = tiles_of(p.prefix_len);
     const int64_t T_all = kPaired ? static_cast<int64_t>(p.x_pairs) * p.kv_heads * x_tiles : p.info[0];
@@ -443,9 +458,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int rps = kPaired ? p.x_rps : p.rps;
     uint8_t* const ring = ring0 + rs * p.nst * stage_bytes<DH>();
 
-    if (warp < 2) {
+    if (warp < 2 || (kSelected && warp >= 4 && quarter >= active)) {
         // ------------------------------------------------- producer
         if (kPaired && slot == 1) goto done;
+        const int copier = warp < 2 ? 0 : 1 + half * (4 - active) + quarter - active;
         Ring at;
         int64_t issued = 0;
         int npiece = 0;
@@ -503,55 +519,36 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 pc.slot = s * p.kv_heads + pc.kvh + worker;
                 pc.direct = p.prefix_mode == 0 && pc.ntiles == tph;
             }
-            // The piece's record; consumers see it through the Q barrier.
-            if (lane == 0) {
-#pragma unroll
-                for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
-                    const int to = kPaired ? x : slot;
-                    Piece w = pc;
-                    if (kPaired) {
-                        w.row0 = pc.row0 + x * rps;
-                        w.nrows = max(0, min(rps, p.rows - w.row0));
-                    }
-                    sh.piece[to][npiece % kPieces] = w;
-                }
-            }
             const int32_t* pages = pc.req < 0 ? p.prefix_pages : p.bt + pc.req * p.bt_stride;
             const int npages = (pc.keys + kPage - 1) / kPage;
             int held = 0, held_next = 0;                                // 32 page ids, one per lane
+            int ids[4], ids_next[4];                                    // 128 listed slots, lane + 32 j in ids[j]
+            auto listed = [&](int tile, int (&to)[4]) {
+                const int* list = p.list + static_cast<int64_t>(pc.row0) * p.kpad + tile * kTile + lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[j] = tile * kTile + 32 * j + lane < pc.keys ? list[32 * j] : -1;
+            };
+            auto fetch = [&](int first) {
+                const int j = first + lane;
+                int id = p.num_pages;                                   // outside the map: zeros
+                if (j < npages) {
+                    id = pages[j];
+                    if (id < 0 || id >= p.num_pages) {
+                        if (p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
+                        id = p.num_pages;
+                    }
+                }
+                return id;
+            };
+            if (kSelected) listed(pc.tile0, ids_next);
             for (int i = 0; i < pc.ntiles && ok; ++i) {
                 const int tile = pc.tile0 + i;
-                int4 krow, vrow;
                 int pg0 = 0, pg1 = 0;
                 if (kSelected) {
-                    const int* list = p.list + static_cast<int64_t>(pc.row0) * p.kpad + tile * kTile + lane * 4;
-                    const int4 e = *reinterpret_cast<const int4*>(list);   // kpad is a multiple of 128
-                    const int left = pc.keys - tile * kTile - lane * 4;
-                    auto kr = [&](int slot_id, int j) {
-                        return j < left && slot_id >= 0
-                                   ? (slot_id >> 6) * p.kpu + (slot_id & 63) * p.ktu + pc.kvh * p.khu
-                                   : p.k_none;
-                    };
-                    auto vr = [&](int slot_id, int j) {
-                        return j < left && slot_id >= 0
-                                   ? (slot_id >> 6) * p.vpu + (slot_id & 63) * p.vtu + pc.kvh * p.vhu
-                                   : p.v_none;
-                    };
-                    krow = make_int4(kr(e.x, 0), kr(e.y, 1), kr(e.z, 2), kr(e.w, 3));
-                    vrow = make_int4(vr(e.x, 0), vr(e.y, 1), vr(e.z, 2), vr(e.w, 3));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ids[j] = ids_next[j];
+                    if (i + 1 < pc.ntiles) listed(tile + 1, ids_next);
                 } else {
-                    auto fetch = [&](int first) {
-                        const int j = first + lane;
-                        int id = p.num_pages;                           // outside the map: zeros
-                        if (j < npages) {
-                            id = pages[j];
-                            if (id < 0 || id >= p.num_pages) {
-                                if (p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-                                id = p.num_pages;
-                            }
-                        }
-                        return id;
-                    };
                     if ((i & 15) == 0) {
                         held = i == 0 ? fetch(2 * tile) : held_next;
                         held_next = pc.ntiles - i > 16 ? fetch(2 * tile + 32) : 0;
@@ -565,23 +562,36 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (!ok) break;
                     uint64_t* bar = &sh.full[rs][at.st];
                     uint8_t* dst = ring + at.st * stage_bytes<DH>();
-                    const CUtensorMap* map = kv ? &vmap : &kmap;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, stage_bytes<DH>());
-                    ++issued;
                     if (kSelected) {
-                        __syncwarp();
+                        // 16 bytes a lane, several keys at once, swizzled as TMA would place them
+                        constexpr int kLanes = DH * 8, kKeys = 32 / kLanes;   // lanes per key, keys per step
+                        const int sub = lane / kLanes, ch = lane % kLanes;
+                        const uint16_t* src = (kv ? p.vbase + pc.kvh * p.vh : p.kbase + pc.kvh * p.kh) + ch * 8;
+                        const int64_t ps = kv ? p.vp : p.kp, ts = kv ? p.vt : p.kt;
+                        const bool in = ch * 8 < p.dim;
 #pragma unroll
-                        for (int h = 0; h < DH; ++h)
-                            tma_gather4(dst + h * kTile * 128 + lane * 512, map, h * 64, kv ? vrow : krow, bar);
+                        for (int j = 0; j < 4; ++j) {
+                            for (int r0 = copier * kKeys; r0 < 32; r0 += copiers * kKeys) {
+                                const int id = __shfl_sync(0xFFFFFFFFu, ids[j], r0 + sub);
+                                const int r = j * 32 + r0 + sub;
+                                const bool on = in && id >= 0;
+                                cp_async16(dst + (ch >> 3) * kTile * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                                           on ? src + (id >> 6) * ps + (id & 63) * ts : src, on ? 16 : 0);
+                            }
+                        }
+                        cp_async_arrive(bar);
                     } else if (lane == 0) {
+                        const CUtensorMap* map = kv ? &vmap : &kmap;
+                        mbar_arrive_expect_tx(bar, stage_bytes<DH>());
 #pragma unroll
                         for (int h = 0; h < DH; ++h) {
                             tma_load_4d(dst + h * kTile * 128, map, h * 64, 0, pc.kvh, pg0, bar);
                             tma_load_4d(dst + h * kTile * 128 + kPage * 128, map, h * 64, 0, pc.kvh, pg1, bar);
                         }
                     }
+                    ++issued;
                     at.next(p.nst);
-                    if (i == 0 && kv == 0) {
+                    if (i == 0 && kv == 0 && copier == 0) {
                         // Q of the piece, behind its first key tile: the buffer is free once the products of
                         // the piece before last (or the last, with one buffer) are done.
                         const int b = npiece % p.nqb;
@@ -591,6 +601,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             const int to = kPaired ? x : slot;
                             ok = ok && warp_wait(&sh.qempty[to][b], ph ^ 1, abort, p.status);
                             if (ok && lane == 0) {
+                                // The piece's record; its readers see it through this barrier.
+                                Piece w = pc;
+                                if (kPaired) {
+                                    w.row0 = pc.row0 + x * rps;
+                                    w.nrows = max(0, min(rps, p.rows - w.row0));
+                                }
+                                sh.piece[to][npiece % kPieces] = w;
                                 uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
                                 mbar_arrive_expect_tx(&sh.qfull[to][b], DH * 128 * p.group * rps);
 #pragma unroll
@@ -609,14 +626,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         // Every stage and Q buffer has been released: no arrival is still on its way when the CTA exits.
         for (int64_t i = issued > p.nst ? issued - p.nst : 0; i < issued && ok; ++i)
             ok = warp_wait(&sh.empty[rs][i % p.nst], (i / p.nst) & 1, abort, p.status);
+        // (only the warp that loads Q counts pieces)
         for (int x = 0; x < (kPaired ? 2 : 1); ++x)
             for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece && ok; ++i)
                 ok = warp_wait(&sh.qempty[kPaired ? x : slot][i % p.nqb], (i / p.nqb) & 1, abort, p.status);
         if (!ok) {
             // The copies in flight land before the CTA exits.
             const unsigned long long deadline = globaltimer() + kWaitLimitNs;
+            if (kSelected) asm volatile("cp.async.wait_all;" ::: "memory");
             const int64_t first = issued > p.nst ? issued - p.nst : 0;
-            for (int64_t i = first; i < issued; ++i)
+            for (int64_t i = first; i < issued && !kSelected; ++i)
                 if (!mbar_drain(&sh.full[rs][i % p.nst], (i / p.nst) & 1, deadline, p.status)) break;
             for (int x = 0; x < (kPaired ? 2 : 1); ++x)
                 for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece; ++i)
@@ -630,6 +649,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t id_o = idesc_f16(Facts<T>::mma, 128, p.dim, 1);
         const uint32_t d_s = tmem + slot * 128, d_o = tmem + 256 + slot * 128;
         const int ksteps = p.dim / 16;
+        const uint64_t q_next = (p.q_half >> 4) - 8;                    // from columns 48.. to columns 64..
         Ring at;
         uint32_t ph_p = 0, ph_of = 0;
         int npiece = 0;
@@ -646,13 +666,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 ok = warp_wait(&sh.full[rs][at.st], at.ph, abort, p.status);
                 if (!ok) break;
                 if (lane == 0) {
+                    if (kSelected) fence_proxy_async_smem();           // the keys were written by plain copies
                     tc_fence_after();
-                    const uint32_t ka = smem_u32(ring + at.st * stage_bytes<DH>());
-                    for (int kk = 0; kk < ksteps; ++kk) {
-                        const int h = DH == 1 ? 0 : kk >> 2, c = kk & 3;
-                        tc_mma_f16(d_s, desc_sw128(qa + h * p.q_half) + 2 * c,
-                                   desc_sw128(ka + h * kTile * 128) + 2 * c, id_s, kk > 0);
-                    }
+                    const uint64_t qd = desc_sw128(qa);
+                    const uint64_t kd = desc_sw128(smem_u32(ring + at.st * stage_bytes<DH>()));
+#pragma unroll
+                    for (int kk = 0; kk < DH * 4; ++kk)
+                        if (kk < ksteps)
+                            tc_mma_f16(d_s, qd + 2 * kk + (kk >= 4 ? q_next : 0),
+                                       kd + 2 * kk + (kk >= 4 ? (kTile * 128 >> 4) - 8 : 0), id_s, kk > 0);
                     tc_commit(&sh.sfull[slot]);
                     mbar_arrive(&sh.sfull[slot]);      // passes the piece's record on
                     tc_commit(&sh.empty[rs][at.st]);
@@ -703,6 +725,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     ph_of ^= 1;
                 }
                 if (lane == 0) {
+                    if (kSelected) fence_proxy_async_smem();
                     tc_fence_after();
                     const uint64_t vd = desc_mn_sw128(smem_u32(va), kTile * 128);
 #pragma unroll
@@ -725,11 +748,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             mbar_drain(&sh.drain[slot], 0, globaltimer() + kWaitLimitNs, p.status);
         }
     } else {
-        // ------------------------------------------------- softmax, one row per thread
-        const int quarter = warp & 3;
+        // ------------------------------------------------- softmax, half a row per thread
         if (quarter >= active) goto done;
         const int m = quarter * 32 + lane;                              // tile row
         const int mi = m / p.group, mg = m - mi * p.group;              // query row of the piece, head of the group
+        const int pair = 1 + slot * 4 + quarter;                        // named barrier of the row's two warps
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t a_s = tmem + lanes + slot * 128, a_o = tmem + lanes + 256 + slot * 128;
         const float c = p.scale_log2;
@@ -748,29 +771,39 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 ph_s ^= 1;
                 tc_fence_after();
                 if (i == 0) {
+                    // the sums of the piece before, in the maxima's place, have been read
+                    ok = npiece == 0 || warp_wait(&sh.ofree[slot], (npiece - 1) & 1, abort, p.status);
+                    if (!ok) break;
                     ntiles = pc.ntiles, tile0 = pc.tile0;
-                    on = mi < pc.nrows && m < p.group * rps;
+                    on = mi < pc.nrows;
                     warp_on = quarter * 32 < pc.nrows * p.group;
                     bound = pc.keys;
                     if (on && pc.minb != pc.keys) bound = p.ends[pc.row0 + mi];
                 }
                 if (warp_on) {
-                    uint32_t w[128];
-                    uint32_t(&lo)[64] = *reinterpret_cast<uint32_t(*)[64]>(w);
-                    uint32_t(&hi)[64] = *reinterpret_cast<uint32_t(*)[64]>(w + 64);
-                    tc_ld_32x32b_x64(a_s, lo);
-                    tc_ld_32x32b_x64(a_s + 64, hi);
-                    tc_wait_ld_regs<128>(w);
-                    const int left = bound - (tile0 + i) * kTile;
-                    if (left < kTile) {
+                    uint32_t w[64];
+                    tc_ld_32x32b_x64(a_s + half * 64, w);
+                    tc_wait_ld_regs<64>(w);
+                    const int left = bound - (tile0 + i) * kTile - half * 64;
+                    if (left < 64) {
 #pragma unroll
-                        for (int j = 0; j < kTile; ++j)
+                        for (int j = 0; j < 64; ++j)
                             if (j >= left) w[j] = 0xFF800000u;
                     }
-                    float mx = __uint_as_float(w[0]);
+                    float m4[4];
 #pragma unroll
-                    for (int j = 1; j < kTile; ++j) mx = fmaxf(mx, __uint_as_float(w[j]));
-                    mx *= c;
+                    for (int j = 0; j < 4; ++j) m4[j] = fmaxf(__uint_as_float(w[j]), __uint_as_float(w[j + 4]));
+#pragma unroll
+                    for (int j = 8; j < 64; j += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            m4[x] = fmaxf(fmaxf(m4[x], __uint_as_float(w[j + x])), __uint_as_float(w[j + x + 4]));
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    // The other half's maximum; both warps have now read their scores, so the weights
+                    // may take the scores' columns.
+                    sh.half[slot][half][m] = mx;
+                    pair_sync(pair);
+                    mx = fmaxf(mx, sh.half[slot][half ^ 1][m]) * c;
                     const bool up = mx > m_ref + kSlack;
                     if (__any_sync(0xFFFFFFFFu, up)) {
                         const float nm = up ? mx : m_ref;
@@ -779,7 +812,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         l *= f;
                         if (i > 0) {
                             // every product of this slot so far is done (they precede this tile's scores)
-                            for (int x = 0; x < p.dim; x += 16) {
+                            for (int x = half * 16; x < p.dim; x += 32) {
                                 uint32_t o[16];
                                 tc_ld_32x32b_x16(a_o + x, o);
                                 tc_wait_ld16(o);
@@ -793,7 +826,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
                     uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-                    for (int j = 0; j < kTile; j += 2) {
+                    for (int j = 0; j < 64; j += 2) {
                         const float2 e = unpack2(fma2(pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), c2, b2));
                         const float p0 = ex2(e.x), p1 = ex2(e.y);
                         if (j & 2) s1 = add2(s1, pack2(p0, p1));
@@ -802,8 +835,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                     const float2 sum = unpack2(add2(s0, s1));
                     l += sum.x + sum.y;
-                    tc_st_32x32b_x32(a_s, w);
-                    tc_st_32x32b_x32(a_s + 32, w + 32);
+                    tc_st_32x32b_x32(a_s + half * 32, w);
                     tc_wait_st();
                 }
                 tc_fence_before();
@@ -816,6 +848,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             ph_o ^= 1;
             tc_fence_after();
             if (warp_on) {
+                // (the products are done, so both warps are past the last tile's maxima)
+                sh.half[slot][half][m] = l;
+                pair_sync(pair);
+                l = sh.half[slot][0][m] + sh.half[slot][1][m];
                 const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
                 const float ref = m_ref == -INFINITY ? -INFINITY : m_ref - Facts<T>::shift;
                 const int row = pc.row0 + mi, head = pc.kvh * p.group + mg;
@@ -826,16 +862,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (kPaired) {
                     const int64_t at = (static_cast<int64_t>(pc.slot) * 2 + slot) * 128 + m;
                     part = p.xo + at * p.dim;
-                    if (on) p.xml[at] = make_float2(ref, l);
+                    if (on && half == 0) p.xml[at] = make_float2(ref, l);
                 } else {
                     const int64_t at = static_cast<int64_t>(pc.slot) * p.rows_cap + m;
                     part = p.po + at * p.dim;
-                    if (on && !direct) p.pml[at] = make_float2(ref, l);
+                    if (on && !direct && half == 0) p.pml[at] = make_float2(ref, l);
                 }
-                if (on && direct && p.lse)
+                if (on && direct && half == 0 && p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
                         l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
-                for (int x = 0; x < p.dim; x += 16) {
+                for (int x = half * 16; x < p.dim; x += 32) {
                     uint32_t o[16];
                     tc_ld_32x32b_x16(a_o + x, o);
                     tc_wait_ld16(o);
@@ -845,7 +881,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         for (int k = from; k < to; ++k) {
                             const int page = p.bt[pc.req * p.bt_stride + k / kPage];
                             if (page < 0 || page >= p.num_pages) continue;
-                            const uint16_t* v = p.v + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
+                            const uint16_t* v = p.vbase + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 if (half_wild<T>(v[j]))
@@ -872,6 +908,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             t += ntiles;
             ++npiece;
         }
+        if (!ok) pair_leave(pair);
     }
 done:
     tc_fence_before();
@@ -1062,15 +1099,6 @@ static bool fix_stride(int64_t& s, int64_t extent, int64_t instead) {
     return extent <= 1;
 }
 
-static int64_t gcd64(int64_t a, int64_t b) {
-    while (b) {
-        const int64_t t = a % b;
-        a = b;
-        b = t;
-    }
-    return a;
-}
-
 struct AttCall {
     AttParams p;
     AttLayout L;
@@ -1124,34 +1152,13 @@ static int page_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t
                : DSA_ERR_CUDA;
 }
 
-// A pool as rows of dim columns that start every `unit` elements, the unit a
-// common divisor of its strides, so that every (page, token, head) is one row.
-static int row_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t ps, int64_t ts, int64_t hs, int* pu,
-                   int* tu, int* hu, int* none) {
-    if (!fix_stride(ps, c->num_pages, 0) || !fix_stride(ts, kPage, 0) || !fix_stride(hs, c->heads, 0))
-        return DSA_ERR_UNSUPPORTED;
-    int64_t unit = gcd64(gcd64(ps, ts), hs);
-    if (unit == 0) unit = c->dim;
-    const int64_t n = ((c->num_pages - 1) * ps + (kPage - 1) * ts + (c->heads - 1) * hs) / unit + 1;
-    if (n > 0x7FFFFF00) return DSA_ERR_UNSUPPORTED;
-    *pu = static_cast<int>(ps / unit), *tu = static_cast<int>(ts / unit), *hu = static_cast<int>(hs / unit);
-    *none = static_cast<int>(n);
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->dim), static_cast<cuuint64_t>(n)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(unit) * 2};
-    const cuuint32_t box[2] = {64, 1};
-    return encode_tiled(map, map_type(c->dtype), 2, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
-                   CUDA_SUCCESS
-               ? DSA_OK
-               : DSA_ERR_CUDA;
-}
-
 constexpr int kSmemMost = 232448;   // 227 KB
 
 // Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
 static int fit_shared(int rows, int halves, bool paired, AttParams& p) {
     p.q_half = (rows * 128 + 1023) / 1024 * 1024;
     p.nqb = !paired && rows <= 32 ? 2 : 1;
-    const int stage = halves * kTile * 128, fixed = 2 * p.nqb * halves * p.q_half + kAttMeta + 1024;
+    const int stage = halves * kTile * 128, fixed = 2 * p.nqb * halves * p.q_half + kAttMeta;
     int n = (kSmemMost - fixed) / stage;
     if (!paired) n /= 2;
     p.nst = n > kMaxStages ? kMaxStages : n;
@@ -1219,7 +1226,9 @@ static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
     const int sms = device_sm_count();
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.workers = 2 * a.ctas;
-    p.v = static_cast<const uint16_t*>(c->v);
+    p.kbase = static_cast<const uint16_t*>(c->k);
+    p.vbase = static_cast<const uint16_t*>(c->v);
+    p.kp = c->k_page_stride, p.kt = c->k_token_stride, p.kh = c->k_head_stride;
     p.vp = c->v_page_stride, p.vt = c->v_token_stride, p.vh = c->v_head_stride;
 }
 
@@ -1319,13 +1328,7 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
     p.rps = 1;
     rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, 1);
-    const dsa_kv_cache c = mapped_cache(cache, workspace);
-    if (rc == DSA_OK)
-        rc = row_map(&a.k, &c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride, &p.kpu, &p.ktu, &p.khu,
-                     &p.k_none);
-    if (rc == DSA_OK)
-        rc = row_map(&a.v, &c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride, &p.vpu, &p.vtu, &p.vhu,
-                     &p.v_none);
+    a.k = a.v = a.q;   // (keys are copied from the pools, not through maps)
     if (rc != DSA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const int smem = fit_shared(p.rows_cap, p.dim > 64 ? 2 : 1, false, p);
