@@ -368,6 +368,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// One lane of the warp, chosen so that the compiler knows it is one: tensor and
+// copy instructions take their operands from uniform registers, and under a
+// plain lane test each of them is preceded by moves that cost about 100 cycles.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on != 0;
+}
+
 // The two warps that share 32 tile rows meet (a warp that gives up arrives
 // once, so that the other does not wait for it).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
@@ -400,7 +411,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const AttParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a shuffled value is uniform to the compiler, and what follows from it stays in uniform registers)
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int q_bytes = DH * p.q_half;                                  // one Q buffer
     uint8_t* const ring0 = smem + 2 * p.nqb * q_bytes;
     const int rings = kPaired ? 1 : 2;
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -580,7 +592,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             }
                         }
                         cp_async_arrive(bar);
-                    } else if (lane == 0) {
+                    } else if (elect_one()) {
                         const CUtensorMap* map = kv ? &vmap : &kmap;
                         mbar_arrive_expect_tx(bar, stage_bytes<DH>());
 #pragma unroll
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             for (int i = 0; i < ntiles; ++i) {
                 ok = warp_wait(&sh.full[rs][at.st], at.ph, abort, p.status);
                 if (!ok) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     if (kSelected) fence_proxy_async_smem();           // the keys were written by plain copies
                     tc_fence_after();
                     const uint64_t qd = desc_sw128(qa);
@@ -724,7 +736,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (!ok) break;
                     ph_of ^= 1;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     if (kSelected) fence_proxy_async_smem();
                     tc_fence_after();
                     const uint64_t vd = desc_mn_sw128(smem_u32(va), kTile * 128);
@@ -742,7 +754,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             t += ntiles;
             ++npiece;
         }
-        if (any && (!ok || *abort) && lane == 0) {
+        if (any && !ok && elect_one()) {
             // The products in flight end before the CTA exits.
             tc_commit(&sh.drain[slot]);
             mbar_drain(&sh.drain[slot], 0, globaltimer() + kWaitLimitNs, p.status);
