@@ -6,8 +6,12 @@
 //   running reference m of the row; pieces of a row's keys taken by different
 //   CTAs are joined by their (m, l, O).
 //
-// Launches: a plan (segments of rows that share keys, tiles of all segments on
-// one axis), the attention kernel over equal shares of that axis, and the join.
+// The keys of all (segment, key head) items lie on one axis of 128-key tiles: a
+// segment is a run of rows that share keys (rows of one request, or all rows
+// behind the prefix, or one row's listed keys).  Every worker (a pipeline slot of
+// a CTA) takes an equal share of the axis, so one long context and many short
+// ones fill the GPU alike; an item that several workers share is joined by a
+// last, small kernel.
 #include <math.h>
 
 #include "elem16.cuh"
@@ -20,12 +24,13 @@ int check_kv_cache(const dsa_kv_cache* c);
 constexpr int kTile = 128;          // keys per tile: two pages, or 128 listed keys
 constexpr int kMaxCtas = 192;       // workspace and tables are sized for at most this many CTAs
 constexpr int kMaxWorkers = 2 * kMaxCtas;
-constexpr int kAttThreads = 640;    // 2 producer warps, 2 MMA warps, 2 x 8 softmax warps
 constexpr int kMaxStages = 12;
 constexpr int kPieces = 4;          // piece records in flight per slot: two with Q buffers, one in use, one being read out
 constexpr int kPlanThreads = 512;
 constexpr int kListThreads = 256;
 constexpr int kPrefixSmem = 2048;
+constexpr int kPlanSegs = 128;      // up to this many segments every CTA lays out the axis itself
+constexpr int kPlanRows = 4096;     // ... and up to this many rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The reference m of a row is raised when a tile's maximum passes it by more
@@ -45,32 +50,41 @@ struct Piece {
     int pad;
 };
 
+// Where the join finds a row's own pieces.
+struct RowInfo {
+    int64_t first;        // first tile of the segment on the axis
+    int seg, row0, tph;   // segment (own ones count from 0; -1 outside every request), its first row, tiles per head
+    int pad;
+};
+
+// The axis: tile prefix (all key heads), {first row, rows, request or -1, largest
+// bound} and smallest bound of every segment, in shared or global memory.
+struct Axis {
+    int64_t* prefix;
+    int4* seg;
+    int* minb;
+};
+
 // Workspace regions, 256-byte aligned.
 struct AttLayout {
-    size_t ticket;    // int: zero on entry, zero again on return
     size_t info;      // int64[2]: tiles on the axis, segments
-    size_t seg;       // int4[S]: first row, rows, request, largest bound
-    size_t minb;      // int[S]: smallest bound
-    size_t prefix;    // int64[S + 1]: tiles of all key heads before the segment
+    size_t seg, minb, prefix;   // the axis in global memory (S = max_segs)
     size_t worker;    // int[kMaxWorkers]: segment of the worker's first tile
-    size_t row_seg;   // int[rows]: the row's segment, -1 outside every request
-    size_t ends;      // int[rows]: validated bounds
+    size_t row_info;  // RowInfo[rows]
+    size_t count;     // int[rows]: listed keys of each row
     size_t list;      // int[rows][kpad]: slots of the selected keys, packed
-    size_t po, pml;   // float[pieces][rows_cap][dim], float2[pieces][rows_cap]: partial results
-    size_t xo, xml;   // the same of the prefix's row-tile pairs (2 x 128 rows a piece)
+    size_t po, pml;   // float[pieces][own_cap][dim], float2[pieces][own_cap]: partial results
+    size_t xo, xml;   // the same of the prefix's pieces
     size_t total;
-    int64_t max_segs, kpad, rows_cap;
+    int64_t max_segs, kpad, own_rps;
 };
 
 struct AttParams {
     int64_t* info;
-    int* ticket;
-    int4* seg;
-    int* minb;
-    int64_t* prefix;
+    Axis axis;
     int* worker;
-    int* row_seg;
-    int* ends;
+    RowInfo* row_info;
+    int* count;
     int* list;
     float* po;
     float2* pml;
@@ -93,11 +107,14 @@ struct AttParams {
     int R, rows, heads, group, kv_heads, dim, max_keys, num_pages;
     int k, kpad;
     int prefix_len;                        // shared keys; prefix_mode says who computes them
-    int prefix_mode;                       // 0 none, 1 a segment of the axis, 2 the paired kernel
-    int rps, rows_cap;                     // query rows per segment, tile rows (group * rps)
+    int prefix_mode;                       // 0 none, 1 segments of the axis, 2 the paired kernel
+    int px_segs;                           // mode 1: the prefix's segments, first on the axis
+    int rps, rows_cap;                     // query rows and tile rows (group * rps) of a tile
+    int own_rps, own_cap;                  // the same of a request's segments
     int q_half, nqb, nst;                  // Q bytes per 64 columns, Q buffers and ring stages per slot
     int max_segs, workers;                 // workers: 2 per CTA of the axis' kernel
-    int x_rps, x_pairs, x_workers;         // paired kernel: query rows per row tile, row-tile pairs, workers
+    int plan_in_cta;                       // every CTA lays out the axis, no plan kernel
+    int x_rps, x_pairs, x_workers, x_cap;  // prefix: query rows per row tile, pairs of them, paired workers, tile rows
     float scale_log2;
 };
 
@@ -137,115 +154,149 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* warp_tmp, in
     return v;
 }
 
-// Tile prefix of S segments and every worker's first segment (whole block).
-__device__ void finish_plan(const AttParams& p, int S) {
-    __shared__ int64_t tmp[32], total;
-    __shared__ int64_t sp[kPrefixSmem + 1];
-    int64_t carry = 0;
-    for (int base = 0; base < S; base += blockDim.x) {
-        const int i = base + threadIdx.x;
-        const int64_t n = i < S ? static_cast<int64_t>(tiles_of(__ldcg(&p.seg[i].w))) * p.kv_heads : 0;
-        const int64_t before = carry + block_scan64(n, tmp, &total) - n;
-        if (i < S) {
-            p.prefix[i] = before;
-            if (i < kPrefixSmem) sp[i] = before;
+// Lays out the axis (whole block).  `tmp`: 33 int64 of shared scratch; `bounds`:
+// shared scratch of one int per row, or null.  One block also writes what the
+// join reads (`write`).  Returns the tiles; *segs: the segments.
+template <bool kSelected>
+__device__ int64_t lay_out(const AttParams& p, const Axis& ax, int64_t* tmp, int* bounds, bool write, int* segs) {
+    int64_t* total = tmp + 32;
+    const int nt = blockDim.x;
+    bool bad = false;
+    int S;
+    if (kSelected) {
+        S = p.rows;
+        for (int r = threadIdx.x; r < S; r += nt) {
+            const int n = p.count[r];
+            ax.seg[r] = make_int4(r, 1, 0, n);
+            ax.minb[r] = n;
         }
-        carry += total;
+    } else {
+        if (bounds)
+            for (int r = threadIdx.x; r < p.rows; r += nt) bounds[r] = p.row_ends[r];
+        if (write)
+            for (int r = threadIdx.x; r < p.rows; r += nt) p.row_info[r] = RowInfo{0, -1, 0, 0, 0};
+        for (int i = threadIdx.x; i < p.px_segs; i += nt) {
+            ax.seg[i] = make_int4(i * p.x_rps, min(p.x_rps, p.rows - i * p.x_rps), -1, p.prefix_len);
+            ax.minb[i] = p.prefix_len;
+        }
+        int carry = p.px_segs;
         __syncthreads();
-    }
-    const int64_t T = carry;
-    if (threadIdx.x == 0) {
-        p.prefix[S] = T;
-        p.info[0] = T;
-        p.info[1] = S;
+        for (int base = 0; base < p.R; base += nt) {
+            const int q = base + threadIdx.x;
+            int s0 = 0, s1 = 0;
+            if (q < p.R) {
+                const int a = p.starts[q], b = p.starts[q + 1];
+                if (a < 0 || b < a || b > p.rows) bad = true;
+                s0 = min(max(a, 0), p.rows);
+                s1 = min(max(b, s0), p.rows);
+            }
+            const int nseg = (s1 - s0 + p.own_rps - 1) / p.own_rps;
+            const int at = carry + static_cast<int>(block_scan64(nseg, tmp, total)) - nseg;
+            for (int i = 0; i < nseg; ++i) {
+                if (at + i >= p.max_segs) {   // overlapping requests
+                    bad = true;
+                    break;
+                }
+                const int row0 = s0 + i * p.own_rps, nr = min(p.own_rps, s1 - row0);
+                int most = 0, least = 0x7FFFFFFF;
+                for (int r = row0; r < row0 + nr; ++r) {
+                    const int given = bounds ? bounds[r] : p.row_ends[r];
+                    const int e = min(max(given, 0), p.max_keys);
+                    if (e != given) bad = true;
+                    most = max(most, e);
+                    least = min(least, e);
+                }
+                ax.seg[at + i] = make_int4(row0, nr, q, most);
+                ax.minb[at + i] = least;
+            }
+            carry = static_cast<int>(min(carry + *total, static_cast<int64_t>(p.max_segs)));
+            __syncthreads();
+        }
+        S = carry;
     }
     __syncthreads();
-    const int64_t W = p.workers < T ? p.workers : T;
-    for (int w = threadIdx.x; w < W; w += blockDim.x) {
-        const int64_t t = share_start(w, T, W);
-        int lo = 0, hi = S - 1;   // the last segment that starts at or before t and has tiles
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            const int64_t b = mid < kPrefixSmem ? sp[mid] : p.prefix[mid];
-            if (b <= t) lo = mid;
-            else hi = mid - 1;
+    int64_t carry = 0;
+    for (int base = 0; base < S; base += nt) {
+        const int i = base + threadIdx.x;
+        const int4 rec = i < S ? ax.seg[i] : make_int4(0, 0, 0, 0);
+        const int tph = tiles_of(rec.w);
+        const int64_t n = static_cast<int64_t>(tph) * p.kv_heads;
+        const int64_t before = carry + block_scan64(n, tmp, total) - n;
+        if (i < S) {
+            ax.prefix[i] = before;
+            if (write && i >= p.px_segs)
+                for (int r = rec.x; r < rec.x + rec.y; ++r)
+                    p.row_info[r] = RowInfo{before, i - p.px_segs, rec.x, tph, 0};
         }
-        p.worker[w] = lo;
+        carry += *total;
+        __syncthreads();
     }
+    if (threadIdx.x == 0) {
+        ax.prefix[S] = carry;
+        if (write) {
+            p.info[0] = carry;
+            p.info[1] = S;
+        }
+    }
+    if (write && bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    __syncthreads();
+    *segs = S;
+    return carry;
 }
 
-__device__ __forceinline__ int checked_bound(int e, int max_keys, bool& bad) {
-    if (e < 0 || e > max_keys) bad = true;
-    return min(max(e, 0), max_keys);
+// The segment with tile t: the last that starts at or before it (segments
+// without tiles come before the next one's start, so the last is not empty).
+__device__ __forceinline__ int segment_of(const int64_t* prefix, int S, int64_t t) {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
 }
 
-// Segments of the dense call: up to rps rows of one request each, behind the
-// prefix's one where the axis carries it.  One CTA.
+// The axis in global memory, for calls of many segments.  One CTA.
+template <bool kSelected>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ int64_t tmp[32], total;
-    for (int r = threadIdx.x; r < p.rows; r += blockDim.x) {
-        p.row_seg[r] = -1;
-        p.ends[r] = 0;
-    }
-    int carry = 0;
-    if (p.prefix_mode == 1) {
-        if (threadIdx.x == 0) {
-            p.seg[0] = make_int4(0, p.rows, -1, p.prefix_len);
-            p.minb[0] = p.prefix_len;
-        }
-        carry = 1;
-    }
+    __shared__ int64_t tmp[33];
+    __shared__ int64_t sp[kPrefixSmem];
+    __shared__ int bounds[kPlanRows];
+    int S;
+    const int64_t T =
+        lay_out<kSelected>(p, p.axis, tmp, p.rows <= kPlanRows ? bounds : nullptr, true, &S);
+    const bool fits = S <= kPrefixSmem;
+    if (fits)
+        for (int i = threadIdx.x; i < S; i += blockDim.x) sp[i] = p.axis.prefix[i];
     __syncthreads();
-    bool bad = false;
-    for (int base = 0; base < p.R; base += blockDim.x) {
-        const int q = base + threadIdx.x;
-        int s0 = 0, s1 = 0;
-        if (q < p.R) {
-            const int a = p.starts[q], b = p.starts[q + 1];
-            if (a < 0 || b < a || b > p.rows) bad = true;
-            s0 = min(max(a, 0), p.rows);
-            s1 = min(max(b, s0), p.rows);
-        }
-        const int nseg = (s1 - s0 + p.rps - 1) / p.rps;
-        const int at = carry + static_cast<int>(block_scan64(nseg, tmp, &total)) - nseg;
-        for (int i = 0; i < nseg; ++i) {
-            if (at + i >= p.max_segs) {   // overlapping requests
-                bad = true;
-                break;
-            }
-            const int row0 = s0 + i * p.rps, nr = min(p.rps, s1 - row0);
-            int most = 0, least = 0x7FFFFFFF;
-            for (int r = row0; r < row0 + nr; ++r) {
-                const int e = checked_bound(p.row_ends[r], p.max_keys, bad);
-                p.ends[r] = e;
-                p.row_seg[r] = at + i;
-                most = max(most, e);
-                least = min(least, e);
-            }
-            p.seg[at + i] = make_int4(row0, nr, q, most);
-            p.minb[at + i] = least;
-        }
-        carry += static_cast<int>(total < 0x3FFFFFFF ? total : 0x3FFFFFFF);
-        if (carry > p.max_segs) carry = p.max_segs;
-        __syncthreads();
-    }
-    if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
-    __threadfence_block();
-    __syncthreads();
-    finish_plan(p, carry);
+    const int64_t W = p.workers < T ? p.workers : T;
+    for (int w = threadIdx.x; w < W; w += blockDim.x)
+        p.worker[w] = segment_of(fits ? sp : p.axis.prefix, S, share_start(w, T, W));
 }
 
-// Segments of the selected call: one row each.  A CTA packs its row's listed
-// keys into slots (page * 64 + token; -1 for a page outside the pool); the last
-// CTA lays out the axis.
+// Packs each row's listed keys into slots (page * 64 + token; -1 for a page
+// outside the pool) and counts them.  One CTA a row.
 __global__ void __launch_bounds__(kListThreads) attend_list_kernel(const AttParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ int64_t tmp[32], total;
-    __shared__ int s_req, s_last;
+    __shared__ int64_t tmp[33];
+    __shared__ int s_req;
     const int row = blockIdx.x;
+    // (the first entries and the bound are on their way while the row's request is looked up)
+    const int32_t* src = p.topk + row * p.topk_stride;
+    int* dst = p.list + static_cast<int64_t>(row) * p.kpad;
+    int next[4];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = base + threadIdx.x * 4 + i;
+            next[i] = at < p.k ? src[at] : -1;
+        }
+    };
+    load(0);
+    const int e = p.row_ends[row];
     if (threadIdx.x == 0) s_req = -1;
     __syncthreads();
     bool bad = false, bad_page = false;
@@ -258,45 +309,33 @@ __global__ void __launch_bounds__(kListThreads) attend_list_kernel(const AttPara
     const int req = s_req;
     int count = 0;
     if (req >= 0) {
-        const int bound = checked_bound(p.row_ends[row], p.max_keys, bad);
-        const int32_t* src = p.topk + row * p.topk_stride;
-        int* dst = p.list + static_cast<int64_t>(row) * p.kpad;
+        if (e < 0 || e > p.max_keys) bad = true;
+        const int bound = min(max(e, 0), p.max_keys);
+        const int32_t* pages = p.bt + req * p.bt_stride;
         for (int base = 0; base < p.k; base += 4 * kListThreads) {
             int slot[4], n = 0;
+            int page[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) page[i] = next[i] >= 0 && next[i] < bound ? pages[next[i] / kPage] : -1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = base + threadIdx.x * 4 + i;
-                const int t = at < p.k ? src[at] : -1;
+                const int t = next[i];
                 if (t >= bound) bad = true;
-                const bool on = t >= 0 && t < bound;
-                if (on) {
-                    const int page = p.bt[req * p.bt_stride + t / kPage];
-                    const bool ok = page >= 0 && page < p.num_pages;
+                if (t >= 0 && t < bound) {
+                    const bool ok = page[i] >= 0 && page[i] < p.num_pages;
                     bad_page |= !ok;
-                    slot[n++] = ok ? page * kPage + t % kPage : -1;
+                    slot[n++] = ok ? page[i] * kPage + t % kPage : -1;
                 }
             }
-            int o = count + static_cast<int>(block_scan64(n, tmp, &total)) - n;
+            if (base + 4 * kListThreads < p.k) load(base + 4 * kListThreads);
+            const int o = count + static_cast<int>(block_scan64(n, tmp, tmp + 32)) - n;
             for (int i = 0; i < n; ++i) dst[o + i] = slot[i];
-            count += static_cast<int>(total);
+            count += static_cast<int>(tmp[32]);
         }
     }
+    if (threadIdx.x == 0) p.count[row] = count;
     if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
     if (bad_page && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        p.seg[row] = make_int4(row, 1, req, count);
-        p.minb[row] = count;
-        p.row_seg[row] = req >= 0 ? row : -1;
-        __threadfence();
-        s_last = atomicAdd(p.ticket, 1) == p.rows - 1;
-        if (s_last) *p.ticket = 0;
-    }
-    __syncthreads();
-    if (s_last) {
-        __threadfence();
-        finish_plan(p, p.rows);
-    }
 }
 
 // ----------------------------------------------------------------- attention
@@ -304,7 +343,8 @@ struct AttShared {
     uint64_t full[2][kMaxStages], empty[2][kMaxStages];
     uint64_t qfull[2][2], qempty[2][2];
     uint64_t sfull[2], pfull[2], ofull[2], ofree[2], drain[2];
-    float half[2][2][128];            // maxima (then sums) of the two halves of each row
+    float half[2][2][128];            // maxima (then sums) of the two halves of each row; narrow: {m, l} of the strips
+    uint64_t merge[2];                // narrow: the strips of a piece meet
     Piece piece[2][kPieces];
     int abort;
     uint32_t tmem;
@@ -400,14 +440,52 @@ struct Ring {
     }
 };
 
+// The values that were taken out of the products because some rows must not see
+// them, added to a row that does: columns x .. x + 15.
+template <typename T>
+__device__ __noinline__ void add_wild(const AttParams& p, const Piece& pc, int bound, int x, uint32_t (&o)[16]) {
+    const int from = max(pc.minb, pc.tile0 * kTile), to = min(bound, (pc.tile0 + pc.ntiles) * kTile);
+    for (int k = from; k < to; ++k) {
+        const int page = p.bt[pc.req * p.bt_stride + k / kPage];
+        if (page < 0 || page >= p.num_pages) continue;
+        const uint16_t* v = p.vbase + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (half_wild<T>(v[j])) o[j] = __float_as_uint(__uint_as_float(o[j]) + T::unpack(v[j]).x);
+    }
+}
+
+// Room for the axis of a call of few segments.
+struct AxisShared {
+    int64_t prefix[kPlanSegs + 1];
+    int4 seg[kPlanSegs];
+    int minb[kPlanSegs];
+};
+
+// Threads of a CTA: 2 producer warps and 2 MMA warps, then softmax warps: 8 a
+// slot, or 4 where tiles are narrow (and 4 more a slot that copy listed keys).
+template <bool kSelected, bool kNarrow>
+__host__ __device__ constexpr int att_threads() { return kNarrow && !kSelected ? 384 : 640; }
+constexpr int kMergeCols = 16;
+constexpr int kMergeBytes = 4 * 32 * kMergeCols * 4;   // narrow: one slot's buffer
+
 // One CTA runs two slots, each a pipeline of its own: a producer warp (TMA), an
-// MMA warp and eight softmax warps; two threads share a tile row, half of the
-// tile's keys each.  Independent
+// MMA warp and softmax warps, a thread per tile row (the lanes of tensor memory).
+//
+// Wide tiles (up to 128 rows): two threads share a row, half of the tile's keys
+// each, and agree on its reference.  Narrow tiles (up to 32 rows, the usual
+// decode): the rows are laid four times into the 128 tile rows, one copy to each
+// warp of the slot; copy j weighs only keys 32j .. 32j + 31 of a tile (its other
+// weights are zero) and keeps its own reference, so the softmax of a tile, which
+// every product waits for, is a quarter as long and no warp waits for another;
+// the four partial outputs are added at the end of the piece.
+//
+// Independent
 // slots take two shares of the axis, each with its own ring of key and value
 // stages; paired slots take two row tiles of one share and read the same ring
 // (the prefix of a large batch: each key tile is loaded once for 256 rows).
-template <typename T, bool kPaired, bool kSelected, int DH>
-__global__ void __launch_bounds__(kAttThreads, 1)
+template <typename T, bool kPaired, bool kSelected, bool kNarrow, int DH>
+__global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const AttParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -416,11 +494,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int q_bytes = DH * p.q_half;                                  // one Q buffer
     uint8_t* const ring0 = smem + 2 * p.nqb * q_bytes;
     const int rings = kPaired ? 1 : 2;
-    AttShared& sh = *reinterpret_cast<AttShared*>(ring0 + rings * p.nst * stage_bytes<DH>());
+    uint8_t* const merge_buf = ring0 + rings * p.nst * stage_bytes<DH>();
+    AttShared& sh = *reinterpret_cast<AttShared*>(merge_buf + (kNarrow ? 2 * kMergeBytes : 0));
+    AxisShared& axis_sh = *reinterpret_cast<AxisShared*>(reinterpret_cast<uint8_t*>(&sh) + kAttMeta);
     volatile int* const abort = &sh.abort;
-    const int active = (p.rows_cap + 31) / 32;                          // 32-row quarters with rows
-    // Listed keys are copied by the producer warp and by the softmax warps without rows.
-    const int copiers = kSelected ? 1 + 2 * (4 - active) : 1;
+    const int active = kNarrow ? 4 : (p.rows_cap + 31) / 32;            // 32-row quarters with rows
+    const int softmax_warps = kNarrow ? 4 : 2 * active;                 // per slot
+    // Listed keys are copied by the producer warp and by the warps that have no rows.
+    const int copiers = !kSelected ? 1 : kNarrow ? 5 : 1 + 2 * (4 - active);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -433,9 +514,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 mbar_init(&sh.qempty[s][i], 1);
             }
             mbar_init(&sh.sfull[s], 2);
-            mbar_init(&sh.pfull[s], 2 * active);
+            mbar_init(&sh.pfull[s], softmax_warps);
             mbar_init(&sh.ofull[s], 2);
-            mbar_init(&sh.ofree[s], 2 * active);
+            mbar_init(&sh.ofree[s], softmax_warps);
+            mbar_init(&sh.merge[s], softmax_warps);
             mbar_init(&sh.drain[s], 1);
         }
         sh.abort = 0;
@@ -456,11 +538,27 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    const int slot = warp < 4 ? (warp & 1) : (warp - 4) >> 3;
-    const int half = ((warp - 4) >> 2) & 1, quarter = warp & 3;         // softmax: keys of the tile, rows (TMEM lanes)
+    const bool copies = kSelected && (kNarrow ? warp >= 12 : warp >= 4 && (warp & 3) >= active);
+    const int slot = warp < 4 ? (warp & 1) : kNarrow ? (warp >> 2) - (warp < 12 ? 1 : 3) : (warp - 4) >> 3;
+    const int half = ((warp - 4) >> 2) & 1, quarter = warp & 3;         // softmax: keys of the tile (wide), tile rows
     const int rs = kPaired ? 0 : slot;                                  // whose ring
     const int x_tiles = tiles_of(p.prefix_len);
-    const int64_t T_all = kPaired ? static_cast<int64_t>(p.x_pairs) * p.kv_heads * x_tiles : p.info[0];
+    int S = 0;
+    int64_t T_all;
+    Axis axis = p.axis;
+    if (kPaired) {
+        T_all = static_cast<int64_t>(p.x_pairs) * p.kv_heads * x_tiles;
+    } else if (p.plan_in_cta) {
+        // (the ring is scratch until the first copy)
+        axis = Axis{axis_sh.prefix, axis_sh.seg, axis_sh.minb};
+        T_all = lay_out<kSelected>(p, axis, reinterpret_cast<int64_t*>(ring0), reinterpret_cast<int*>(ring0 + 512),
+                                   blockIdx.x == 0, &S);
+        fence_proxy_async_smem();
+        __syncthreads();
+    } else {
+        T_all = p.info[0];
+        S = static_cast<int>(p.info[1]);
+    }
     const int64_t W_most = kPaired ? p.x_workers : p.workers;
     const int64_t W = W_most < T_all ? W_most : T_all;
     const int worker = kPaired ? blockIdx.x : slot * gridDim.x + blockIdx.x;
@@ -470,15 +568,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int rps = kPaired ? p.x_rps : p.rps;
     uint8_t* const ring = ring0 + rs * p.nst * stage_bytes<DH>();
 
-    if (warp < 2 || (kSelected && warp >= 4 && quarter >= active)) {
+    if (warp < 2 || copies) {
         // ------------------------------------------------- producer
         if (kPaired && slot == 1) goto done;
-        const int copier = warp < 2 ? 0 : 1 + half * (4 - active) + quarter - active;
+        const int copier = warp < 2 ? 0 : kNarrow ? 1 + quarter : 1 + half * (4 - active) + quarter - active;
         Ring at;
         int64_t issued = 0;
         int npiece = 0;
         bool ok = true;
-        int s = works && !kPaired ? p.worker[worker] : 0;
+        int s = !works || kPaired ? 0 : p.plan_in_cta ? segment_of(axis.prefix, S, t0) : p.worker[worker];
         int sb = -64;                                                   // first of 32 segments held by the lanes
         int4 rec = {0, 0, 0, 0};
         int rec_min = 0;
@@ -504,11 +602,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (s < sb || s >= sb + 32) {
                         sb = s;
                         const int i = s + lane;
-                        if (i < p.max_segs && i < static_cast<int>(p.info[1])) {
-                            rec = p.seg[i];
-                            rec_min = p.minb[i];
-                            rec_pre = p.prefix[i];
-                            rec_next = p.prefix[i + 1];
+                        if (i < S) {
+                            rec = axis.seg[i];
+                            rec_min = axis.minb[i];
+                            rec_pre = axis.prefix[i];
+                            rec_next = axis.prefix[i + 1];
                         } else {
                             rec_pre = rec_next = T_all;
                         }
@@ -528,7 +626,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 pc.kvh = local / tph;
                 pc.tile0 = local - pc.kvh * tph;
                 pc.ntiles = static_cast<int>(min(static_cast<int64_t>(tph - pc.tile0), t1 - t));
-                pc.slot = s * p.kv_heads + pc.kvh + worker;
+                pc.slot = (pc.req < 0 ? s : s - p.px_segs) * p.kv_heads + pc.kvh + worker;
                 pc.direct = p.prefix_mode == 0 && pc.ntiles == tph;
             }
             const int32_t* pages = pc.req < 0 ? p.prefix_pages : p.bt + pc.req * p.bt_stride;
@@ -621,11 +719,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 }
                                 sh.piece[to][npiece % kPieces] = w;
                                 uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
-                                mbar_arrive_expect_tx(&sh.qfull[to][b], DH * 128 * p.group * rps);
+                                constexpr int kCopies = kNarrow ? 4 : 1;
+                                mbar_arrive_expect_tx(&sh.qfull[to][b], kCopies * DH * 128 * p.group * rps);
 #pragma unroll
-                                for (int h = 0; h < DH; ++h)
-                                    tma_load_3d(qdst + h * p.q_half, &qmap, h * 64, pc.kvh * p.group,
-                                                pc.row0 + (kPaired ? x * rps : 0), &sh.qfull[to][b]);
+                                for (int h = 0; h < DH * kCopies; ++h)
+                                    tma_load_3d(qdst + h / kCopies * p.q_half + h % kCopies * 32 * 128, &qmap,
+                                                h / kCopies * 64, pc.kvh * p.group, pc.row0 + (kPaired ? x * rps : 0),
+                                                &sh.qfull[to][b]);
                             }
                         }
                         ++npiece;
@@ -759,8 +859,169 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             tc_commit(&sh.drain[slot]);
             mbar_drain(&sh.drain[slot], 0, globaltimer() + kWaitLimitNs, p.status);
         }
+    } else if (kNarrow) {
+        // ------------------------------------------------- softmax, narrow: 32 keys of a row per thread
+        const int mi = lane / p.group, mg = lane - mi * p.group;        // query row of the piece, head of the group
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t a_s = tmem + lanes + slot * 128, a_o = tmem + lanes + 256 + slot * 128;
+        const float c = p.scale_log2;
+        float2* const ml = reinterpret_cast<float2*>(&sh.half[0][0][0]) + slot * 128;   // [strip][row]
+        float* const buf = reinterpret_cast<float*>(merge_buf + slot * kMergeBytes);    // [strip][column][row]
+        uint32_t ph_s = 0, ph_o = 0, ph_m = 0;
+        int npiece = 0;
+        bool ok = true;
+        auto meet = [&]() {                                             // the slot's four warps, bounded
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.merge[slot]);
+            ok = warp_wait(&sh.merge[slot], ph_m, abort, p.status);
+            ph_m ^= 1;
+            return ok;
+        };
+        int64_t t = t0;
+        while (t < t1 && ok) {
+            float m_ref = -INFINITY, l = 0.0f;
+            int ntiles = 1, tile0 = 0, bound = 0;
+            bool on = false;
+            const Piece& pc = sh.piece[slot][npiece % kPieces];
+            for (int i = 0; i < ntiles; ++i) {
+                ok = warp_wait(&sh.sfull[slot], ph_s, abort, p.status);
+                if (!ok) break;
+                ph_s ^= 1;
+                tc_fence_after();
+                if (i == 0) {
+                    ntiles = pc.ntiles, tile0 = pc.tile0;
+                    on = mi < pc.nrows;
+                    bound = pc.keys;
+                    if (on && pc.minb != pc.keys) bound = min(max(p.row_ends[pc.row0 + mi], 0), p.max_keys);
+                }
+                uint32_t w[32];
+                tc_ld_32x32b_x32(a_s + quarter * 32, w);
+                tc_wait_ld_regs<32>(w);
+                const int left = bound - (tile0 + i) * kTile - quarter * 32;
+                if (left < 32) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j >= left) w[j] = 0xFF800000u;
+                }
+                float m4[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m4[j] = fmaxf(__uint_as_float(w[j]), __uint_as_float(w[j + 4]));
+#pragma unroll
+                for (int j = 8; j < 32; j += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        m4[x] = fmaxf(fmaxf(m4[x], __uint_as_float(w[j + x])), __uint_as_float(w[j + x + 4]));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+                const bool up = mx > m_ref + kSlack;
+                if (__any_sync(0xFFFFFFFFu, up)) {
+                    const float nm = up ? mx : m_ref;
+                    const float f = up ? ex2(m_ref - nm) : 1.0f;
+                    m_ref = nm;
+                    l *= f;
+                    if (i > 0) {
+                        // every product of this slot so far is done (they precede this tile's scores)
+                        for (int x = 0; x < p.dim; x += 16) {
+                            uint32_t o[16];
+                            tc_ld_32x32b_x16(a_o + x, o);
+                            tc_wait_ld16(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tc_st_32x32b_x16(a_o + x, o);
+                        }
+                    }
+                }
+                const float base = m_ref == -INFINITY ? 0.0f : Facts<T>::shift - m_ref;
+                const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
+                uint64_t s0 = 0, s1 = 0;
+                uint32_t h[16];
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 e = unpack2(fma2(pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), c2, b2));
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
+                    if (j & 2) s1 = add2(s1, pack2(p0, p1));
+                    else s0 = add2(s0, pack2(p0, p1));
+                    h[j / 2] = T::pack(p0, p1);
+                }
+                const float2 sum = unpack2(add2(s0, s1));
+                l += sum.x + sum.y;
+                // The weights take the scores' place, in this warp's own lanes: its strip, zeros elsewhere.
+                uint32_t zero[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) zero[j] = 0;
+#pragma unroll
+                for (int x = 1; x < 4; ++x) tc_st_32x32b_x16(a_s + ((quarter + x) & 3) * 16, zero);
+                tc_st_32x32b_x16(a_s + quarter * 16, h);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.pfull[slot]);
+            }
+            if (!ok) break;
+            ok = warp_wait(&sh.ofull[slot], ph_o, abort, p.status);
+            if (!ok) break;
+            ph_o ^= 1;
+            tc_fence_after();
+            // The four strips are joined: each scaled to the common reference, then added.
+            const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
+            const int row = pc.row0 + mi, head = pc.kvh * p.group + mg;
+            const bool direct = pc.direct, own = pc.req >= 0 || kSelected;
+            ml[quarter * 32 + lane] = make_float2(m_ref, l);
+            if (!meet()) break;
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top = fmaxf(top, ml[x * 32 + lane].x);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 e = ml[x * 32 + lane];
+                sum += e.y * (e.x == -INFINITY ? 0.0f : ex2(e.x - top));
+            }
+            const float f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - top);
+            const float ref = top == -INFINITY ? -INFINITY : top - Facts<T>::shift;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint16_t* out = p.out + row * p.orow + head * p.ohead;
+            const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + lane;
+            float* part = (own ? p.po : p.xo) + at * p.dim;
+            if (on && quarter == 0) {
+                if (!direct)
+                    (own ? p.pml : p.xml)[at] = make_float2(ref, sum);
+                else if (p.lse)
+                    p.lse[static_cast<int64_t>(row) * p.heads + head] =
+                        sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+            }
+            for (int x = 0; x < p.dim; x += kMergeCols) {
+                uint32_t o[16];
+                tc_ld_32x32b_x16(a_o + x, o);
+                tc_wait_ld16(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                if (!kSelected && poison && on && quarter == 0) add_wild<T>(p, pc, bound, x, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) buf[(quarter * 16 + j) * 32 + lane] = __uint_as_float(o[j]);
+                if (!meet()) break;
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = 0.0f;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) v[j] += buf[(y * 16 + quarter * 4 + j) * 32 + lane];
+                }
+                const int col = x + quarter * 4;
+                if (on && direct)
+                    *reinterpret_cast<uint2*>(out + col) =
+                        make_uint2(T::pack(v[0] * inv, v[1] * inv), T::pack(v[2] * inv, v[3] * inv));
+                else if (on)
+                    *reinterpret_cast<float4*>(part + col) = make_float4(v[0], v[1], v[2], v[3]);
+                if (!meet()) break;
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.ofree[slot]);
+            t += ntiles;
+            ++npiece;
+        }
     } else {
-        // ------------------------------------------------- softmax, half a row per thread
+        // ------------------------------------------------- softmax, wide: half a row per thread
         if (quarter >= active) goto done;
         const int m = quarter * 32 + lane;                              // tile row
         const int mi = m / p.group, mg = m - mi * p.group;              // query row of the piece, head of the group
@@ -790,7 +1051,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     on = mi < pc.nrows;
                     warp_on = quarter * 32 < pc.nrows * p.group;
                     bound = pc.keys;
-                    if (on && pc.minb != pc.keys) bound = p.ends[pc.row0 + mi];
+                    if (on && pc.minb != pc.keys) bound = min(max(p.row_ends[pc.row0 + mi], 0), p.max_keys);
                 }
                 if (warp_on) {
                     uint32_t w[64];
@@ -876,9 +1137,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     part = p.xo + at * p.dim;
                     if (on && half == 0) p.xml[at] = make_float2(ref, l);
                 } else {
-                    const int64_t at = static_cast<int64_t>(pc.slot) * p.rows_cap + m;
-                    part = p.po + at * p.dim;
-                    if (on && !direct && half == 0) p.pml[at] = make_float2(ref, l);
+                    const bool own = kSelected || pc.req >= 0;
+                    const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + m;
+                    part = (own ? p.po : p.xo) + at * p.dim;
+                    if (on && !direct && half == 0) (own ? p.pml : p.xml)[at] = make_float2(ref, l);
                 }
                 if (on && direct && half == 0 && p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
@@ -887,19 +1149,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     uint32_t o[16];
                     tc_ld_32x32b_x16(a_o + x, o);
                     tc_wait_ld16(o);
-                    if (!kSelected && poison && on) {
-                        // the values that were taken out of the products, for the rows that see them
-                        const int from = max(pc.minb, tile0 * kTile), to = min(bound, (tile0 + ntiles) * kTile);
-                        for (int k = from; k < to; ++k) {
-                            const int page = p.bt[pc.req * p.bt_stride + k / kPage];
-                            if (page < 0 || page >= p.num_pages) continue;
-                            const uint16_t* v = p.vbase + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (half_wild<T>(v[j]))
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) + T::unpack(v[j]).x);
-                        }
-                    }
+                    if (!kSelected && poison && on) add_wild<T>(p, pc, bound, x, o);
                     if (on && direct) {
                         uint32_t h[8];
 #pragma unroll
@@ -944,48 +1194,51 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
     if (item >= static_cast<int64_t>(p.rows) * p.heads) return;
     const int row = static_cast<int>(item / p.heads), head = static_cast<int>(item % p.heads);
     const int kvh = head / p.group, g = head - kvh * p.group;
-    const int s = p.row_seg[row];
+    const RowInfo ri = p.row_info[row];
+    const int64_t T_all = p.info[0];
     // two runs of pieces: the row's own keys and the prefix
     const float2* ml[2] = {nullptr, nullptr};
     const float* po[2] = {nullptr, nullptr};
-    int64_t step[2] = {0, 0};   // tile rows from one piece to the next
+    int step[2] = {p.own_cap, p.x_cap};   // tile rows from one piece to the next
     int n[2] = {0, 0};
-    if (s >= 0) {
-        const int64_t T_all = p.info[0];
+    if (ri.seg >= 0) {
         const int64_t W = p.workers < T_all ? p.workers : T_all;
-        for (int x = 0; x < (p.prefix_mode == 1 ? 2 : 1); ++x) {
-            const int sx = x == 0 ? s : 0;
-            const int4 rec = p.seg[sx];
-            const int tph = tiles_of(rec.w);
-            if (tph == 0) continue;
-            const int64_t first = p.prefix[sx] + static_cast<int64_t>(kvh) * tph;
-            const int wa = worker_of(first, T_all, W), wb = worker_of(first + tph - 1, T_all, W);
-            const int64_t at = (static_cast<int64_t>(sx) * p.kv_heads + kvh + wa) * p.rows_cap + (row - rec.x) * p.group + g;
-            ml[x] = p.pml + at;
-            po[x] = p.po + at * p.dim;
-            step[x] = p.rows_cap;
-            n[x] = wb - wa + 1;
+        if (ri.tph > 0) {
+            const int64_t first = ri.first + static_cast<int64_t>(kvh) * ri.tph;
+            const int wa = worker_of(first, T_all, W), wb = worker_of(first + ri.tph - 1, T_all, W);
+            const int64_t at =
+                (static_cast<int64_t>(ri.seg) * p.kv_heads + kvh + wa) * p.own_cap + (row - ri.row0) * p.group + g;
+            ml[0] = p.pml + at;
+            po[0] = p.po + at * p.dim;
+            n[0] = wb - wa + 1;
+            if (p.prefix_mode == 0 && n[0] == 1) return;   // written by the attention kernel
         }
-        if (p.prefix_mode == 0 && n[0] == 1) return;   // written by the attention kernel
-        if (p.prefix_mode == 2) {
+        if (p.prefix_mode != 0) {
             const int tph = tiles_of(p.prefix_len);
-            const int64_t T_x = static_cast<int64_t>(p.x_pairs) * p.kv_heads * tph;
-            const int64_t W_x = p.x_workers < T_x ? p.x_workers : T_x;
-            const int pair = row / (2 * p.x_rps), in = row - pair * 2 * p.x_rps;
-            const int64_t it = static_cast<int64_t>(kvh) * p.x_pairs + pair;
-            const int wa = worker_of(it * tph, T_x, W_x), wb = worker_of(it * tph + tph - 1, T_x, W_x);
-            const int half = in >= p.x_rps;
-            const int64_t at = ((it + wa) * 2 + half) * 128 + (in - half * p.x_rps) * p.group + g;
+            const int tile = row / p.x_rps, in = row - tile * p.x_rps;   // row tile of 128 rows
+            int64_t at;
+            if (p.prefix_mode == 1) {
+                const int64_t it = static_cast<int64_t>(tile) * p.kv_heads + kvh;
+                const int wa = worker_of(it * tph, T_all, W), wb = worker_of(it * tph + tph - 1, T_all, W);
+                at = (it + wa) * p.x_cap + in * p.group + g;
+                n[1] = wb - wa + 1;
+            } else {
+                const int64_t T_x = static_cast<int64_t>(p.x_pairs) * p.kv_heads * tph;
+                const int64_t W_x = p.x_workers < T_x ? p.x_workers : T_x;
+                const int64_t it = static_cast<int64_t>(kvh) * p.x_pairs + tile / 2;
+                const int wa = worker_of(it * tph, T_x, W_x), wb = worker_of(it * tph + tph - 1, T_x, W_x);
+                at = ((it + wa) * 2 + tile % 2) * 128 + in * p.group + g;
+                step[1] = 256;
+                n[1] = wb - wa + 1;
+            }
             ml[1] = p.xml + at;
             po[1] = p.xo + at * p.dim;
-            step[1] = 256;
-            n[1] = wb - wa + 1;
         }
     }
     const bool on = lane * 4 < p.dim;
     float top = -INFINITY;
     for (int x = 0; x < 2; ++x)
-        for (int i = lane; i < n[x]; i += 32) top = fmaxf(top, ml[x][i * step[x]].x);
+        for (int i = lane; i < n[x]; i += 32) top = fmaxf(top, ml[x][static_cast<int64_t>(i) * step[x]].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     float l = 0.0f;
@@ -993,9 +1246,9 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
     for (int x = 0; x < 2; ++x) {
 #pragma unroll 4
         for (int i = kWarps == 1 ? 0 : warp; i < n[x]; i += kWarps) {
-            const float2 e = ml[x][i * step[x]];
+            const float2 e = ml[x][static_cast<int64_t>(i) * step[x]];
             float4 v = {0, 0, 0, 0};
-            if (on) v = *reinterpret_cast<const float4*>(po[x] + i * step[x] * p.dim + lane * 4);
+            if (on) v = *reinterpret_cast<const float4*>(po[x] + static_cast<int64_t>(i) * step[x] * p.dim + lane * 4);
             const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - top);
             l += e.y * f;
             o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
@@ -1030,23 +1283,16 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// Query rows per segment: what fits a tile of 128 rows, no more than a request
-// is said to have, but all rows where they fit one tile (a prefix then is one segment).
-static int64_t rows_per_segment(int64_t rows, int64_t group, int64_t max_query_len, int64_t k) {
-    if (k > 0) return 1;
-    const int64_t most = 128 / group;
-    return rows <= most ? (rows > 0 ? rows : 1) : clamp64(max_query_len, 1, most);
-}
-
 static AttLayout attend_layout(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
                                int64_t max_query_len, int64_t k) {
     AttLayout L = {};
-    const int64_t group = heads / kv_heads;
-    const int64_t rps = rows_per_segment(rows, group, max_query_len, k);
-    // every request starts a segment of its own; one more for the prefix
-    const int64_t full = rows / rps + num_requests;
-    L.max_segs = k > 0 ? rows : (rows < full ? rows : full) + 1;
-    L.rows_cap = group * rps;
+    const int64_t group = heads / kv_heads, most = 128 / group;
+    // a request's segments: as many rows as a request is said to have, no more than fit a tile
+    L.own_rps = k > 0 ? 1 : clamp64(max_query_len < rows ? max_query_len : rows, 1, most);
+    const int64_t full = rows / L.own_rps + num_requests;   // every request starts a segment of its own
+    const int64_t segs = k > 0 || rows < full ? rows : full;
+    const int64_t px = k > 0 ? 0 : (rows + most - 1) / most;   // row tiles behind a prefix
+    L.max_segs = segs + px;
     L.kpad = (k + kTile - 1) / kTile * kTile;
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -1054,21 +1300,22 @@ static AttLayout attend_layout(int64_t rows, int64_t num_requests, int64_t heads
         at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
         return here;
     };
-    L.ticket = take(256);
     L.info = take(16);
     L.seg = take(L.max_segs * 16);
     L.minb = take(L.max_segs * 4);
     L.prefix = take((L.max_segs + 1) * 8);
     L.worker = take(kMaxWorkers * 4);
-    L.row_seg = take(rows * 4);
-    L.ends = take(rows * 4);
+    L.row_info = take(rows * static_cast<int64_t>(sizeof(RowInfo)));
+    L.count = take(k > 0 ? rows * 4 : 0);
     L.list = take(rows * L.kpad * 4);
-    const int64_t slots = (L.max_segs * kv_heads + kMaxWorkers) * L.rows_cap;
+    // a piece per item, and one more where a worker's share ends inside an item
+    const int64_t slots = (segs * kv_heads + kMaxWorkers) * group * L.own_rps;
     L.po = take(slots * dim * 4);
     L.pml = take(slots * 8);
-    if (k == 0 && rows * group > 128) {
-        const int64_t x_rps = 128 / group, pairs = (rows + 2 * x_rps - 1) / (2 * x_rps);
-        const int64_t xslots = (pairs * kv_heads + kMaxCtas) * 256;
+    if (k == 0) {
+        // single row tiles over 2 workers a CTA, or pairs of them over one: pairs take the most room
+        const int64_t xslots = px == 1 ? (kv_heads + kMaxWorkers) * group * (rows < most ? rows : most)
+                                       : ((px + 1) / 2 * kv_heads + kMaxCtas) * 256;
         L.xo = take(xslots * dim * 4);
         L.xml = take(xslots * 8);
     }
@@ -1167,19 +1414,21 @@ static int page_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t
 constexpr int kSmemMost = 232448;   // 227 KB
 
 // Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
-static int fit_shared(int rows, int halves, bool paired, AttParams& p) {
-    p.q_half = (rows * 128 + 1023) / 1024 * 1024;
-    p.nqb = !paired && rows <= 32 ? 2 : 1;
-    const int stage = halves * kTile * 128, fixed = 2 * p.nqb * halves * p.q_half + kAttMeta;
+static int fit_shared(int halves, bool paired, bool narrow, AttParams& p) {
+    p.q_half = narrow ? 128 * 128 : (p.rows_cap * 128 + 1023) / 1024 * 1024;
+    p.nqb = 1;
+    const int stage = halves * kTile * 128;
+    const int fixed = 2 * halves * p.q_half + (narrow ? 2 * kMergeBytes : 0) + kAttMeta +
+                      (p.plan_in_cta && !paired ? static_cast<int>(sizeof(AxisShared)) : 0);
     int n = (kSmemMost - fixed) / stage;
     if (!paired) n /= 2;
     p.nst = n > kMaxStages ? kMaxStages : n;
     return fixed + (paired ? 1 : 2) * p.nst * stage;
 }
 
-template <typename T, bool kPaired, bool kSelected, int DH>
-static int launch_attention(const AttCall& a, int grid, int smem, cudaStream_t stream) {
-    auto* kernel = attend_kernel<T, kPaired, kSelected, DH>;
+template <typename T, bool kPaired, bool kSelected, bool kNarrow, int DH>
+static int launch_attention(const AttCall& a, int smem, cudaStream_t stream) {
+    auto* kernel = attend_kernel<T, kPaired, kSelected, kNarrow, DH>;
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
@@ -1188,26 +1437,28 @@ static int launch_attention(const AttCall& a, int grid, int smem, cudaStream_t s
             return DSA_ERR_CUDA;
         attr_set[dev] = true;
     }
-    return launch_pdl(kernel, dim3(grid), dim3(kAttThreads), smem, stream, a.q, a.k, a.v, a.p) == cudaSuccess
+    return launch_pdl(kernel, dim3(a.ctas), dim3(att_threads<kSelected, kNarrow>()), smem, stream, a.q, a.k, a.v,
+                      a.p) == cudaSuccess
                ? DSA_OK
                : DSA_ERR_CUDA;
 }
 
-template <bool kPaired, bool kSelected>
-static int launch_attention(const AttCall& a, int dtype, int grid, int smem, cudaStream_t stream) {
+template <bool kPaired, bool kSelected, bool kNarrow>
+static int launch_attention(AttCall& a, int dtype, cudaStream_t stream) {
+    const int smem = fit_shared(a.p.dim > 64 ? 2 : 1, kPaired, kNarrow, a.p);
     if (a.p.dim > 64)
-        return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, 2>(a, grid, smem, stream)
-                                 : launch_attention<Fp16, kPaired, kSelected, 2>(a, grid, smem, stream);
-    return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, 1>(a, grid, smem, stream)
-                             : launch_attention<Fp16, kPaired, kSelected, 1>(a, grid, smem, stream);
+        return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, kNarrow, 2>(a, smem, stream)
+                                 : launch_attention<Fp16, kPaired, kSelected, kNarrow, 2>(a, smem, stream);
+    return dtype == DSA_BF16 ? launch_attention<Bf16, kPaired, kSelected, kNarrow, 1>(a, smem, stream)
+                             : launch_attention<Fp16, kPaired, kSelected, kNarrow, 1>(a, smem, stream);
 }
 
 template <typename T>
-static int launch_join(const AttParams& p, int ctas, cudaStream_t stream) {
+static int launch_join(const AttParams& p, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
     if (items > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     // few rows: their many pieces are shared by the warps of a CTA
-    const cudaError_t e = items <= 16 * ctas
+    const cudaError_t e = static_cast<int64_t>(p.rows) * p.kv_heads * 4 <= p.workers
                               ? launch_pdl(attend_join_kernel<T, 8>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
                                            stream, p)
                               : launch_pdl(attend_join_kernel<T, 1>, dim3(static_cast<unsigned>((items + 3) / 4)),
@@ -1215,26 +1466,40 @@ static int launch_join(const AttParams& p, int ctas, cudaStream_t stream) {
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+// Plan (where the CTAs do not make it), attention over the axis, join.
+template <bool kSelected>
+static int launch_axis(AttCall& a, int dtype, cudaStream_t stream) {
+    AttParams& p = a.p;
+    if (!p.plan_in_cta && launch_pdl(attend_plan_kernel<kSelected>, dim3(1), dim3(kPlanThreads), 0, stream, p) !=
+                              cudaSuccess)
+        return DSA_ERR_CUDA;
+    const int rc = p.rows_cap <= 32 ? launch_attention<false, kSelected, true>(a, dtype, stream)
+                                    : launch_attention<false, kSelected, false>(a, dtype, stream);
+    if (rc != DSA_OK) return rc;
+    return dtype == DSA_BF16 ? launch_join<Bf16>(p, stream) : launch_join<Fp16>(p, stream);
+}
+
 static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
     AttParams& p = a.p;
     const AttLayout& L = a.L;
-    p.ticket = reinterpret_cast<int*>(ws + L.ticket);
     p.info = reinterpret_cast<int64_t*>(ws + L.info);
-    p.seg = reinterpret_cast<int4*>(ws + L.seg);
-    p.minb = reinterpret_cast<int*>(ws + L.minb);
-    p.prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
+    p.axis = Axis{reinterpret_cast<int64_t*>(ws + L.prefix), reinterpret_cast<int4*>(ws + L.seg),
+                  reinterpret_cast<int*>(ws + L.minb)};
     p.worker = reinterpret_cast<int*>(ws + L.worker);
-    p.row_seg = reinterpret_cast<int*>(ws + L.row_seg);
-    p.ends = reinterpret_cast<int*>(ws + L.ends);
+    p.row_info = reinterpret_cast<RowInfo*>(ws + L.row_info);
+    p.count = reinterpret_cast<int*>(ws + L.count);
     p.list = reinterpret_cast<int*>(ws + L.list);
     p.po = reinterpret_cast<float*>(ws + L.po);
     p.pml = reinterpret_cast<float2*>(ws + L.pml);
     p.xo = reinterpret_cast<float*>(ws + L.xo);
     p.xml = reinterpret_cast<float2*>(ws + L.xml);
     p.max_segs = static_cast<int>(L.max_segs);
-    p.rows_cap = static_cast<int>(L.rows_cap);
+    p.own_rps = static_cast<int>(L.own_rps);
     p.kpad = static_cast<int>(L.kpad);
     p.group = p.heads / p.kv_heads;
+    p.own_cap = p.group * p.own_rps;
+    p.rps = p.own_rps, p.rows_cap = p.own_cap;
+    p.plan_in_cta = p.max_segs <= kPlanSegs && p.rows <= kPlanRows;
     const int sms = device_sm_count();
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.workers = 2 * a.ctas;
@@ -1283,32 +1548,38 @@ extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_
     p.prefix_len = static_cast<int>(prefix_len);
     p.scale_log2 = scale * kLog2e;
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
-    p.rps = static_cast<int>(rows_per_segment(rows, p.group, max_query_len, 0));
-    p.prefix_mode = prefix_len == 0 ? 0 : rows * p.group <= 128 ? 1 : 2;
+    if (prefix_len > 0) {
+        const int most = 128 / p.group;
+        p.x_rps = p.rows < most ? p.rows : most;
+        p.x_cap = p.group * p.x_rps;
+        const int tiles = (p.rows + p.x_rps - 1) / p.x_rps;
+        p.x_pairs = (tiles + 1) / 2;
+        p.x_workers = a.ctas;
+        // Row tiles in pairs read the prefix half as often; single ones share the axis (and the launch).
+        p.prefix_mode = tiles > 1 && static_cast<int64_t>(p.x_pairs) * p.kv_heads * ((prefix_len + kTile - 1) / kTile) >
+                                         2 * a.ctas
+                            ? 2
+                            : 1;
+        if (p.prefix_mode == 1) {
+            p.px_segs = tiles;
+            p.rps = p.x_rps > p.own_rps ? p.x_rps : p.own_rps;
+            p.rows_cap = p.group * p.rps;
+        }
+    }
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const dsa_kv_cache c = mapped_cache(cache, workspace);
     rc = page_map(&a.k, &c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride);
     if (rc == DSA_OK) rc = page_map(&a.v, &c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride);
     if (rc != DSA_OK) return rc;
-    const int halves = p.dim > 64 ? 2 : 1;
-    if (launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return DSA_ERR_CUDA;
     if (p.prefix_mode == 2) {
         AttCall x = a;
-        p.x_rps = 128 / p.group;
-        p.x_pairs = static_cast<int>((rows + 2 * p.x_rps - 1) / (2 * p.x_rps));
-        p.x_workers = a.ctas;
-        x.p = p;
-        x.p.rows_cap = p.group * p.x_rps;
-        const int smem = fit_shared(x.p.rows_cap, halves, true, x.p);
+        x.p.rows_cap = p.x_cap;
         rc = query_map(&x.q, cache, q, q_row_stride, q_head_stride, rows, heads, p.x_rps);
-        if (rc == DSA_OK) rc = launch_attention<true, false>(x, cache->dtype, a.ctas, smem, stream);
+        if (rc == DSA_OK) rc = launch_attention<true, false, false>(x, cache->dtype, stream);
         if (rc != DSA_OK) return rc;
     }
-    const int smem = fit_shared(p.rows_cap, halves, false, p);
     rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, p.rps);
-    if (rc == DSA_OK) rc = launch_attention<false, false>(a, cache->dtype, a.ctas, smem, stream);
-    if (rc != DSA_OK) return rc;
-    return cache->dtype == DSA_BF16 ? launch_join<Bf16>(p, a.ctas, stream) : launch_join<Fp16>(p, a.ctas, stream);
+    return rc == DSA_OK ? launch_axis<false>(a, cache->dtype, stream) : rc;
 }
 
 extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -1338,16 +1609,12 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0, p.num_pages = static_cast<int>(cache->num_pages);
     p.scale_log2 = scale * kLog2e;
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
-    p.rps = 1;
     rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, 1);
     a.k = a.v = a.q;   // (keys are copied from the pools, not through maps)
     if (rc != DSA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    const int smem = fit_shared(p.rows_cap, p.dim > 64 ? 2 : 1, false, p);
     if (launch_pdl(attend_list_kernel, dim3(static_cast<unsigned>(rows)), dim3(kListThreads), 0, stream, p) !=
         cudaSuccess)
         return DSA_ERR_CUDA;
-    rc = launch_attention<false, true>(a, cache->dtype, a.ctas, smem, stream);
-    if (rc != DSA_OK) return rc;
-    return cache->dtype == DSA_BF16 ? launch_join<Bf16>(p, a.ctas, stream) : launch_join<Fp16>(p, a.ctas, stream);
+    return launch_axis<true>(a, cache->dtype, stream);
 }
