@@ -154,7 +154,7 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* warp_tmp, in
     return v;
 }
 
-// Lays out the axis (whole block).  `tmp`: 33 int64 of shared scratch; `bounds`:
+// Lays out the axis in global memory (whole block).  `tmp`: 33 int64 of shared scratch; `bounds`:
 // shared scratch of one int per row, or null.  One block also writes what the
 // join reads (`write`).  Returns the tiles; *segs: the segments.
 template <bool kSelected>
@@ -242,6 +242,113 @@ __device__ int64_t lay_out(const AttParams& p, const Axis& ax, int64_t* tmp, int
     __syncthreads();
     *segs = S;
     return carry;
+}
+
+// The same for up to kPlanSegs segments of at most as many requests, in shared
+// memory: one warp does it with warp scans (the block's scans and their barriers
+// cost 2 us where this takes half of one), after all threads have fetched the
+// bounds.
+template <bool kSelected>
+__device__ int64_t lay_out_few(const AttParams& p, const Axis& ax, int* bounds, int64_t* result, bool write,
+                               int* segs) {
+    constexpr int kChunks = kPlanSegs / 32;
+    const int lane = threadIdx.x & 31;
+    const bool first = threadIdx.x < 32;
+    int a[kChunks], b[kChunks];
+    if (!kSelected && first) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int q = i * 32 + lane;
+            a[i] = q < p.R ? p.starts[q] : 0;
+            b[i] = q < p.R ? p.starts[q + 1] : 0;
+        }
+    }
+    for (int r = threadIdx.x; r < p.rows; r += blockDim.x) bounds[r] = kSelected ? p.count[r] : p.row_ends[r];
+    if (!kSelected && write)
+        for (int r = threadIdx.x; r < p.rows; r += blockDim.x) p.row_info[r] = RowInfo{0, -1, 0, 0, 0};
+    __syncthreads();
+    if (first) {
+        bool bad = false;
+        int S = p.rows;
+        if (kSelected) {
+            for (int r = lane; r < S; r += 32) {
+                ax.seg[r] = make_int4(r, 1, 0, bounds[r]);
+                ax.minb[r] = bounds[r];
+            }
+        } else {
+            for (int i = lane; i < p.px_segs; i += 32) {
+                ax.seg[i] = make_int4(i * p.x_rps, min(p.x_rps, p.rows - i * p.x_rps), -1, p.prefix_len);
+                ax.minb[i] = p.prefix_len;
+            }
+            S = p.px_segs;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                if (i * 32 >= p.R) break;
+                if (a[i] < 0 || b[i] < a[i] || b[i] > p.rows) bad = true;
+                const int s0 = min(max(a[i], 0), p.rows), s1 = min(max(b[i], s0), p.rows);
+                const int nseg = (s1 - s0 + p.own_rps - 1) / p.own_rps;
+                int inc = nseg;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                const int at = S + inc - nseg;
+                for (int j = 0; j < nseg; ++j) {
+                    if (at + j >= p.max_segs) {   // overlapping requests
+                        bad = true;
+                        break;
+                    }
+                    const int row0 = s0 + j * p.own_rps, nr = min(p.own_rps, s1 - row0);
+                    int most = 0, least = 0x7FFFFFFF;
+                    for (int r = row0; r < row0 + nr; ++r) {
+                        const int e = min(max(bounds[r], 0), p.max_keys);
+                        if (e != bounds[r]) bad = true;
+                        most = max(most, e);
+                        least = min(least, e);
+                    }
+                    ax.seg[at + j] = make_int4(row0, nr, i * 32 + lane, most);
+                    ax.minb[at + j] = least;
+                }
+                S = min(S + __shfl_sync(0xFFFFFFFFu, inc, 31), p.max_segs);
+            }
+        }
+        __syncwarp();
+        int64_t carry = 0;
+        for (int base = 0; base < S; base += 32) {
+            const int i = base + lane;
+            const int4 rec = i < S ? ax.seg[i] : make_int4(0, 0, 0, 0);
+            const int tph = tiles_of(rec.w);
+            int64_t inc = static_cast<int64_t>(tph) * p.kv_heads;
+            const int64_t n = inc;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            const int64_t before = carry + inc - n;
+            if (i < S) {
+                ax.prefix[i] = before;
+                if (write && i >= p.px_segs)
+                    for (int r = rec.x; r < rec.x + rec.y; ++r)
+                        p.row_info[r] = RowInfo{before, i - p.px_segs, rec.x, tph, 0};
+            }
+            carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        if (lane == 0) {
+            ax.prefix[S] = carry;
+            result[0] = carry;
+            result[1] = S;
+            if (write) {
+                p.info[0] = carry;
+                p.info[1] = S;
+            }
+        }
+        if (write && bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    }
+    __syncthreads();
+    *segs = static_cast<int>(result[1]);
+    return result[0];
 }
 
 // The segment with tile t: the last that starts at or before it (segments
@@ -466,8 +573,10 @@ struct AxisShared {
 // slot, or 4 where tiles are narrow (and 4 more a slot that copy listed keys).
 template <bool kSelected, bool kNarrow>
 __host__ __device__ constexpr int att_threads() { return kNarrow && !kSelected ? 384 : 640; }
-constexpr int kMergeCols = 16;
-constexpr int kMergeBytes = 4 * 32 * kMergeCols * 4;   // narrow: one slot's buffer
+// Narrow: the part of a strip's outputs that is joined at a time, 8 rows of 64
+// columns, 16 of 32 or 32 of 16, each row padded by four floats.
+constexpr int kMergeFloats = 640;
+constexpr int kMergeBytes = 4 * kMergeFloats * 4;    // four strips, one slot
 
 // One CTA runs two slots, each a pipeline of its own: a producer warp (TMA), an
 // MMA warp and softmax warps, a thread per tile row (the lanes of tensor memory).
@@ -551,8 +660,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     } else if (p.plan_in_cta) {
         // (the ring is scratch until the first copy)
         axis = Axis{axis_sh.prefix, axis_sh.seg, axis_sh.minb};
-        T_all = lay_out<kSelected>(p, axis, reinterpret_cast<int64_t*>(ring0), reinterpret_cast<int*>(ring0 + 512),
-                                   blockIdx.x == 0, &S);
+        T_all = lay_out_few<kSelected>(p, axis, reinterpret_cast<int*>(ring0 + 512), reinterpret_cast<int64_t*>(ring0),
+                                       blockIdx.x == 0, &S);
         fence_proxy_async_smem();
         __syncthreads();
     } else {
@@ -861,7 +970,11 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         }
     } else if (kNarrow) {
         // ------------------------------------------------- softmax, narrow: 32 keys of a row per thread
-        const int mi = lane / p.group, mg = lane - mi * p.group;        // query row of the piece, head of the group
+        const int mi = lane / p.group;                                  // query row of the piece
+        // the join at a piece's end: rows the buffer is laid out for, this thread's row there and its first column
+        const int mrows = p.rows_cap <= 8 ? 8 : p.rows_cap <= 16 ? 16 : 32;
+        const int r = (quarter * 32 + lane) & (mrows - 1), col4 = (quarter * 32 + lane) / mrows * 4;
+        const int ri = r / p.group, rg = r - ri * p.group, mcols = 512 / mrows;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t a_s = tmem + lanes + slot * 128, a_o = tmem + lanes + 256 + slot * 128;
         const float c = p.scale_log2;
@@ -961,57 +1074,82 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             if (!ok) break;
             ph_o ^= 1;
             tc_fence_after();
-            // The four strips are joined: each scaled to the common reference, then added.
-            const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
-            const int row = pc.row0 + mi, head = pc.kvh * p.group + mg;
-            const bool direct = pc.direct, own = pc.req >= 0 || kSelected;
+            // The four strips are joined, as many columns at a time as the buffer holds for this call's rows.
+            // (Loops stay rolled and accesses are 16 bytes wide: this code runs once a piece, and instructions
+            // that are not in the cache cost more than what they do.)  A thread writes its row's strip and adds
+            // four columns of row `r`, each strip brought to the row's common reference.
             ml[quarter * 32 + lane] = make_float2(m_ref, l);
             if (!meet()) break;
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) top = fmaxf(top, ml[x * 32 + lane].x);
+            const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
+            const bool direct = pc.direct, own = pc.req >= 0 || kSelected;
+            const bool r_on = ri < pc.nrows;
+            float2 e[4];
+            float top = -INFINITY, sum = 0.0f, f[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float2 e = ml[x * 32 + lane];
-                sum += e.y * (e.x == -INFINITY ? 0.0f : ex2(e.x - top));
+                e[x] = ml[x * 32 + r];
+                top = fmaxf(top, e[x].x);
             }
-            const float f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - top);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                f[x] = e[x].x == -INFINITY ? 0.0f : ex2(e[x].x - top);
+                sum += e[x].y * f[x];
+            }
             const float ref = top == -INFINITY ? -INFINITY : top - Facts<T>::shift;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int row = pc.row0 + ri, head = pc.kvh * p.group + rg;
             uint16_t* out = p.out + row * p.orow + head * p.ohead;
-            const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + lane;
+            const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + r;
             float* part = (own ? p.po : p.xo) + at * p.dim;
-            if (on && quarter == 0) {
+            if (direct) {
+                const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] *= inv;
+            }
+            if (r_on && col4 == 0) {
                 if (!direct)
                     (own ? p.pml : p.xml)[at] = make_float2(ref, sum);
                 else if (p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
-                        sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                        sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
             }
-            for (int x = 0; x < p.dim; x += kMergeCols) {
-                uint32_t o[16];
-                tc_ld_32x32b_x16(a_o + x, o);
-                tc_wait_ld16(o);
+#pragma unroll 1
+            for (int x = 0; x < p.dim; x += mcols) {
+                if (x > 0 && !meet()) break;                            // the buffer has been read
+#pragma unroll 1
+                for (int y = 0; y < mcols; y += 16) {
+                    if (x + y >= p.dim) break;
+                    uint32_t o[16];
+                    tc_ld_32x32b_x16(a_o + x + y, o);
+                    tc_wait_ld16(o);
+                    if (!kSelected && poison && on && quarter == 0) {
+                        uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                if (!kSelected && poison && on && quarter == 0) add_wild<T>(p, pc, bound, x, o);
+                        for (int j = 0; j < 16; ++j) w[j] = o[j];
+                        add_wild<T>(p, pc, bound, x + y, w);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) buf[(quarter * 16 + j) * 32 + lane] = __uint_as_float(o[j]);
-                if (!meet()) break;
-                float v[4];
+                        for (int j = 0; j < 16; ++j) o[j] = w[j];
+                    }
+                    if (lane < mrows) {
+                        uint4* to = reinterpret_cast<uint4*>(buf + quarter * kMergeFloats + lane * (mcols + 4) + y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] = 0.0f;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) v[j] += buf[(y * 16 + quarter * 4 + j) * 32 + lane];
+                        for (int j = 0; j < 4; ++j)
+                            to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
                 }
-                const int col = x + quarter * 4;
-                if (on && direct)
-                    *reinterpret_cast<uint2*>(out + col) =
-                        make_uint2(T::pack(v[0] * inv, v[1] * inv), T::pack(v[2] * inv, v[3] * inv));
-                else if (on)
-                    *reinterpret_cast<float4*>(part + col) = make_float4(v[0], v[1], v[2], v[3]);
                 if (!meet()) break;
+                float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float4 u = *reinterpret_cast<const float4*>(buf + y * kMergeFloats + r * (mcols + 4) + col4);
+                    v.x += u.x * f[y], v.y += u.y * f[y], v.z += u.z * f[y], v.w += u.w * f[y];
+                }
+                if (r_on && x + col4 < p.dim) {
+                    if (direct)
+                        *reinterpret_cast<uint2*>(out + x + col4) =
+                            make_uint2(T::pack(v.x, v.y), T::pack(v.z, v.w));
+                    else
+                        *reinterpret_cast<float4*>(part + x + col4) = v;
+                }
             }
             if (!ok) break;
             tc_fence_before();
@@ -1149,7 +1287,14 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     uint32_t o[16];
                     tc_ld_32x32b_x16(a_o + x, o);
                     tc_wait_ld16(o);
-                    if (!kSelected && poison && on) add_wild<T>(p, pc, bound, x, o);
+                    if (!kSelected && poison && on) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = o[j];
+                        add_wild<T>(p, pc, bound, x, w);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = w[j];
+                    }
                     if (on && direct) {
                         uint32_t h[8];
 #pragma unroll
@@ -1236,38 +1381,57 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
         }
     }
     const bool on = lane * 4 < p.dim;
-    float top = -INFINITY;
-    for (int x = 0; x < 2; ++x)
-        for (int i = lane; i < n[x]; i += 32) top = fmaxf(top, ml[x][static_cast<int64_t>(i) * step[x]].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    float l = 0.0f;
+    // One pass over the pieces of both runs, kAhead at a time, with a running reference.
+    constexpr int kAhead = kWarps == 1 ? 4 : 8;
+    const int all = n[0] + n[1];
+    float top = -INFINITY, l = 0.0f;
     float4 o = {0, 0, 0, 0};
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll 4
-        for (int i = kWarps == 1 ? 0 : warp; i < n[x]; i += kWarps) {
-            const float2 e = ml[x][static_cast<int64_t>(i) * step[x]];
-            float4 v = {0, 0, 0, 0};
-            if (on) v = *reinterpret_cast<const float4*>(po[x] + static_cast<int64_t>(i) * step[x] * p.dim + lane * 4);
-            const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - top);
-            l += e.y * f;
-            o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+    for (int base = kWarps == 1 ? 0 : warp; base < all; base += kAhead * kWarps) {
+        float2 e[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = base + j * kWarps;
+            const int x = i < n[0] ? 0 : 1;
+            const int64_t at = static_cast<int64_t>(i - (x ? n[0] : 0)) * step[x];
+            e[j] = make_float2(-INFINITY, 0.0f);
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < all) {
+                e[j] = ml[x][at];
+                if (on) v[j] = *reinterpret_cast<const float4*>(po[x] + at * p.dim + lane * 4);
+            }
+        }
+        float m = top;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) m = fmaxf(m, e[j].x);
+        const float keep = top == -INFINITY ? 0.0f : ex2(top - m);
+        top = m;
+        l *= keep;
+        o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const float f = e[j].x == -INFINITY ? 0.0f : ex2(e[j].x - m);
+            l += e[j].y * f;
+            o.x += v[j].x * f, o.y += v[j].y * f, o.z += v[j].z * f, o.w += v[j].w * f;
         }
     }
     if (kWarps > 1) {
-        __shared__ float sl[kWarps];
+        __shared__ float2 sl[kWarps];
         __shared__ float4 so[kWarps][32];
-        if (lane == 0) sl[warp] = l;
+        if (lane == 0) sl[warp] = make_float2(top, l);
         so[warp][lane] = o;
         __syncthreads();
         if (warp > 0) return;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sl[w].x);
         l = 0.0f;
         o = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float4 v = so[w][lane];
-            l += sl[w];
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            const float f = sl[w].x == -INFINITY ? 0.0f : ex2(sl[w].x - top);
+            l += sl[w].y * f;
+            o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1499,7 +1663,7 @@ static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
     p.group = p.heads / p.kv_heads;
     p.own_cap = p.group * p.own_rps;
     p.rps = p.own_rps, p.rows_cap = p.own_cap;
-    p.plan_in_cta = p.max_segs <= kPlanSegs && p.rows <= kPlanRows;
+    p.plan_in_cta = p.max_segs <= kPlanSegs && p.R <= kPlanSegs && p.rows <= kPlanRows;
     const int sms = device_sm_count();
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.workers = 2 * a.ctas;
