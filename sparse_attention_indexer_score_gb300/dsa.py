@@ -2,7 +2,8 @@
 
 Argument marshalling only: tensors become device pointers, sizes and strides
 become integers, the current CUDA stream is passed through, and a negative
-return code raises.  Every step of the decode step runs in the library's CUDA
+return code raises (by ctypes, and by the native extension ``_dsa_binding`` for
+the append and attention calls, whose latency counts).  Every step of the decode step runs in the library's CUDA
 kernels; there is no fallback path.  The library is loaded on first use and a
 missing library raises.
 """
@@ -25,6 +26,7 @@ Q_ROW_BYTES = 4096
 PAGE_BYTES = {"fp8": 8448, "fp8_mx": 8448, "mxfp4": 4352, "mxfp4_rg": 4352}
 
 _lib = None
+_binding = None
 
 _c = ctypes
 _P = _c.c_void_p
@@ -77,8 +79,6 @@ class KvCache(_c.Structure):
                 ("num_pages", _I64), ("heads", _I64), ("dim", _I64), ("dtype", _c.c_int32)]
 
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1}
-PAGE_TOKENS = 64
 
 
 def lib():
@@ -420,28 +420,17 @@ def topk(logits: torch.Tensor, row_ends: torch.Tensor, k: int, width: Optional[i
     return out
 
 
-def _kv_cache(k_cache: torch.Tensor, v_cache: torch.Tensor):
-    """The C view of the pools, and (heads, dim, dtype)."""
-    dtype, shape = k_cache.dtype, k_cache.shape
-    if dtype not in DTYPES or v_cache.dtype is not dtype:
-        raise ValueError("k_cache and v_cache must both be BF16 or both FP16")
-    if len(shape) != 4 or shape[1] != PAGE_TOKENS or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must be [pages, 64, heads, dim]")
-    pages, _, heads, dim = shape
-    kp, kt, kh, kc = k_cache.stride()
-    vp, vt, vh, vc = v_cache.stride()
-    if kc != 1 or vc != 1:
-        raise ValueError("cache columns must be contiguous")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), kp, kt, kh, vp, vt, vh, pages, heads, dim,
-                   DTYPES[dtype]), heads, dim, dtype
-
-
-def _raw_stream(t: torch.Tensor) -> int:
-    """The current stream's handle without the Python stream object (a call of these is a few microseconds)."""
-    index = t.get_device()
-    if index < 0:
-        raise ValueError("the caches must be CUDA tensors")
-    return torch._C._cuda_getCurrentRawStream(index)
+def _native():
+    """The extension that marshals the calls below (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            from . import _dsa_binding
+        except ImportError as e:
+            raise RuntimeError(f"{HERE}/_dsa_binding.so is missing: build it with __graft_entry__.build()") from e
+        _binding = _dsa_binding
+    return _binding
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -453,44 +442,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: to
     (FP32 [positions, rot]: cosines, then sines) keys and the optional queries
     [n, q_heads, dim] are rotated to ``positions`` (int64 [n]) on the way.
     Returns the rotated queries (``q_out``, which may be ``q``), or None."""
-    c, heads, dim, dtype = _kv_cache(k_cache, v_cache)
-    ks, vs, shape = k.stride(), v.stride(), k.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or v.shape != shape or k.dtype is not dtype \
-            or v.dtype is not dtype or ks[2] != 1 or vs[2] != 1:
-        raise ValueError("k and v must be [n, heads, dim] of the cache's type with contiguous columns")
-    n = shape[0]
-    if slots.dtype is not torch.int64 or slots.shape != (n,) or not slots.is_contiguous():
-        raise ValueError("slots must be contiguous int64 [n], one per key")
-    rot = max_pos = cs_stride = 0
-    pos_ptr = cs_ptr = None
-    if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or (cos_sin.shape[1] and cos_sin.stride(1) != 1):
-            raise ValueError("cos_sin must be FP32 [positions, rot] with contiguous rows")
-        if positions is None or positions.dtype is not torch.int64 or positions.shape != (n,) \
-                or not positions.is_contiguous():
-            raise ValueError("positions must be contiguous int64 [n]")
-        max_pos, rot = cos_sin.shape
-        cs_stride, pos_ptr, cs_ptr = cos_sin.stride(0), positions.data_ptr(), cos_sin.data_ptr()
-    q_heads = qt = qh = ot = oh = 0
-    q_ptr = out_ptr = None
-    if q is not None:
-        qs, shape = q.stride(), q.shape
-        if q.dtype is not dtype or len(shape) != 3 or shape[0] != n or shape[2] != dim or qs[2] != 1:
-            raise ValueError("q must be [n, q_heads, dim] of the cache's type with contiguous columns")
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        elif q_out.dtype is not dtype or q_out.shape != shape or q_out.stride(2) != 1:
-            raise ValueError("q_out must match q")
-        ot, oh, _ = q_out.stride()
-        q_heads, qt, qh, q_ptr, out_ptr = shape[1], qs[0], qs[1], q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    rc = lib().dsa_kv_append(_c.addressof(c), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], q_ptr, qt, qh,
-                             q_heads, out_ptr, ot, oh, n, slots.data_ptr(), pos_ptr, cs_ptr, cs_stride, max_pos, rot,
-                             interleaved, _ptr(status), _raw_stream(k_cache))
-    if rc:
-        _check(rc, "dsa_kv_append")
-    return q_out
+    return (_binding or _native()).kv_append(k, v, slots, k_cache, v_cache, positions, cos_sin, q, q_out, interleaved,
+                                             status)
 
 
 def attend_workspace_size(rows: int, num_requests: int, heads: int, kv_heads: int, dim: int, max_query_len: int,
@@ -498,35 +451,6 @@ def attend_workspace_size(rows: int, num_requests: int, heads: int, kv_heads: in
     """Bytes of scratch of ``attend_paged`` (k = 0) or ``attend_selected`` (k =
     the list length, 1 for empty lists)."""
     return int(lib().dsa_attend_workspace_size(rows, num_requests, heads, kv_heads, dim, max_query_len, k))
-
-
-def _attend_args(q, c, dim, dtype, block_table, starts, row_ends, out, want_lse):
-    """The checks and C arguments the two attention calls share."""
-    shape, qs = q.shape, q.stride()
-    if q.dtype is not dtype or len(shape) != 3 or shape[2] != dim or qs[2] != 1:
-        raise ValueError("q must be [rows, heads, dim] of the cache's type with contiguous columns")
-    i32 = torch.int32
-    if block_table.dtype is not i32 or starts.dtype is not i32 or row_ends.dtype is not i32:
-        raise ValueError("block_table, starts and row_ends must be int32")
-    table, rows, heads = block_table.shape, shape[0], shape[1]
-    requests = starts.numel() - 1
-    if len(table) != 2:
-        raise ValueError("block_table must be [requests, pages]")
-    bt_stride, bt_col = block_table.stride()
-    if table[0] != requests or starts.dim() != 1 or not starts.is_contiguous():
-        raise ValueError("starts must be contiguous, one entry per request and one more")
-    if bt_col != 1 and table[0] and table[1]:
-        raise ValueError("block_table rows must be contiguous")
-    if row_ends.shape != (rows,) or not row_ends.is_contiguous():
-        raise ValueError("row_ends must hold one bound per query row")
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.dtype is not dtype or out.shape != shape or out.stride(2) != 1:
-        raise ValueError("out must match q")
-    lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device) if want_lse else None
-    head = (_c.addressof(c), q.data_ptr(), qs[0], qs[1], heads, block_table.data_ptr(), bt_stride, table[1],
-            starts.data_ptr(), row_ends.data_ptr(), requests, rows)
-    return head, out, lse
 
 
 def attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -539,24 +463,8 @@ def attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     ``prefix_pages`` (int32), shared by the batch, and keys t < row_ends[r] of
     its request.  scale defaults to dim ** -0.5.  Returns (out, lse FP32
     [rows, heads] or None)."""
-    c, kv_heads, dim, dtype = _kv_cache(k_cache, v_cache)
-    head, out, lse = _attend_args(q, c, dim, dtype, block_table, starts, row_ends, out, want_lse)
-    prefix_ptr = None
-    if prefix_len:
-        if prefix_pages is None or prefix_pages.dtype is not torch.int32 or not prefix_pages.is_contiguous() \
-                or prefix_pages.numel() * PAGE_TOKENS < prefix_len:
-            raise ValueError("prefix_pages must be contiguous int32 and hold prefix_len keys")
-        prefix_ptr = prefix_pages.data_ptr()
-    if workspace is None:
-        workspace = new_workspace(
-            attend_workspace_size(head[11], head[10], head[4], kv_heads, dim, max_query_len), q.device)
-    os_ = out.stride()
-    rc = lib().dsa_attend_paged(*head, max_query_len, prefix_ptr, prefix_len, dim ** -0.5 if scale is None else scale,
-                                out.data_ptr(), os_[0], os_[1], _ptr(lse), workspace.data_ptr(), workspace.numel(),
-                                _ptr(status), _raw_stream(k_cache))
-    if rc:
-        _check(rc, "dsa_attend_paged")
-    return out, lse
+    return (_binding or _native()).attend_paged(q, k_cache, v_cache, block_table, starts, row_ends, max_query_len,
+                                                prefix_pages, prefix_len, scale, out, want_lse, workspace, status)
 
 
 def attend_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -566,23 +474,8 @@ def attend_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of decode rows over the key positions of ``topk`` (int32
     [rows, k], the indexer's selection; negative entries are empty).  Other
     arguments and results as ``attend_paged``."""
-    c, kv_heads, dim, dtype = _kv_cache(k_cache, v_cache)
-    head, out, lse = _attend_args(q, c, dim, dtype, block_table, starts, row_ends, out, want_lse)
-    lists = topk.shape
-    if topk.dtype is not torch.int32 or len(lists) != 2 or lists[0] != head[11] \
-            or (topk.stride(1) != 1 and topk.numel()):
-        raise ValueError("topk must be int32 [rows, k] with contiguous rows")
-    k = lists[1]
-    if workspace is None:
-        workspace = new_workspace(attend_workspace_size(head[11], head[10], head[4], kv_heads, dim, 1, max(k, 1)),
-                                  q.device)
-    os_ = out.stride()
-    rc = lib().dsa_attend_selected(*head, topk.data_ptr(), topk.stride(0), k, dim ** -0.5 if scale is None else scale,
-                                   out.data_ptr(), os_[0], os_[1], _ptr(lse), workspace.data_ptr(),
-                                   workspace.numel(), _ptr(status), _raw_stream(k_cache))
-    if rc:
-        _check(rc, "dsa_attend_selected")
-    return out, lse
+    return (_binding or _native()).attend_selected(q, k_cache, v_cache, block_table, starts, row_ends, topk, scale,
+                                                   out, want_lse, workspace, status)
 
 
 class TimingEvent:
