@@ -97,9 +97,10 @@ struct AttParams {
     const int32_t* prefix_pages;
     const int32_t* topk;
     int64_t topk_stride;
-    const uint16_t* kbase;                 // the pools (element strides), where keys are listed
-    const uint16_t* vbase;                 // and where a value is not finite
-    int64_t kp, kt, kh, vp, vt, vh;
+    const uint16_t* vbase;                 // the value pool (element strides), read where a value is not finite
+    int64_t vp, vt, vh;
+    int kpu, ktu, khu, vpu, vtu, vhu;      // listed keys: row numbers per page, token, head in the pools' row maps
+    int k_none, v_none;                    // ... and a row outside the map
     uint16_t* out;
     int64_t orow, ohead;
     float* lse;
@@ -530,11 +531,6 @@ __device__ __forceinline__ bool elect_one() {
 // once, so that the other does not wait for it).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void pair_leave(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
-// The barrier counts this thread once its copies so far are in shared memory.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Where a role stands on the axis, and the ring position it is at.
 struct Ring {
     int st = 0;
@@ -609,13 +605,15 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     volatile int* const abort = &sh.abort;
     const int active = kNarrow ? 4 : (p.rows_cap + 31) / 32;            // 32-row quarters with rows
     const int softmax_warps = kNarrow ? 4 : 2 * active;                 // per slot
-    // Listed keys are copied by the producer warp and by the warps that have no rows.
-    const int copiers = !kSelected ? 1 : kNarrow ? 5 : 1 + 2 * (4 - active);
+    // Listed keys are copied by the warps that have no rows, while the producer warp loads Q; by the
+    // producer warp where every warp has rows.
+    const int helpers = !kSelected ? 0 : kNarrow ? 4 : 2 * (4 - active);
+    const int copiers = helpers ? helpers : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             for (int i = 0; i < p.nst; ++i) {
-                mbar_init(&sh.full[s][i], kSelected ? 32 * copiers : 1);
+                mbar_init(&sh.full[s][i], 1);
                 mbar_init(&sh.empty[s][i], kPaired ? 2 : 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -680,7 +678,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     if (warp < 2 || copies) {
         // ------------------------------------------------- producer
         if (kPaired && slot == 1) goto done;
-        const int copier = warp < 2 ? 0 : kNarrow ? 1 + quarter : 1 + half * (4 - active) + quarter - active;
+        const bool lead = warp < 2;                                     // loads Q and writes the pieces' records
+        const int copier = lead ? 0 : kNarrow ? quarter : half * (4 - active) + quarter - active;
         Ring at;
         int64_t issued = 0;
         int npiece = 0;
@@ -691,6 +690,35 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         int rec_min = 0;
         int64_t rec_pre = 0, rec_next = 0;
         int64_t t = t0;
+        // Q of a piece: the buffer is free once the products of the piece that had it are done.
+        auto load_q = [&](const Piece& pc) {
+            const int b = npiece % p.nqb;
+            const uint32_t ph = (npiece / p.nqb) & 1;
+            bool got = true;
+#pragma unroll
+            for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
+                const int to = kPaired ? x : slot;
+                got = got && warp_wait(&sh.qempty[to][b], ph ^ 1, abort, p.status);
+                if (got && elect_one()) {
+                    // The piece's record; its readers see it through this barrier.
+                    Piece w = pc;
+                    if (kPaired) {
+                        w.row0 = pc.row0 + x * rps;
+                        w.nrows = max(0, min(rps, p.rows - w.row0));
+                    }
+                    sh.piece[to][npiece % kPieces] = w;
+                    uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
+                    constexpr int kCopies = kNarrow ? 4 : 1;
+                    mbar_arrive_expect_tx(&sh.qfull[to][b], kCopies * DH * 128 * p.group * rps);
+#pragma unroll
+                    for (int h = 0; h < DH * kCopies; ++h)
+                        tma_load_3d(qdst + h / kCopies * p.q_half + h % kCopies * 32 * 128, &qmap, h / kCopies * 64,
+                                    pc.kvh * p.group, pc.row0 + (kPaired ? x * rps : 0), &sh.qfull[to][b]);
+                }
+            }
+            ++npiece;
+            return got;
+        };
         while (t < t1 && ok) {
             Piece pc;
             pc.poison = 0;
@@ -738,14 +766,23 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 pc.slot = (pc.req < 0 ? s : s - p.px_segs) * p.kv_heads + pc.kvh + worker;
                 pc.direct = p.prefix_mode == 0 && pc.ntiles == tph;
             }
+            if (kSelected && lead && helpers) {
+                ok = load_q(pc);
+                t += pc.ntiles;
+                continue;
+            }
             const int32_t* pages = pc.req < 0 ? p.prefix_pages : p.bt + pc.req * p.bt_stride;
             const int npages = (pc.keys + kPage - 1) / kPage;
             int held = 0, held_next = 0;                                // 32 page ids, one per lane
-            int ids[4], ids_next[4];                                    // 128 listed slots, lane + 32 j in ids[j]
-            auto listed = [&](int tile, int (&to)[4]) {
-                const int* list = p.list + static_cast<int64_t>(pc.row0) * p.kpad + tile * kTile + lane;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) to[j] = tile * kTile + 32 * j + lane < pc.keys ? list[32 * j] : -1;
+            int4 ids = {0, 0, 0, 0}, ids_next = {0, 0, 0, 0};          // listed slots 4 lane .. 4 lane + 3 of a tile
+            auto listed = [&](int tile) {   // (the list's rows are whole tiles)
+                const int at = tile * kTile + lane * 4;
+                int4 e = *reinterpret_cast<const int4*>(p.list + static_cast<int64_t>(pc.row0) * p.kpad + at);
+                if (at >= pc.keys) e.x = -1;
+                if (at + 1 >= pc.keys) e.y = -1;
+                if (at + 2 >= pc.keys) e.z = -1;
+                if (at + 3 >= pc.keys) e.w = -1;
+                return e;
             };
             auto fetch = [&](int first) {
                 const int j = first + lane;
@@ -759,14 +796,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 }
                 return id;
             };
-            if (kSelected) listed(pc.tile0, ids_next);
+            if (kSelected) ids_next = listed(pc.tile0);
             for (int i = 0; i < pc.ntiles && ok; ++i) {
                 const int tile = pc.tile0 + i;
                 int pg0 = 0, pg1 = 0;
                 if (kSelected) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) ids[j] = ids_next[j];
-                    if (i + 1 < pc.ntiles) listed(tile + 1, ids_next);
+                    ids = ids_next;
+                    if (i + 1 < pc.ntiles) ids_next = listed(tile + 1);
                 } else {
                     if ((i & 15) == 0) {
                         held = i == 0 ? fetch(2 * tile) : held_next;
@@ -782,23 +818,34 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     uint64_t* bar = &sh.full[rs][at.st];
                     uint8_t* dst = ring + at.st * stage_bytes<DH>();
                     if (kSelected) {
-                        // 16 bytes a lane, several keys at once, swizzled as TMA would place them
-                        constexpr int kLanes = DH * 8, kKeys = 32 / kLanes;   // lanes per key, keys per step
-                        const int sub = lane / kLanes, ch = lane % kLanes;
-                        const uint16_t* src = (kv ? p.vbase + pc.kvh * p.vh : p.kbase + pc.kvh * p.kh) + ch * 8;
-                        const int64_t ps = kv ? p.vp : p.kp, ts = kv ? p.vt : p.kt;
-                        const bool in = ch * 8 < p.dim;
+                        // Four listed rows a copy.  The copies' operands pass through uniform registers, which
+                        // makes issuing them the cost: the slot's copiers take every copiers-th group of four.
+                        const CUtensorMap* map = kv ? &vmap : &kmap;
+                        const int pu = kv ? p.vpu : p.kpu, tu = kv ? p.vtu : p.ktu, none = kv ? p.v_none : p.k_none;
+                        const int head = pc.kvh * (kv ? p.vhu : p.khu);
+                        auto row = [&](int id) { return id < 0 ? none : (id >> 6) * pu + (id & 63) * tu + head; };
+                        const int4 r = make_int4(row(ids.x), row(ids.y), row(ids.z), row(ids.w));
+                        if (copier == 0 && elect_one()) mbar_arrive_expect_tx(bar, stage_bytes<DH>());
+                        // (eight groups at a time, so that their operands are fetched together)
+                        for (int g0 = copier; g0 < 32; g0 += 8 * copiers) {
+                            int4 rg[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            for (int r0 = copier * kKeys; r0 < 32; r0 += copiers * kKeys) {
-                                const int id = __shfl_sync(0xFFFFFFFFu, ids[j], r0 + sub);
-                                const int r = j * 32 + r0 + sub;
-                                const bool on = in && id >= 0;
-                                cp_async16(dst + (ch >> 3) * kTile * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                                           on ? src + (id >> 6) * ps + (id & 63) * ts : src, on ? 16 : 0);
+                            for (int j = 0; j < 8; ++j) {
+                                const int g = (g0 + j * copiers) & 31;
+                                rg[j] = make_int4(__shfl_sync(0xFFFFFFFFu, r.x, g), __shfl_sync(0xFFFFFFFFu, r.y, g),
+                                                  __shfl_sync(0xFFFFFFFFu, r.z, g), __shfl_sync(0xFFFFFFFFu, r.w, g));
+                            }
+                            if (elect_one()) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int g = g0 + j * copiers;
+                                    if (g < 32)
+#pragma unroll
+                                        for (int h = 0; h < DH; ++h)
+                                            tma_gather4(dst + h * kTile * 128 + g * 512, map, h * 64, rg[j], bar);
+                                }
                             }
                         }
-                        cp_async_arrive(bar);
                     } else if (elect_one()) {
                         const CUtensorMap* map = kv ? &vmap : &kmap;
                         mbar_arrive_expect_tx(bar, stage_bytes<DH>());
@@ -810,36 +857,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     }
                     ++issued;
                     at.next(p.nst);
-                    if (i == 0 && kv == 0 && copier == 0) {
-                        // Q of the piece, behind its first key tile: the buffer is free once the products of
-                        // the piece before last (or the last, with one buffer) are done.
-                        const int b = npiece % p.nqb;
-                        const uint32_t ph = (npiece / p.nqb) & 1;
-#pragma unroll
-                        for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
-                            const int to = kPaired ? x : slot;
-                            ok = ok && warp_wait(&sh.qempty[to][b], ph ^ 1, abort, p.status);
-                            if (ok && lane == 0) {
-                                // The piece's record; its readers see it through this barrier.
-                                Piece w = pc;
-                                if (kPaired) {
-                                    w.row0 = pc.row0 + x * rps;
-                                    w.nrows = max(0, min(rps, p.rows - w.row0));
-                                }
-                                sh.piece[to][npiece % kPieces] = w;
-                                uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
-                                constexpr int kCopies = kNarrow ? 4 : 1;
-                                mbar_arrive_expect_tx(&sh.qfull[to][b], kCopies * DH * 128 * p.group * rps);
-#pragma unroll
-                                for (int h = 0; h < DH * kCopies; ++h)
-                                    tma_load_3d(qdst + h / kCopies * p.q_half + h % kCopies * 32 * 128, &qmap,
-                                                h / kCopies * 64, pc.kvh * p.group, pc.row0 + (kPaired ? x * rps : 0),
-                                                &sh.qfull[to][b]);
-                            }
-                        }
-                        ++npiece;
-                        if (!ok) break;
-                    }
+                    // Q behind its first key tile
+                    if (i == 0 && kv == 0 && lead && !(ok = load_q(pc))) break;
                 }
             }
             t += pc.ntiles;
@@ -854,9 +873,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         if (!ok) {
             // The copies in flight land before the CTA exits.
             const unsigned long long deadline = globaltimer() + kWaitLimitNs;
-            if (kSelected) asm volatile("cp.async.wait_all;" ::: "memory");
             const int64_t first = issued > p.nst ? issued - p.nst : 0;
-            for (int64_t i = first; i < issued && !kSelected; ++i)
+            for (int64_t i = first; i < issued; ++i)
                 if (!mbar_drain(&sh.full[rs][i % p.nst], (i / p.nst) & 1, deadline, p.status)) break;
             for (int x = 0; x < (kPaired ? 2 : 1); ++x)
                 for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece; ++i)
@@ -887,7 +905,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 ok = warp_wait(&sh.full[rs][at.st], at.ph, abort, p.status);
                 if (!ok) break;
                 if (elect_one()) {
-                    if (kSelected) fence_proxy_async_smem();           // the keys were written by plain copies
                     tc_fence_after();
                     const uint64_t qd = desc_sw128(qa);
                     const uint64_t kd = desc_sw128(smem_u32(ring + at.st * stage_bytes<DH>()));
@@ -946,7 +963,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     ph_of ^= 1;
                 }
                 if (elect_one()) {
-                    if (kSelected) fence_proxy_async_smem();
                     tc_fence_after();
                     const uint64_t vd = desc_mn_sw128(smem_u32(va), kTile * 128);
 #pragma unroll
@@ -1575,6 +1591,36 @@ static int page_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t
                : DSA_ERR_CUDA;
 }
 
+static int64_t gcd64(int64_t a, int64_t b) {
+    while (b) {
+        const int64_t t = a % b;
+        a = b;
+        b = t;
+    }
+    return a;
+}
+
+// A pool as rows of dim columns that start every `unit` elements, the unit a
+// common divisor of its strides, so that every (page, token, head) is one row.
+static int row_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t ps, int64_t ts, int64_t hs, int* pu,
+                   int* tu, int* hu, int* none) {
+    if (!fix_stride(ps, c->num_pages, 0) || !fix_stride(ts, kPage, 0) || !fix_stride(hs, c->heads, 0))
+        return DSA_ERR_UNSUPPORTED;
+    int64_t unit = gcd64(gcd64(ps, ts), hs);
+    if (unit == 0) unit = c->dim;
+    const int64_t n = ((c->num_pages - 1) * ps + (kPage - 1) * ts + (c->heads - 1) * hs) / unit + 1;
+    if (n > 0x7FFFFF00) return DSA_ERR_UNSUPPORTED;
+    *pu = static_cast<int>(ps / unit), *tu = static_cast<int>(ts / unit), *hu = static_cast<int>(hs / unit);
+    *none = static_cast<int>(n);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->dim), static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(unit) * 2};
+    const cuuint32_t box[2] = {64, 1};
+    return encode_tiled(map, map_type(c->dtype), 2, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+                   CUDA_SUCCESS
+               ? DSA_OK
+               : DSA_ERR_CUDA;
+}
+
 constexpr int kSmemMost = 232448;   // 227 KB
 
 // Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
@@ -1667,9 +1713,7 @@ static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
     const int sms = device_sm_count();
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.workers = 2 * a.ctas;
-    p.kbase = static_cast<const uint16_t*>(c->k);
     p.vbase = static_cast<const uint16_t*>(c->v);
-    p.kp = c->k_page_stride, p.kt = c->k_token_stride, p.kh = c->k_head_stride;
     p.vp = c->v_page_stride, p.vt = c->v_token_stride, p.vh = c->v_head_stride;
 }
 
@@ -1774,7 +1818,13 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
     p.scale_log2 = scale * kLog2e;
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
     rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, 1);
-    a.k = a.v = a.q;   // (keys are copied from the pools, not through maps)
+    const dsa_kv_cache c = mapped_cache(cache, workspace);
+    if (rc == DSA_OK)
+        rc = row_map(&a.k, &c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride, &p.kpu, &p.ktu, &p.khu,
+                     &p.k_none);
+    if (rc == DSA_OK)
+        rc = row_map(&a.v, &c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride, &p.vpu, &p.vtu, &p.vhu,
+                     &p.v_none);
     if (rc != DSA_OK) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (launch_pdl(attend_list_kernel, dim3(static_cast<unsigned>(rows)), dim3(kListThreads), 0, stream, p) !=

@@ -200,6 +200,15 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
 }
+// Four rows r (a 2D map whose box is one row high) at column c; rows outside
+// the map arrive as zeros.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int c, int4 r, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
+        : "memory");
+}
 // Plain bulk copy global -> shared (both 16-byte aligned, size a multiple of 16).
 // Per-thread asynchronous global -> shared copies (completion tracked per
 // thread by commit/wait groups; bytes past src_bytes are zero-filled and not
