@@ -34,7 +34,8 @@ int device_sm_count();
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
 CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* addr,
                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                      CUtensorMapSwizzle swizzle);
+                      CUtensorMapSwizzle swizzle,
+                      CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Launch with programmatic stream serialization (the kernel may start while
 // the previous kernel on the stream finishes; it must call griddepcontrol.wait

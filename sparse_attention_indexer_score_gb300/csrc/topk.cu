@@ -561,7 +561,7 @@ int device_sm_count() {
 
 CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* addr,
                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                      CUtensorMapSwizzle swizzle) {
+                      CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
     using Fn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -578,7 +578,7 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t ran
     if (!fn) return CUDA_ERROR_NOT_FOUND;
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return fn(map, type, rank, addr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 int launch_select(const float* logits, float* logits_fill, int64_t ld, int64_t width, const int32_t* ends,
