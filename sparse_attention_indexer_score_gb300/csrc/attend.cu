@@ -121,7 +121,10 @@ struct AttParams {
 
 // ----------------------------------------------------------------- the axis
 // Worker w of W takes tiles [w T / W, (w + 1) T / W).
-__host__ __device__ __forceinline__ int64_t share_start(int64_t w, int64_t T, int64_t W) { return w * T / W; }
+__device__ __forceinline__ int64_t share_start(int64_t w, int64_t T, int64_t W) {
+    if ((w + 1) * T < (int64_t(1) << 32)) return static_cast<uint32_t>(w * T) / static_cast<uint32_t>(W);
+    return w * T / W;
+}
 __device__ __forceinline__ int worker_of(int64_t t, int64_t T, int64_t W) {
     if (T * W < (int64_t(1) << 32))   // (a 64-bit division takes about five times the instructions)
         return static_cast<int>((static_cast<uint32_t>(t + 1) * static_cast<uint32_t>(W) - 1) / static_cast<uint32_t>(T));
@@ -252,17 +255,12 @@ __device__ int64_t lay_out(const AttParams& p, const Axis& ax, int64_t* tmp, int
 template <bool kSelected>
 __device__ int64_t lay_out_few(const AttParams& p, const Axis& ax, int* bounds, int64_t* result, bool write,
                                int* segs) {
-    constexpr int kChunks = kPlanSegs / 32;
     const int lane = threadIdx.x & 31;
     const bool first = threadIdx.x < 32;
-    int a[kChunks], b[kChunks];
-    if (!kSelected && first) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int q = i * 32 + lane;
-            a[i] = q < p.R ? p.starts[q] : 0;
-            b[i] = q < p.R ? p.starts[q + 1] : 0;
-        }
+    int a_next = 0, b_next = 0;
+    if (!kSelected && first && lane < p.R) {
+        a_next = p.starts[lane];
+        b_next = p.starts[lane + 1];
     }
     for (int r = threadIdx.x; r < p.rows; r += blockDim.x) bounds[r] = kSelected ? p.count[r] : p.row_ends[r];
     if (!kSelected && write)
@@ -282,11 +280,16 @@ __device__ int64_t lay_out_few(const AttParams& p, const Axis& ax, int* bounds, 
                 ax.minb[i] = p.prefix_len;
             }
             S = p.px_segs;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                if (i * 32 >= p.R) break;
-                if (a[i] < 0 || b[i] < a[i] || b[i] > p.rows) bad = true;
-                const int s0 = min(max(a[i], 0), p.rows), s1 = min(max(b[i], s0), p.rows);
+#pragma unroll 1
+            for (int base = 0; base < p.R; base += 32) {
+                const int a = a_next, b = b_next, q = base + 32 + lane;
+                a_next = b_next = 0;
+                if (q < p.R) {
+                    a_next = p.starts[q];
+                    b_next = p.starts[q + 1];
+                }
+                if (a < 0 || b < a || b > p.rows) bad = true;
+                const int s0 = min(max(a, 0), p.rows), s1 = min(max(b, s0), p.rows);
                 const int nseg = (s1 - s0 + p.own_rps - 1) / p.own_rps;
                 int inc = nseg;
 #pragma unroll
@@ -308,7 +311,7 @@ __device__ int64_t lay_out_few(const AttParams& p, const Axis& ax, int* bounds, 
                         most = max(most, e);
                         least = min(least, e);
                     }
-                    ax.seg[at + j] = make_int4(row0, nr, i * 32 + lane, most);
+                    ax.seg[at + j] = make_int4(row0, nr, base + lane, most);
                     ax.minb[at + j] = least;
                 }
                 S = min(S + __shfl_sync(0xFFFFFFFFu, inc, 31), p.max_segs);
@@ -316,6 +319,7 @@ __device__ int64_t lay_out_few(const AttParams& p, const Axis& ax, int* bounds, 
         }
         __syncwarp();
         int64_t carry = 0;
+#pragma unroll 1
         for (int base = 0; base < S; base += 32) {
             const int i = base + lane;
             const int4 rec = i < S ? ax.seg[i] : make_int4(0, 0, 0, 0);
