@@ -25,7 +25,8 @@ constexpr int kTile = 128;          // keys per tile: two pages, or 128 listed k
 constexpr int kMaxCtas = 192;       // workspace and tables are sized for at most this many CTAs
 constexpr int kMaxWorkers = 2 * kMaxCtas;
 constexpr int kMaxStages = 10;
-constexpr int kPieces = 4;          // piece records in flight per slot: two with Q buffers, one in use, one being read out
+constexpr int kQBuffers = 1;        // Q tiles in flight per slot
+constexpr int kPieces = 4;          // piece records in flight per slot: ahead, in use, being read out
 constexpr int kPlanThreads = 512;
 constexpr int kListThreads = 256;
 constexpr int kPrefixSmem = 2048;
@@ -112,7 +113,7 @@ struct AttParams {
     int px_segs;                           // mode 1: the prefix's segments, first on the axis
     int rps, rows_cap;                     // query rows and tile rows (group * rps) of a tile
     int own_rps, own_cap;                  // the same of a request's segments
-    int q_half, nqb, nst;                  // Q bytes per 64 columns, Q buffers and ring stages per slot
+    int q_half, nst;                       // Q bytes per 64 columns and ring stages per slot
     int max_segs, workers;                 // workers: 2 per CTA of the axis' kernel
     int plan_in_cta;                       // every CTA lays out the axis, no plan kernel
     int x_rps, x_pairs, x_workers, x_cap;  // prefix: query rows per row tile, pairs of them, paired workers, tile rows
@@ -586,16 +587,20 @@ struct AxisShared {
 // slot, or 4 where tiles are narrow (and 4 more a slot that copy listed keys).
 template <bool kSelected, bool kNarrow>
 __host__ __device__ constexpr int att_threads() { return kNarrow && !kSelected ? 384 : 640; }
+// Rows up to which a tile is narrow.  (17 to 32 rows: four copies of 32 rows were
+// slower than wide tiles, 488 against 471 us for 128 requests of 1 to 4 rows of
+// eight heads, since the copies' join at a piece's end grows with the rows.)
+constexpr int kNarrowRows = 16;
 // Narrow: the part of a strip's outputs that is joined at a time, 8 rows of 64
-// columns, 16 of 32 or 32 of 16, each row padded by four floats.
-constexpr int kMergeFloats = 640;
+// columns or 16 of 32, each row padded by four floats.
+constexpr int kMergeFloats = 576;
 constexpr int kMergeBytes = 4 * kMergeFloats * 4;    // four strips, one slot
 
 // One CTA runs two slots, each a pipeline of its own: a producer warp (TMA), an
 // MMA warp and softmax warps, a thread per tile row (the lanes of tensor memory).
 //
 // Wide tiles (up to 128 rows): two threads share a row, half of the tile's keys
-// each, and agree on its reference.  Narrow tiles (up to 32 rows, the usual
+// each, and agree on its reference.  Narrow tiles (up to 16 rows, the usual
 // decode): the rows are laid four times into the 128 tile rows, one copy to each
 // warp of the slot; copy j weighs only keys 32j .. 32j + 31 of a tile (its other
 // weights are zero) and keeps its own reference, so the softmax of a tile, which
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     // (a shuffled value is uniform to the compiler, and what follows from it stays in uniform registers)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int q_bytes = DH * p.q_half;                                  // one Q buffer
-    uint8_t* const ring0 = smem + 2 * p.nqb * q_bytes;
+    uint8_t* const ring0 = smem + 2 * kQBuffers * q_bytes;
     const int rings = kPaired ? 1 : 2;
     uint8_t* const merge_buf = ring0 + rings * p.nst * stage_bytes<DH>();
     AttShared& sh = *reinterpret_cast<AttShared*>(merge_buf + (kNarrow ? 2 * kMergeBytes : 0));
@@ -705,6 +710,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         int64_t issued = 0;
         int npiece = 0;
         bool ok = true;
+        const uint64_t once = l2_evict_first_policy();
         int s = !works || kPaired ? 0 : p.plan_in_cta ? segment_of(axis.prefix, S, t0) : p.worker[worker];
         int sb = -64;                                                   // first of 32 segments held by the lanes
         int4 rec = {0, 0, 0, 0};
@@ -713,8 +719,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         int64_t t = t0;
         // Q of a piece: the buffer is free once the products of the piece that had it are done.
         auto load_q = [&](const Piece& pc) {
-            const int b = npiece % p.nqb;
-            const uint32_t ph = (npiece / p.nqb) & 1;
+            const int b = npiece % kQBuffers;
+            const uint32_t ph = (npiece / kQBuffers) & 1;
             bool got = true;
 #pragma unroll
             for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                         w.nrows = max(0, min(rps, p.rows - w.row0));
                     }
                     sh.piece[to][npiece % kPieces] = w;
-                    uint8_t* qdst = smem + (to * p.nqb + b) * q_bytes;
+                    uint8_t* qdst = smem + (to * kQBuffers + b) * q_bytes;
                     constexpr int kCopies = kNarrow ? 4 : 1;
                     mbar_arrive_expect_tx(&sh.qfull[to][b], kCopies * DH * 128 * p.group * rps);
 #pragma unroll
@@ -872,8 +878,16 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                         mbar_arrive_expect_tx(bar, stage_bytes<DH>());
 #pragma unroll
                         for (int h = 0; h < DH; ++h) {
-                            tma_load_4d(dst + h * kTile * 128, map, h * 64, 0, pc.kvh, pg0, bar);
-                            tma_load_4d(dst + h * kTile * 128 + kPage * 128, map, h * 64, 0, pc.kvh, pg1, bar);
+                            // (a request's keys are read once: they leave L2 first, before the partial results;
+                            // 128 requests behind a prefix 496 -> 488 us)
+                            uint8_t *d0 = dst + h * kTile * 128, *d1 = d0 + kPage * 128;
+                            if (!kPaired && pc.req >= 0) {
+                                tma_load_4d_hint(d0, map, h * 64, 0, pc.kvh, pg0, bar, once);
+                                tma_load_4d_hint(d1, map, h * 64, 0, pc.kvh, pg1, bar, once);
+                            } else {
+                                tma_load_4d(d0, map, h * 64, 0, pc.kvh, pg0, bar);
+                                tma_load_4d(d1, map, h * 64, 0, pc.kvh, pg1, bar);
+                            }
                         }
                     }
                     ++issued;
@@ -889,8 +903,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             ok = warp_wait(&sh.empty[rs][i % p.nst], (i / p.nst) & 1, abort, p.status);
         // (only the warp that loads Q counts pieces)
         for (int x = 0; x < (kPaired ? 2 : 1); ++x)
-            for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece && ok; ++i)
-                ok = warp_wait(&sh.qempty[kPaired ? x : slot][i % p.nqb], (i / p.nqb) & 1, abort, p.status);
+            for (int i = npiece > kQBuffers ? npiece - kQBuffers : 0; i < npiece && ok; ++i)
+                ok = warp_wait(&sh.qempty[kPaired ? x : slot][i % kQBuffers], (i / kQBuffers) & 1, abort, p.status);
         if (!ok) {
             // The copies in flight land before the CTA exits.
             const unsigned long long deadline = globaltimer() + kWaitLimitNs;
@@ -898,10 +912,10 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             for (int64_t i = first; i < issued; ++i)
                 if (!mbar_drain(&sh.full[rs][i % p.nst], (i / p.nst) & 1, deadline, p.status)) break;
             for (int x = 0; x < (kPaired ? 2 : 1); ++x)
-                for (int i = npiece > p.nqb ? npiece - p.nqb : 0; i < npiece; ++i)
+                for (int i = npiece > kQBuffers ? npiece - kQBuffers : 0; i < npiece; ++i)
                     // (a buffer whose copy was not issued after a failed wait is one phase behind: already past)
-                    if (mbar_test_wait(&sh.qempty[kPaired ? x : slot][i % p.nqb], ((i / p.nqb) & 1) ^ 1))
-                        mbar_drain(&sh.qfull[kPaired ? x : slot][i % p.nqb], (i / p.nqb) & 1, deadline, p.status);
+                    if (mbar_test_wait(&sh.qempty[kPaired ? x : slot][i % kQBuffers], ((i / kQBuffers) & 1) ^ 1))
+                        mbar_drain(&sh.qfull[kPaired ? x : slot][i % kQBuffers], (i / kQBuffers) & 1, deadline, p.status);
         }
     } else if (warp < 4) {
         // ------------------------------------------------- MMA issuer
@@ -918,13 +932,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         bool ok = true, any = false;
         int64_t t = t0;
         while (t < t1 && ok) {
-            const int b = npiece % p.nqb;
-            ok = warp_wait(&sh.qfull[slot][b], (npiece / p.nqb) & 1, abort, p.status);
+            const int b = npiece % kQBuffers;
+            ok = warp_wait(&sh.qfull[slot][b], (npiece / kQBuffers) & 1, abort, p.status);
             if (!ok) break;
             any = true;
             Piece& pc = sh.piece[slot][npiece % kPieces];
             const int ntiles = pc.ntiles, tile0 = pc.tile0, keys = pc.keys, minb = pc.minb;
-            const uint64_t qd = desc_sw128(smem_u32(smem + (slot * p.nqb + b) * q_bytes));
+            const uint64_t qd = desc_sw128(smem_u32(smem + (slot * kQBuffers + b) * q_bytes));
             // A step is a tile (narrow), or half of one (wide, the last tile's second half only where it has keys).
             constexpr int kStep = kNarrow ? 1 : 2;
             const int steps = kNarrow ? ntiles : (min(keys - tile0 * kTile, ntiles * kTile) + 63) / 64;
@@ -1032,7 +1046,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         // ------------------------------------------------- softmax, narrow: 32 keys of a row per thread
         const int mi = lane / p.group;                                  // query row of the piece
         // the join at a piece's end: rows the buffer is laid out for, this thread's row there and its first column
-        const int mrows = p.rows_cap <= 8 ? 8 : p.rows_cap <= 16 ? 16 : 32;
+        const int mrows = p.rows_cap <= 8 ? 8 : kNarrowRows;
         const int r = (quarter * 32 + lane) & (mrows - 1), col4 = (quarter * 32 + lane) / mrows * 4;
         const int ri = r / p.group, rg = r - ri * p.group, mcols = 512 / mrows;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -1696,7 +1710,6 @@ constexpr int kSmemMost = 232448;   // 227 KB
 // Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
 static int fit_shared(int halves, bool paired, bool narrow, AttParams& p) {
     p.q_half = narrow ? 128 * 128 : (p.rows_cap * 128 + 1023) / 1024 * 1024;
-    p.nqb = 1;
     const int stage = halves * kTile * 128;
     const int fixed = 2 * halves * p.q_half + (narrow ? 2 * kMergeBytes : 0) + kAttMeta +
                       (p.plan_in_cta && !paired ? static_cast<int>(sizeof(AxisShared)) : 0);
@@ -1753,7 +1766,7 @@ static int launch_axis(AttCall& a, int dtype, cudaStream_t stream) {
     if (!p.plan_in_cta && launch_pdl(attend_plan_kernel<kSelected>, dim3(1), dim3(kPlanThreads), 0, stream, p) !=
                               cudaSuccess)
         return DSA_ERR_CUDA;
-    const int rc = p.rows_cap <= 32 ? launch_attention<false, kSelected, true>(a, dtype, stream)
+    const int rc = p.rows_cap <= kNarrowRows ? launch_attention<false, kSelected, true>(a, dtype, stream)
                                     : launch_attention<false, kSelected, false>(a, dtype, stream);
     if (rc != DSA_OK) return rc;
     return dtype == DSA_BF16 ? launch_join<Bf16>(p, stream) : launch_join<Fp16>(p, stream);
