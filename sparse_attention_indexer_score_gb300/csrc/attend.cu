@@ -25,7 +25,6 @@ constexpr int kTile = 128;          // keys per tile: two pages, or 128 listed k
 constexpr int kMaxCtas = 192;       // workspace and tables are sized for at most this many CTAs
 constexpr int kMaxWorkers = 2 * kMaxCtas;
 constexpr int kMaxStages = 10;
-constexpr int kQBuffers = 1;        // Q tiles in flight per slot
 constexpr int kPieces = 4;          // piece records in flight per slot: ahead, in use, being read out
 constexpr int kPlanThreads = 512;
 constexpr int kListThreads = 256;
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(kListThreads) attend_list_kernel(const AttPara
 // ----------------------------------------------------------------- attention
 struct AttShared {
     uint64_t full[2][kMaxStages], empty[2][kMaxStages];
-    uint64_t qfull[2][2], qempty[2][2];
+    uint64_t qfull[2], qempty[2];
     uint64_t sfull[2][2], pfull[2][2];   // per half tile (wide); [0] per tile (narrow)
     uint64_t ofull[2], ofree[2], drain[2];
     uint64_t pvdone[2], xch[2][4];       // wide: products of a half tile; the two warps of 32 rows meet
@@ -618,8 +617,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     // (a shuffled value is uniform to the compiler, and what follows from it stays in uniform registers)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int q_bytes = DH * p.q_half;                                  // one Q buffer
-    uint8_t* const ring0 = smem + 2 * kQBuffers * q_bytes;
+    const int q_bytes = DH * p.q_half;                                  // one slot's Q
+    uint8_t* const ring0 = smem + 2 * q_bytes;
     const int rings = kPaired ? 1 : 2;
     uint8_t* const merge_buf = ring0 + rings * p.nst * stage_bytes<DH>();
     AttShared& sh = *reinterpret_cast<AttShared*>(merge_buf + (kNarrow ? 2 * kMergeBytes : 0));
@@ -638,10 +637,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 mbar_init(&sh.full[s][i], 1);
                 mbar_init(&sh.empty[s][i], kPaired ? 2 : 1);
             }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&sh.qfull[s][i], 1);
-                mbar_init(&sh.qempty[s][i], 1);
-            }
+            mbar_init(&sh.qfull[s], 1);
+            mbar_init(&sh.qempty[s], 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh.sfull[s][i], 2);
                 mbar_init(&sh.pfull[s][i], softmax_warps);
@@ -719,13 +716,12 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         int64_t t = t0;
         // Q of a piece: the buffer is free once the products of the piece that had it are done.
         auto load_q = [&](const Piece& pc) {
-            const int b = npiece % kQBuffers;
-            const uint32_t ph = (npiece / kQBuffers) & 1;
+            const uint32_t ph = npiece & 1;
             bool got = true;
 #pragma unroll
             for (int x = 0; x < (kPaired ? 2 : 1); ++x) {
                 const int to = kPaired ? x : slot;
-                got = got && warp_wait(&sh.qempty[to][b], ph ^ 1, abort, p.status);
+                got = got && warp_wait(&sh.qempty[to], ph ^ 1, abort, p.status);
                 if (got && elect_one()) {
                     // The piece's record; its readers see it through this barrier.
                     Piece w = pc;
@@ -734,13 +730,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                         w.nrows = max(0, min(rps, p.rows - w.row0));
                     }
                     sh.piece[to][npiece % kPieces] = w;
-                    uint8_t* qdst = smem + (to * kQBuffers + b) * q_bytes;
+                    uint8_t* qdst = smem + to * q_bytes;
                     constexpr int kCopies = kNarrow ? 4 : 1;
-                    mbar_arrive_expect_tx(&sh.qfull[to][b], kCopies * DH * 128 * p.group * rps);
+                    mbar_arrive_expect_tx(&sh.qfull[to], kCopies * DH * 128 * p.group * rps);
 #pragma unroll
                     for (int h = 0; h < DH * kCopies; ++h)
                         tma_load_3d(qdst + h / kCopies * p.q_half + h % kCopies * 32 * 128, &qmap, h / kCopies * 64,
-                                    pc.kvh * p.group, pc.row0 + (kPaired ? x * rps : 0), &sh.qfull[to][b]);
+                                    pc.kvh * p.group, pc.row0 + (kPaired ? x * rps : 0), &sh.qfull[to]);
                 }
             }
             ++npiece;
@@ -903,8 +899,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             ok = warp_wait(&sh.empty[rs][i % p.nst], (i / p.nst) & 1, abort, p.status);
         // (only the warp that loads Q counts pieces)
         for (int x = 0; x < (kPaired ? 2 : 1); ++x)
-            for (int i = npiece > kQBuffers ? npiece - kQBuffers : 0; i < npiece && ok; ++i)
-                ok = warp_wait(&sh.qempty[kPaired ? x : slot][i % kQBuffers], (i / kQBuffers) & 1, abort, p.status);
+            if (npiece > 0 && ok)
+                ok = warp_wait(&sh.qempty[kPaired ? x : slot], (npiece - 1) & 1, abort, p.status);
         if (!ok) {
             // The copies in flight land before the CTA exits.
             const unsigned long long deadline = globaltimer() + kWaitLimitNs;
@@ -912,10 +908,9 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             for (int64_t i = first; i < issued; ++i)
                 if (!mbar_drain(&sh.full[rs][i % p.nst], (i / p.nst) & 1, deadline, p.status)) break;
             for (int x = 0; x < (kPaired ? 2 : 1); ++x)
-                for (int i = npiece > kQBuffers ? npiece - kQBuffers : 0; i < npiece; ++i)
-                    // (a buffer whose copy was not issued after a failed wait is one phase behind: already past)
-                    if (mbar_test_wait(&sh.qempty[kPaired ? x : slot][i % kQBuffers], ((i / kQBuffers) & 1) ^ 1))
-                        mbar_drain(&sh.qfull[kPaired ? x : slot][i % kQBuffers], (i / kQBuffers) & 1, deadline, p.status);
+                // (after a failed wait Q was not copied, and its buffer's phase is one behind: already past)
+                if (npiece > 0 && mbar_test_wait(&sh.qempty[kPaired ? x : slot], npiece & 1))
+                    mbar_drain(&sh.qfull[kPaired ? x : slot], (npiece - 1) & 1, deadline, p.status);
         }
     } else if (warp < 4) {
         // ------------------------------------------------- MMA issuer
@@ -932,13 +927,12 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         bool ok = true, any = false;
         int64_t t = t0;
         while (t < t1 && ok) {
-            const int b = npiece % kQBuffers;
-            ok = warp_wait(&sh.qfull[slot][b], (npiece / kQBuffers) & 1, abort, p.status);
+            ok = warp_wait(&sh.qfull[slot], npiece & 1, abort, p.status);
             if (!ok) break;
             any = true;
             Piece& pc = sh.piece[slot][npiece % kPieces];
             const int ntiles = pc.ntiles, tile0 = pc.tile0, keys = pc.keys, minb = pc.minb;
-            const uint64_t qd = desc_sw128(smem_u32(smem + (slot * kQBuffers + b) * q_bytes));
+            const uint64_t qd = desc_sw128(smem_u32(smem + slot * q_bytes));
             // A step is a tile (narrow), or half of one (wide, the last tile's second half only where it has keys).
             constexpr int kStep = kNarrow ? 1 : 2;
             const int steps = kNarrow ? ntiles : (min(keys - tile0 * kTile, ntiles * kTile) + 63) / 64;
@@ -958,7 +952,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     tc_commit(&sh.sfull[slot][h]);
                     mbar_arrive(&sh.sfull[slot][h]);      // passes the piece's record on
                     if (freed) tc_commit(&sh.empty[rs][at_k.st]);
-                    if (last) tc_commit(&sh.qempty[slot][b]);
+                    if (last) tc_commit(&sh.qempty[slot]);
                 }
                 if (freed) {
                     at_k.next(p.nst);
@@ -1472,7 +1466,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
     }
     const bool on = lane * 4 < p.dim;
     // One pass over the pieces of both runs, kAhead at a time, with a running reference.
-    constexpr int kAhead = kWarps == 1 ? 4 : 8;
+    constexpr int kAhead = 4;
     const int all = n[0] + n[1];
     float top = -INFINITY, l = 0.0f;
     float4 o = {0, 0, 0, 0};
@@ -1595,7 +1589,8 @@ static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_
     if (!sizes_ok(rows, num_requests, heads, cache->heads, cache->dim)) return DSA_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !isfinite(scale)) return DSA_ERR_INVALID;
     if (rows == 0) return DSA_OK;
-    if (max_pages > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
+    // (a segment's tiles of all heads are counted in 31 bits)
+    if (max_pages > (int64_t(1) << 24) || (max_pages / 2 + 1) * cache->heads > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     if (!q || !out || !row_ends || !starts || !workspace) return DSA_ERR_INVALID;
     if (max_pages > 0 && num_requests > 0 && (!block_table || bt_stride < max_pages)) return DSA_ERR_INVALID;
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255)) return DSA_ERR_INVALID;
@@ -1823,7 +1818,8 @@ extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_
     if (rc != DSA_OK) return rc;
     if (max_query_len < 0 || prefix_len < 0 || (prefix_len > 0 && (!prefix_pages || cache->num_pages == 0)))
         return DSA_ERR_INVALID;
-    if (prefix_len > (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
+    if (prefix_len > (int64_t(1) << 30) || (prefix_len / kTile + 1) * cache->heads > 0x7FFFFFFF)
+        return DSA_ERR_UNSUPPORTED;
     if (rows == 0) return DSA_OK;
     AttCall a = {};
     a.L = attend_layout(rows, num_requests, heads, cache->heads, cache->dim, max_query_len, 0);
@@ -1884,7 +1880,7 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
                           row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
     if (rc != DSA_OK) return rc;
     if (k < 0 || (k > 0 && rows > 0 && (!topk || topk_stride < k))) return DSA_ERR_INVALID;
-    if (k > (int64_t(1) << 24) || cache->num_pages > (1 << 25)) return DSA_ERR_UNSUPPORTED;
+    if (k > (int64_t(1) << 24) || (k / kTile + 1) * cache->heads > 0x7FFFFFFF || cache->num_pages > (1 << 25)) return DSA_ERR_UNSUPPORTED;
     if (rows == 0) return DSA_OK;
     AttCall a = {};
     // (an empty list is one key long in the workspace: the rows still need their zeros)

@@ -19,7 +19,11 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 
 def empty_cache(pages, heads, dim, dtype, layout, device="cuda", fill=float("nan")):
-    """Pools [pages, 64, heads, dim] in one of three memory orders, full of `fill`."""
+    """Pools [pages, 64, heads, dim] in one of four memory orders, full of `fill`."""
+    if layout == "odd":    # padded tokens and pages: strides whose common divisor is less than a row
+        tok, extra = heads * dim + 8, 24
+        both = [torch.full((pages * (64 * tok + extra),), fill, dtype=DT[dtype], device=device) for _ in range(2)]
+        return [b.as_strided((pages, 64, heads, dim), (64 * tok + extra, tok, dim, 1)) for b in both]
     n = dict(nhd=(pages, 64, heads, dim), hnd=(pages, heads, 64, dim), pair=(pages, 2, 64, heads, dim))[layout]
     if layout == "pair":   # both pools in one tensor, page by page, as merged caches are
         both = torch.full(n, fill, dtype=DT[dtype], device=device)

@@ -61,7 +61,7 @@ def check_append(dsa, q, k, v, slots, kc, vc, pos, cs, inter, want_status=0, **k
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("n,hq,hkv,dim,rot,layout", [
     (1, 8, 2, 128, 128, "nhd"), (3, 32, 8, 128, 64, "hnd"), (77, 5, 5, 80, 32, "pair"), (130, 6, 1, 96, 96, "nhd"),
-    (9, 7, 1, 256, 16, "hnd"), (2, 3, 3, 512, 512, "nhd"), (5, 2, 1, 16, 16, "nhd"), (700, 4, 4, 64, 64, "hnd")])
+    (9, 7, 1, 256, 16, "hnd"), (40, 4, 2, 64, 64, "odd"), (2, 3, 3, 512, 512, "nhd"), (5, 2, 1, 16, 16, "nhd"), (700, 4, 4, 64, 64, "hnd")])
 def test_append(cuda_lib, n, hq, hkv, dim, rot, layout, inter, dtype):
     check_append(cuda_lib, *append_case(n, hq, hkv, dim, rot, dtype, layout, packed=n != 9), inter)
 
@@ -100,8 +100,9 @@ LENS = [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 256, 300]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
-@pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 64), (4, 4, 128), (16, 1, 128), (6, 2, 80), (3, 1, 16)])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "pair", "odd"])
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 64), (4, 4, 128), (16, 1, 128), (6, 2, 80), (3, 1, 16), (40, 2, 96),
+                                        (100, 1, 128)])
 def test_paged_lengths(cuda_lib, hq, hkv, dim, layout, dtype):
     c = Case(LENS, [1] * len(LENS), hq=hq, hkv=hkv, dim=dim, layout=layout, dtype=dtype, pad_rows=2)
     c.check(c.paged(cuda_lib))
@@ -176,7 +177,8 @@ def test_keys_of_other_rows_do_not_leak(cuda_lib):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("k", [1, 7, 128, 129, 300])
-@pytest.mark.parametrize("hq,hkv,dim,layout", [(8, 2, 64, "nhd"), (16, 1, 128, "hnd"), (6, 3, 80, "pair"), (4, 4, 16, "nhd")])
+@pytest.mark.parametrize("hq,hkv,dim,layout", [(8, 2, 64, "nhd"), (16, 1, 128, "hnd"), (6, 3, 80, "pair"), (4, 4, 16, "nhd"),
+                                               (6, 2, 96, "odd"), (40, 2, 64, "nhd"), (128, 1, 128, "hnd")])
 def test_selected(cuda_lib, hq, hkv, dim, layout, k, dtype):
     c = Case([0, 1, 64, 200, 999], [1, 1, 2, 3, 1], hq=hq, hkv=hkv, dim=dim, layout=layout, dtype=dtype, pad_rows=1)
     for holes in (False, True):
@@ -285,11 +287,40 @@ def test_workspace_is_reusable_across_sizes_and_results_repeat(cuda_lib):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+def test_repeated_calls_agree_on_every_bit(cuda_lib):
+    """Nothing depends on the order in which CTAs finish."""
+    c = Case([9000, 5000, 1], [2, 4, 1], prefix=2000, hq=32, hkv=4, dim=128, dtype="fp16")
+    topk = choose(c, 900)
+    first = c.paged(cuda_lib) + c.selected(cuda_lib, topk)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, c.paged(cuda_lib) + c.selected(cuda_lib, topk)))
+
+
 def test_a_workspace_too_small_is_refused(cuda_lib):
     c = Case([90], [1], hq=4, hkv=2, dim=64)
     n = cuda_lib.attend_workspace_size(1, 1, 4, 2, 64, 1)
     with pytest.raises(RuntimeError, match="invalid"):
         c.paged(cuda_lib, workspace=torch.zeros(n - 1, dtype=torch.uint8, device="cuda"))
+
+
+def test_many_requests(cuda_lib):
+    """More segments than a CTA lays out itself, empty ones among them."""
+    lens = [(53 * j) % 301 for j in range(300)]
+    c = Case(lens, [1 + j % 3 if j % 7 else 0 for j in range(300)], hq=4, hkv=2, dim=64, pad_rows=3)
+    rows = range(0, c.q.shape[0], 17)
+    c.check(c.paged(cuda_lib), rows=rows)
+    topk = choose(c, 150)
+    c.check(c.selected(cuda_lib, topk), topk, rows=rows)
+    behind = Case(lens, [1] * 300, prefix=300, hq=4, hkv=2, dim=64, dtype="fp16")
+    behind.check(behind.paged(cuda_lib), rows=rows[:10])
+
+
+def test_a_row_of_many_heads_and_long_queries(cuda_lib):
+    """Requests with more rows than a tile has, bounds that end inside a tile of rows."""
+    c = Case([700, 90, 1500], [130, 3, 260], prefix=33, hq=6, hkv=2, dim=64)
+    c.check(c.paged(cuda_lib), rows=[0, 41, 42, 43, 129, 130, 132, 133, 174, 175, 392])
+    c.qlen = 4
+    c.check(c.paged(cuda_lib), rows=[0, 42, 129, 130, 175, 392])
 
 
 def test_calls_follow_the_current_stream(cuda_lib):
