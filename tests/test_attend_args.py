@@ -158,3 +158,33 @@ def test_the_binding_refuses_other_append_tensors(dsa):
             dsa.kv_append(**bad)
     with pytest.raises(ValueError):
         dsa.kv_append(**dict(good, q=None, q_out=torch.zeros(3, 4, 64, dtype=bf)))
+
+
+def test_the_binding_fails_loudly_without_its_extension(dsa, monkeypatch):
+    import builtins
+    import sys
+
+    monkeypatch.setattr(dsa, "_binding", None)
+    monkeypatch.delitem(sys.modules, "sparse_attention_indexer_score_gb300._dsa_binding", raising=False)
+    package = sys.modules["sparse_attention_indexer_score_gb300"]
+    monkeypatch.delattr(package, "_dsa_binding", raising=False)
+    real = builtins.__import__
+
+    def missing(name, globals=None, locals=None, fromlist=(), level=0):
+        if fromlist and "_dsa_binding" in fromlist:
+            raise ImportError("no _dsa_binding")
+        return real(name, globals, locals, fromlist, level)
+
+    monkeypatch.setattr(builtins, "__import__", missing)
+    with pytest.raises(RuntimeError, match="missing"):
+        dsa.attend_paged(**tensors(), max_query_len=1)
+
+
+def test_the_binding_refuses_cpu_tensors_and_other_numbers(dsa):
+    t = tensors()
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.attend_paged(**t, max_query_len=1, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    for bad in (dict(max_query_len="1"), dict(max_query_len=1, scale="x"), dict(max_query_len=1, prefix_len=None),
+                dict(max_query_len=1, status=torch.zeros(1)), dict(max_query_len=1, q=None)):
+        with pytest.raises(ValueError):
+            dsa.attend_paged(**{**t, **bad})
