@@ -86,6 +86,8 @@ __device__ __forceinline__ void turn_pairs(uint4& x, const float* c, const float
 // walks the token's query, key and value heads in steps of head_lanes.
 template <typename T, bool kInterleaved, bool kStreams>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
     const int per_token = a.units * a.head_lanes;
     const int sub = threadIdx.x / per_token;
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta + sub;
@@ -164,10 +166,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 }
 
 template <typename T>
-static void launch_append(const AppendArgs& a, dim3 grid, bool interleaved, bool streams, cudaStream_t stream) {
+static cudaError_t launch_append(const AppendArgs& a, dim3 grid, bool interleaved, bool streams, cudaStream_t stream) {
     auto* kernel = interleaved ? (streams ? kv_append_kernel<T, true, true> : kv_append_kernel<T, true, false>)
                                : (streams ? kv_append_kernel<T, false, true> : kv_append_kernel<T, false, false>);
-    kernel<<<grid, kAppendThreads, 0, stream>>>(a);
+    return launch_pdl(kernel, grid, dim3(kAppendThreads), 0, stream, a);
 }
 
 int check_kv_cache(const dsa_kv_cache* c) {
@@ -247,9 +249,7 @@ extern "C" int dsa_kv_append(const dsa_kv_cache* cache, const void* k, int64_t k
     if (blocks > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (cache->dtype == DSA_BF16)
-        launch_append<Bf16>(a, grid, interleaved, streams, stream);
-    else
-        launch_append<Fp16>(a, grid, interleaved, streams, stream);
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    const cudaError_t err = cache->dtype == DSA_BF16 ? launch_append<Bf16>(a, grid, interleaved, streams, stream)
+                                                     : launch_append<Fp16>(a, grid, interleaved, streams, stream);
+    return err == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
