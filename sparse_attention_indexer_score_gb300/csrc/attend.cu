@@ -1419,17 +1419,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + (kWarps == 1 ? warp : 0);
-    if (item >= static_cast<int64_t>(p.rows) * p.heads) return;
-    const int row = static_cast<int>(item / p.heads), head = static_cast<int>(item % p.heads);
-    const int kvh = head / p.group, g = head - kvh * p.group;
+    // (the items fit 31 bits; 64-bit divisions here were most of the kernel's instructions)
+    const uint32_t item = blockIdx.x * kItems + (kWarps == 1 ? warp : 0), heads = p.heads;
+    if (item >= static_cast<uint32_t>(p.rows) * heads) return;
+    const int row = item / heads, head = item - row * heads;
+    const int kvh = static_cast<uint32_t>(head) / static_cast<uint32_t>(p.group), g = head - kvh * p.group;
     const RowInfo ri = p.row_info[row];
     const int64_t T_all = p.info[0];
     // two runs of pieces: the row's own keys and the prefix
-    const float2* ml[2] = {nullptr, nullptr};
-    const float* po[2] = {nullptr, nullptr};
-    int step[2] = {p.own_cap, p.x_cap};   // tile rows from one piece to the next
-    int n[2] = {0, 0};
+    const float2 *ml0 = nullptr, *ml1 = nullptr;
+    const float *po0 = nullptr, *po1 = nullptr;
+    int n0 = 0, n1 = 0, step1 = p.x_cap;   // pieces; tile rows from one of the prefix's to the next
     if (ri.seg >= 0) {
         const int64_t W = p.workers < T_all ? p.workers : T_all;
         if (ri.tph > 0) {
@@ -1437,37 +1437,38 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
             const int wa = worker_of(first, T_all, W), wb = worker_of(first + ri.tph - 1, T_all, W);
             const int64_t at =
                 (static_cast<int64_t>(ri.seg) * p.kv_heads + kvh + wa) * p.own_cap + (row - ri.row0) * p.group + g;
-            ml[0] = p.pml + at;
-            po[0] = p.po + at * p.dim;
-            n[0] = wb - wa + 1;
-            if (p.prefix_mode == 0 && n[0] == 1) return;   // written by the attention kernel
+            ml0 = p.pml + at;
+            po0 = p.po + at * p.dim;
+            n0 = wb - wa + 1;
+            if (p.prefix_mode == 0 && n0 == 1) return;   // written by the attention kernel
         }
         if (p.prefix_mode != 0) {
             const int tph = tiles_of(p.prefix_len);
-            const int tile = row / p.x_rps, in = row - tile * p.x_rps;   // row tile of 128 rows
+            const int tile = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.x_rps);   // row tile
+            const int in = row - tile * p.x_rps;
             int64_t at;
             if (p.prefix_mode == 1) {
                 const int64_t it = static_cast<int64_t>(tile) * p.kv_heads + kvh;
                 const int wa = worker_of(it * tph, T_all, W), wb = worker_of(it * tph + tph - 1, T_all, W);
                 at = (it + wa) * p.x_cap + in * p.group + g;
-                n[1] = wb - wa + 1;
+                n1 = wb - wa + 1;
             } else {
                 const int64_t T_x = static_cast<int64_t>(p.x_pairs) * p.kv_heads * tph;
                 const int64_t W_x = p.x_workers < T_x ? p.x_workers : T_x;
                 const int64_t it = static_cast<int64_t>(kvh) * p.x_pairs + tile / 2;
                 const int wa = worker_of(it * tph, T_x, W_x), wb = worker_of(it * tph + tph - 1, T_x, W_x);
                 at = ((it + wa) * 2 + tile % 2) * 128 + in * p.group + g;
-                step[1] = 256;
-                n[1] = wb - wa + 1;
+                step1 = 256;
+                n1 = wb - wa + 1;
             }
-            ml[1] = p.xml + at;
-            po[1] = p.xo + at * p.dim;
+            ml1 = p.xml + at;
+            po1 = p.xo + at * p.dim;
         }
     }
     const bool on = lane * 4 < p.dim;
     // One pass over the pieces of both runs, kAhead at a time, with a running reference.
     constexpr int kAhead = 4;
-    const int all = n[0] + n[1];
+    const int all = n0 + n1;
     float top = -INFINITY, l = 0.0f;
     float4 o = {0, 0, 0, 0};
     for (int base = kWarps == 1 ? 0 : warp; base < all; base += kAhead * kWarps) {
@@ -1476,13 +1477,13 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_join_k
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = base + j * kWarps;
-            const int x = i < n[0] ? 0 : 1;
-            const int64_t at = static_cast<int64_t>(i - (x ? n[0] : 0)) * step[x];
+            const bool own = i < n0;
+            const int at = own ? i * p.own_cap : (i - n0) * step1;   // (at most kMaxWorkers * 256)
             e[j] = make_float2(-INFINITY, 0.0f);
             v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (i < all) {
-                e[j] = ml[x][at];
-                if (on) v[j] = *reinterpret_cast<const float4*>(po[x] + at * p.dim + lane * 4);
+                e[j] = (own ? ml0 : ml1)[at];
+                if (on) v[j] = *reinterpret_cast<const float4*>((own ? po0 : po1) + at * p.dim + lane * 4);
             }
         }
         float m = top;
@@ -1586,7 +1587,8 @@ static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_
     if (rc != DSA_OK) return rc;
     if (heads < 1 || rows < 0 || num_requests < 0 || max_pages < 0) return DSA_ERR_INVALID;
     if (heads % cache->heads) return DSA_ERR_INVALID;
-    if (!sizes_ok(rows, num_requests, heads, cache->heads, cache->dim)) return DSA_ERR_UNSUPPORTED;
+    if (!sizes_ok(rows, num_requests, heads, cache->heads, cache->dim) || rows * heads > 0x7FFFFFFF)
+        return DSA_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !isfinite(scale)) return DSA_ERR_INVALID;
     if (rows == 0) return DSA_OK;
     // (a segment's tiles of all heads are counted in 31 bits)
@@ -1744,7 +1746,6 @@ static int launch_attention(AttCall& a, int dtype, cudaStream_t stream) {
 template <typename T>
 static int launch_join(const AttParams& p, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
-    if (items > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     // few rows: their many pieces are shared by the warps of a CTA
     const cudaError_t e = static_cast<int64_t>(p.rows) * p.kv_heads * 4 <= p.workers
                               ? launch_pdl(attend_join_kernel<T, 8>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
