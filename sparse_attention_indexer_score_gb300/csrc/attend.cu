@@ -1746,8 +1746,9 @@ static int launch_attention(AttCall& a, int dtype, cudaStream_t stream) {
 template <typename T>
 static int launch_join(const AttParams& p, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
-    // few rows: their many pieces are shared by the warps of a CTA
-    const cudaError_t e = static_cast<int64_t>(p.rows) * p.kv_heads * 4 <= p.workers
+    // Where the workers are many to an item of the axis, its many pieces are shared by the warps of a CTA.
+    const int64_t axis_items = static_cast<int64_t>(p.prefix_mode == 1 ? p.px_segs : p.rows) * p.kv_heads;
+    const cudaError_t e = axis_items * 6 <= p.workers
                               ? launch_pdl(attend_join_kernel<T, 8>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
                                            stream, p)
                               : launch_pdl(attend_join_kernel<T, 1>, dim3(static_cast<unsigned>((items + 3) / 4)),
