@@ -12,11 +12,16 @@
  *   4. dsa_score_paged     paged MQA logits score[t] = sum_h w_h * ReLU(q_h . k_t),
  *                          with the top-k selection fused behind it;
  *   5. dsa_topk            top-k of an existing logits matrix.
+ * Around it, the attention of the layer over a paged 16-bit key/value cache:
+ *   dsa_kv_append          rotates and writes the step's keys and values;
+ *   dsa_attend_paged       attention over all keys, behind a shared prefix;
+ *   dsa_attend_selected    attention over the keys the top-k lists.
  *
  * Conventions for every call:
  *   - Every pointer argument except `stream` is a DEVICE pointer owned by the
  *     caller.  The library allocates no device memory; scratch comes from a
- *     caller workspace sized by dsa_workspace_size / dsa_topk_workspace_size.
+ *     caller workspace sized by dsa_workspace_size / dsa_topk_workspace_size /
+ *     dsa_attend_workspace_size; a workspace serves one call at a time.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Every call
  *     only enqueues work and returns; nothing waits for the GPU.
  *   - Return value: DSA_OK, or a negative DSA_ERR_* code.  Argument checks

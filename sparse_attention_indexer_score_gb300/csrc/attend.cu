@@ -7,11 +7,23 @@
 //   CTAs are joined by their (m, l, O).
 //
 // The keys of all (segment, key head) items lie on one axis of 128-key tiles: a
-// segment is a run of rows that share keys (rows of one request, or all rows
-// behind the prefix, or one row's listed keys).  Every worker (a pipeline slot of
-// a CTA) takes an equal share of the axis, so one long context and many short
-// ones fill the GPU alike; an item that several workers share is joined by a
-// last, small kernel.
+// segment is a run of rows that share keys (rows of one request, or rows behind
+// the prefix, or one row's listed keys).  Every worker (a pipeline slot of a CTA)
+// takes an equal share of the axis, so one long context and many short ones fill
+// the GPU alike; an item that several workers share is joined by a last, small
+// kernel.  Up to 128 segments every CTA lays out the axis itself; for more, a plan
+// kernel does.  Listed keys are first packed into slots, a CTA a row; a large
+// batch's prefix has a launch of its own, in pairs of 128-row tiles.
+//
+// What bounds it: a key and its value are 4 d bytes and cost each row that shares
+// them 4 d flops, one flop a byte, so memory bounds it until some 270 rows share a
+// key; a prefix under hundreds of rows and heads is bound by the tensor cores.  Measured on GB300 (BF16, whole calls,
+// 6.8 TB/s and 1.85 PFLOP/s by copy and matrix product): 64 requests of 4096 to
+// 8192 keys, 32 heads over 8: 242 us, 6.7 TB/s.  64 rows of 2048 listed keys:
+// 97 us, 5.5 TB/s (the kernel alone 87 us).  320 rows of 64 heads over 8 behind
+// 32768 keys: 276 us for the prefix, 1.25 PFLOP/s.  One row of 1000 keys: 11 us, a
+// chain of latencies (4600 cycles to the first scores, 2750 for the join of the
+// strips, then the pieces' join as a launch).
 #include <math.h>
 
 #include "elem16.cuh"
@@ -464,7 +476,7 @@ struct AttShared {
     uint32_t tmem;
 };
 constexpr int kAttMeta = (sizeof(AttShared) + 127) / 128 * 128;
-static_assert(kAttMeta <= 3072, "five stages of 32 KB and two Q tiles leave 3 KB");
+static_assert(kAttMeta <= 3 * 1024, "five stages of 32 KB and two Q tiles leave 3 KB");
 
 template <int DH>
 __host__ __device__ constexpr int stage_bytes() { return DH * kTile * 128; }
@@ -606,10 +618,17 @@ constexpr int kMergeBytes = 4 * kMergeFloats * 4;    // four strips, one slot
 // every product waits for, is a quarter as long and no warp waits for another;
 // the four partial outputs are added at the end of the piece.
 //
-// Independent
-// slots take two shares of the axis, each with its own ring of key and value
+// Independent slots take two shares of the axis, each with its own ring of key and value
 // stages; paired slots take two row tiles of one share and read the same ring
 // (the prefix of a large batch: each key tile is loaded once for 256 rows).
+//
+// Measured choices.  Instructions issued by an elected lane instead of lane 0: the
+// paired prefix of the batch above 340 -> 280 us.  Wide tiles in half-tile steps,
+// the next scores made while the softmax works on these: the whole batch 512 -> 500
+// us (half tiles read Q from shared memory twice as often; full tiles could not be
+// made ahead, since scores and output fill tensor memory).  Narrow tiles: 64
+// requests of 4096 to 8192 keys 278 -> 260 us, 64 rows of 2048 listed keys 125 ->
+// 112, measured with up to 32 rows (kNarrowRows says why 16).
 template <typename T, bool kPaired, bool kSelected, bool kNarrow, int DH>
 __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
     attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
