@@ -41,6 +41,7 @@ constexpr int kPieces = 4;          // piece records in flight per slot: ahead, 
 constexpr int kPlanThreads = 512;
 constexpr int kListThreads = 256;
 constexpr int kPrefixSmem = 2048;
+constexpr int kPairTiles = 12;       // tiles a CTA from which a prefix is taken by pairs of row tiles
 constexpr int kPlanSegs = 128;      // up to this many segments every CTA lays out the axis itself
 constexpr int kPlanRows = 4096;     // ... and up to this many rows
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1766,8 +1767,11 @@ template <typename T>
 static int launch_join(const AttParams& p, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
     // Where the workers are many to an item of the axis, its many pieces are shared by the warps of a CTA.
+    // Eight warps against one: 8 items of the axis 19 and 24 us, 16: 22 and 24, 48: equal, 64: 53 and 51.  A CTA per
+    // row and head costs where they are many: 24 rows of 32 heads behind 2000 keys 22 and 24 us, 32 rows of 64 heads
+    // 41 and 39, 64 rows 53 and 41.
     const int64_t axis_items = static_cast<int64_t>(p.prefix_mode == 1 ? p.px_segs : p.rows) * p.kv_heads;
-    const cudaError_t e = axis_items * 6 <= p.workers
+    const cudaError_t e = axis_items * 6 <= p.workers && items <= 4 * p.workers
                               ? launch_pdl(attend_join_kernel<T, 8>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
                                            stream, p)
                               : launch_pdl(attend_join_kernel<T, 1>, dim3(static_cast<unsigned>((items + 3) / 4)),
@@ -1808,6 +1812,7 @@ static void fill_params(AttCall& a, const dsa_kv_cache* c, uint8_t* ws) {
     p.group = p.heads / p.kv_heads;
     p.own_cap = p.group * p.own_rps;
     p.rps = p.own_rps, p.rows_cap = p.own_cap;
+    // (a plan kernel instead: 16 requests of 500 to 1000 keys 22.5 -> 24.5 us, 128 requests 78 -> 84)
     p.plan_in_cta = p.max_segs <= kPlanSegs && p.R <= kPlanSegs && p.rows <= kPlanRows;
     const int sms = device_sm_count();
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
@@ -1864,8 +1869,11 @@ extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_
         p.x_pairs = (tiles + 1) / 2;
         p.x_workers = a.ctas;
         // Row tiles in pairs read the prefix half as often; single ones share the axis (and the launch).
+        // Pairs against the axis, 64 heads over 8, 128 rows, by the pairs' tiles a CTA: 4: 59 and 49 us, 8:
+        // 67 and 61, 16: 82 and 83, 32: 116 and 129, 64: 178 and 227 (32, 64 and 256 rows, and 64
+        // columns, cross between 8 and 16 too).
         p.prefix_mode = tiles > 1 && static_cast<int64_t>(p.x_pairs) * p.kv_heads * ((prefix_len + kTile - 1) / kTile) >
-                                         2 * a.ctas
+                                         kPairTiles * a.ctas
                             ? 2
                             : 1;
         if (p.prefix_mode == 1) {

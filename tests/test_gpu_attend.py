@@ -127,6 +127,25 @@ def test_many_rows_behind_a_prefix(cuda_lib, hq, hkv, rows, prefix):
     wide.check(wide.paged(cuda_lib), rows=range(0, rows, 11))
 
 
+# (the last row tile without a partner, tiles that are not full, prefixes that end inside a page or with a tile)
+PAIRED = [(128, 1, 65, 7301, 64, "bf16", "nhd"), (64, 2, 81, 12001, 128, "fp16", "hnd"),
+          (48, 16, 100, 7680, 96, "bf16", "pair"), (7, 7, 129, 33793, 16, "fp16", "odd"),
+          (64, 8, 320, 8200, 128, "bf16", "odd")]
+
+
+@pytest.mark.parametrize("hq,hkv,rows,prefix,dim,dtype,layout", PAIRED)
+def test_long_prefix_behind_many_rows(cuda_lib, hq, hkv, rows, prefix, dim, dtype, layout):
+    """So many tiles that the prefix has a launch of its own, in pairs of row tiles."""
+    tiles = -(-rows // (128 // (hq // hkv)))
+    assert (tiles + 1) // 2 * hkv * -(-prefix // 128) > 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [(37 * j) % 150 for j in range(rows)]
+    c = Case(lens, [1] * rows, prefix=prefix, hq=hq, hkv=hkv, dim=dim, dtype=dtype, layout=layout, pad_rows=2, seed=6)
+    got = c.paged(cuda_lib)
+    c.check(got, rows=[0, 1, rows // 2, rows - 2, rows - 1, rows, rows + 1])
+    again = c.paged(cuda_lib)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_paged_long_rows(cuda_lib, dtype):
     """Few rows over long contexts: the keys are split over the GPU and joined."""
