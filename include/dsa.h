@@ -581,7 +581,9 @@ int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_t q_row_str
  * topk[r][0 .. k - 1] of its request (dsa_score_paged's or dsa_topk_merge's
  * output): negative entries are empty and may sit anywhere; an entry at or past
  * row_ends[r] (or the block table's end) is skipped and flagged
- * DSA_STATUS_BAD_GEOMETRY; a position listed twice counts twice.
+ * DSA_STATUS_BAD_GEOMETRY; a position listed twice counts twice.  Pools of more
+ * than 2^25 pages, or of more rows of the strides' common divisor than 31 bits
+ * count, are DSA_ERR_UNSUPPORTED.
  *   topk          int32 [rows][topk_stride >= k].
  */
 int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,

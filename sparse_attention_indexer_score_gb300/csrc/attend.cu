@@ -626,8 +626,9 @@ constexpr int kMergeBytes = 4 * kMergeFloats * 4;    // four strips, one slot
 // Measured choices.  Instructions issued by an elected lane instead of lane 0: the
 // paired prefix of the batch above 340 -> 280 us.  Wide tiles in half-tile steps,
 // the next scores made while the softmax works on these: the whole batch 512 -> 500
-// us (half tiles read Q from shared memory twice as often; full tiles could not be
-// made ahead, since scores and output fill tensor memory).  Narrow tiles: 64
+// us (half tiles read Q from shared memory twice as often, but whole tiles cannot be
+// made ahead, since scores and output fill tensor memory: 334 -> 362 us for 320 rows
+// of 64 heads over 8 behind 32768 keys).  Narrow tiles: 64
 // requests of 4096 to 8192 keys 278 -> 260 us, 64 rows of 2048 listed keys 125 ->
 // 112, measured with up to 32 rows (kNarrowRows says why 16).
 template <typename T, bool kPaired, bool kSelected, bool kNarrow, int DH>
@@ -1724,7 +1725,7 @@ static int row_map(CUtensorMap* map, const dsa_kv_cache* c, void* pool, int64_t 
 
 constexpr int kSmemMost = 232448;   // 227 KB
 
-// Q buffers and ring stages for tiles of `rows` query rows; returns the shared memory taken.
+// Q buffers for tiles of p.rows_cap rows, ring stages in what they leave; returns the shared memory taken.
 static int fit_shared(int halves, bool paired, bool narrow, AttParams& p) {
     p.q_half = narrow ? 128 * 128 : (p.rows_cap * 128 + 1023) / 1024 * 1024;
     const int stage = halves * kTile * 128;
