@@ -470,6 +470,7 @@ struct AttShared {
     uint64_t sfull[2][2], pfull[2][2];   // per half tile (wide); [0] per tile (narrow)
     uint64_t ofull[2], ofree[2], drain[2];
     uint64_t pvdone[2], xch[2][4];       // wide: products of a half tile; the two warps of 32 rows meet
+    uint8_t vote[2][4][2][2];            // ... and what each of them says there, by slot, rows, parity and half
     float half[2][2][128];            // maxima (then sums) of the two halves of each row; narrow: {m, l} of the strips
     uint64_t merge[2];                // narrow: the strips of a piece meet
     Piece piece[2][kPieces];
@@ -546,21 +547,6 @@ __device__ __forceinline__ bool elect_one() {
     return on != 0;
 }
 
-// The two warps that share 32 tile rows meet (a warp that gives up arrives
-// once, so that the other does not wait for it).
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-// The two warps meet; whether any of their threads says so.
-__device__ __forceinline__ bool pair_any(int id, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(static_cast<uint32_t>(v))
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void pair_leave(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
 // Where a role stands on the axis, and the ring position it is at.
 struct Ring {
     int st = 0;
@@ -1252,7 +1238,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         if (quarter >= active) goto done;
         const int m = quarter * 32 + lane;                              // tile row
         const int mi = m / p.group, mg = m - mi * p.group;              // query row of the piece, head of the group
-        const int pair = 1 + slot * 4 + quarter;                        // named barrier of the row's two warps
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t a_s = tmem + lanes + slot * 128, a_o = tmem + lanes + 256 + slot * 128;
         const float c = p.scale_log2;
@@ -1260,12 +1245,22 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         uint32_t steps_done = 0;
         int npiece = 0;
         bool ok = true;
-        auto meet = [&]() {                                             // the row's two warps, bounded
+        // The row's two warps meet; bounded, as every wait is that another role may leave unanswered.
+        auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.xch[slot][quarter]);
             ok = warp_wait(&sh.xch[slot][quarter], ph_x, abort, p.status);
             ph_x ^= 1;
             return ok;
+        };
+        // They meet, and either may say so: 0 nobody did, 1 somebody did, -1 the wait ran out.  (A place by the
+        // parity of the meeting: the other warp has read it before it arrives at the next.)
+        auto meet_any = [&](bool v) {
+            uint8_t* const at = sh.vote[slot][quarter][ph_x];
+            v = __any_sync(0xFFFFFFFFu, v);
+            if (lane == 0) at[half] = v;
+            if (!meet()) return -1;
+            return static_cast<int>(v || *const_cast<volatile uint8_t*>(at + (half ^ 1)));
         };
         int64_t t = t0;
         while (t < t1 && ok) {
@@ -1311,7 +1306,9 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
                     // The two warps meet in any case: both have read their scores, so the weights may take the
                     // scores' columns.  Where a row's reference has to rise, they agree on it.
-                    if (pair_any(pair, mx > m_ref + kSlack)) {
+                    const int raise = meet_any(mx > m_ref + kSlack);
+                    if (raise < 0) break;
+                    if (raise) {
                         sh.half[slot][half][m] = mx;
                         if (!meet()) break;
                         mx = fmaxf(mx, sh.half[slot][half ^ 1][m]);
@@ -1366,7 +1363,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             if (warp_on) {
                 // (the products are done, so both warps are past the last tile's maxima)
                 sh.half[slot][half][m] = l;
-                pair_sync(pair);
+                if (!meet()) break;
                 l = sh.half[slot][0][m] + sh.half[slot][1][m];
                 const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
                 const float ref = m_ref == -INFINITY ? -INFINITY : m_ref - Facts<T>::shift;
@@ -1420,7 +1417,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             t += ntiles;
             ++npiece;
         }
-        if (!ok) pair_leave(pair);
     }
 done:
     tc_fence_before();
