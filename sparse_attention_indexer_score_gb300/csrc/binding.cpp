@@ -10,6 +10,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -34,6 +35,15 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
     return THPVariable_Unpack(o);
 }
 
+// A call's device is its caches'; every other tensor's address goes to kernels there.
+const at::Tensor& tensor(PyObject* o, const at::Device& device, const char* what) {
+    const at::Tensor& t = tensor(o, what);
+    if (t.device() != device)
+        throw BadArgument("every tensor must be on the caches' device (" + device.str() + "), not on " +
+                          t.device().str());
+    return t;
+}
+
 bool given(PyObject* o) { return o != Py_None; }
 
 int64_t whole(PyObject* o) {
@@ -49,17 +59,24 @@ bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
 
 void* pointer(const at::Tensor& t) { return t.data_ptr(); }
 
-int32_t* status_word(PyObject* o) {
+int32_t* status_word(PyObject* o, const at::Device& device) {
     if (!given(o)) return nullptr;
-    const at::Tensor& t = tensor(o, "status must be a tensor");
+    const at::Tensor& t = tensor(o, device, "status must be a tensor");
     need(t.scalar_type() == at::kInt && t.numel() >= 1, "status must be int32");
     return static_cast<int32_t*>(pointer(t));
 }
 
-void* stream_of(const at::Tensor& t) {
-    need(t.is_cuda(), "the caches must be CUDA tensors");
-    return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-}
+// The caches' GPU, current for the call: launches, SM counts and new tensors go by the current device.
+struct OnDevice {
+    c10::cuda::OptionalCUDAGuard guard;
+    void* stream;
+
+    explicit OnDevice(const at::Device& device) {
+        need(device.is_cuda(), "the caches must be CUDA tensors");
+        if (c10::cuda::current_device() != device.index()) guard.set_device(device);
+        stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    }
+};
 
 void check(int rc, const char* call) {
     if (rc == DSA_OK) return;
@@ -69,11 +86,18 @@ void check(int rc, const char* call) {
     throw std::runtime_error(std::string(call) + ": " + what);
 }
 
-dsa_kv_cache cache_of(PyObject* k_cache, PyObject* v_cache, at::ScalarType* type) {
+// The caches, and what every other tensor of the call goes by.
+struct Cache {
+    dsa_kv_cache c;
+    at::ScalarType type;
+    at::Device device;
+};
+
+Cache cache_of(PyObject* k_cache, PyObject* v_cache) {
     const at::Tensor& k = tensor(k_cache, "k_cache must be a tensor");
-    const at::Tensor& v = tensor(v_cache, "v_cache must be a tensor");
-    *type = k.scalar_type();
-    need((*type == at::kBFloat16 || *type == at::kHalf) && v.scalar_type() == *type,
+    const at::Tensor& v = tensor(v_cache, k.device(), "v_cache must be a tensor");
+    const at::ScalarType type = k.scalar_type();
+    need((type == at::kBFloat16 || type == at::kHalf) && v.scalar_type() == type,
          "k_cache and v_cache must both be BF16 or both FP16");
     need(k.dim() == 4 && k.size(1) == DSA_PAGE_TOKENS && v.sizes() == k.sizes(),
          "k_cache and v_cache must be [pages, 64, heads, dim]");
@@ -83,19 +107,19 @@ dsa_kv_cache cache_of(PyObject* k_cache, PyObject* v_cache, at::ScalarType* type
     c.k_page_stride = k.stride(0), c.k_token_stride = k.stride(1), c.k_head_stride = k.stride(2);
     c.v_page_stride = v.stride(0), c.v_token_stride = v.stride(1), c.v_head_stride = v.stride(2);
     c.num_pages = k.size(0), c.heads = k.size(2), c.dim = k.size(3);
-    c.dtype = *type == at::kBFloat16 ? DSA_BF16 : DSA_FP16;
-    return c;
+    c.dtype = type == at::kBFloat16 ? DSA_BF16 : DSA_FP16;
+    return Cache{c, type, k.device()};
 }
 
 // [n, heads, dim] of the cache's type with contiguous columns.
-const at::Tensor& rows_of(PyObject* o, at::ScalarType type, int64_t dim, const char* what) {
-    const at::Tensor& t = tensor(o, what);
-    need(t.scalar_type() == type && t.dim() == 3 && t.size(2) == dim && t.stride(2) == 1, what);
+const at::Tensor& rows_of(PyObject* o, const Cache& cache, const char* what) {
+    const at::Tensor& t = tensor(o, cache.device, what);
+    need(t.scalar_type() == cache.type && t.dim() == 3 && t.size(2) == cache.c.dim && t.stride(2) == 1, what);
     return t;
 }
 
-const at::Tensor& list_of(PyObject* o, at::ScalarType type, int64_t n, const char* what) {
-    const at::Tensor& t = tensor(o, what);
+const at::Tensor& list_of(PyObject* o, const at::Device& device, at::ScalarType type, int64_t n, const char* what) {
+    const at::Tensor& t = tensor(o, device, what);
     need(t.scalar_type() == type && t.dim() == 1 && t.size(0) == n && t.is_contiguous(), what);
     return t;
 }
@@ -103,29 +127,29 @@ const at::Tensor& list_of(PyObject* o, at::ScalarType type, int64_t n, const cha
 // The caller's output tensor, or a new one like q.
 at::Tensor output(PyObject* o, const at::Tensor& q, const char* what) {
     if (!given(o)) return at::empty(q.sizes(), q.options());
-    const at::Tensor& t = tensor(o, what);
+    const at::Tensor& t = tensor(o, q.device(), what);
     need(t.scalar_type() == q.scalar_type() && t.sizes() == q.sizes() && t.stride(2) == 1, what);
     return t;
 }
 
 // k, v, slots, k_cache, v_cache, positions, cos_sin, q, q_out, interleaved, status
 PyObject* kv_append(PyObject* const* a) {
-    at::ScalarType type;
-    const dsa_kv_cache c = cache_of(a[3], a[4], &type);
+    const Cache cache = cache_of(a[3], a[4]);
+    const dsa_kv_cache& c = cache.c;
     constexpr const char* kv = "k and v must be [n, heads, dim] of the cache's type with contiguous columns";
-    const at::Tensor &k = rows_of(a[0], type, c.dim, kv), &v = rows_of(a[1], type, c.dim, kv);
+    const at::Tensor &k = rows_of(a[0], cache, kv), &v = rows_of(a[1], cache, kv);
     need(k.size(1) == c.heads && v.sizes() == k.sizes(), kv);
     const int64_t n = k.size(0);
-    const at::Tensor& slots = list_of(a[2], at::kLong, n, "slots must be contiguous int64 [n], one per key");
+    const at::Tensor& slots = list_of(a[2], cache.device, at::kLong, n, "slots must be contiguous int64 [n], one per key");
     const int64_t* positions = nullptr;
     const float* cos_sin = nullptr;
     int64_t rot = 0, max_pos = 0, cs_stride = 0;
     if (given(a[6])) {
         constexpr const char* angles = "cos_sin must be FP32 [positions, rot] with contiguous rows";
-        const at::Tensor& t = tensor(a[6], angles);
+        const at::Tensor& t = tensor(a[6], cache.device, angles);
         need(t.scalar_type() == at::kFloat && t.dim() == 2 && (t.size(1) == 0 || t.stride(1) == 1), angles);
         positions = static_cast<const int64_t*>(
-            pointer(list_of(a[5], at::kLong, n, "positions must be contiguous int64 [n]")));
+            pointer(list_of(a[5], cache.device, at::kLong, n, "positions must be contiguous int64 [n]")));
         cos_sin = static_cast<const float*>(pointer(t));
         max_pos = t.size(0), rot = t.size(1), cs_stride = t.stride(0);
     }
@@ -135,7 +159,7 @@ PyObject* kv_append(PyObject* const* a) {
     at::Tensor out;
     if (given(a[7])) {
         constexpr const char* qs = "q must be [n, q_heads, dim] of the cache's type with contiguous columns";
-        const at::Tensor& q = rows_of(a[7], type, c.dim, qs);
+        const at::Tensor& q = rows_of(a[7], cache, qs);
         need(q.size(0) == n, qs);
         out = output(a[8], q, "q_out must match q");
         q_heads = q.size(1), qt = q.stride(0), qh = q.stride(1), ot = out.stride(0), oh = out.stride(1);
@@ -143,10 +167,11 @@ PyObject* kv_append(PyObject* const* a) {
     } else {
         need(!given(a[8]), "q_out needs q");
     }
+    int32_t* const status = status_word(a[10], cache.device);
+    const OnDevice on(cache.device);
     check(dsa_kv_append(&c, pointer(k), k.stride(0), k.stride(1), pointer(v), v.stride(0), v.stride(1), q_ptr, qt, qh,
                         q_heads, out_ptr, ot, oh, n, static_cast<const int64_t*>(pointer(slots)), positions, cos_sin,
-                        cs_stride, max_pos, rot, truth(a[9]), status_word(a[10]),
-                        stream_of(THPVariable_Unpack(a[3]))),
+                        cs_stride, max_pos, rot, truth(a[9]), status, on.stream),
           "dsa_kv_append");
     if (!out.defined()) Py_RETURN_NONE;
     if (given(a[8])) {
@@ -158,27 +183,27 @@ PyObject* kv_append(PyObject* const* a) {
 
 // What the two attention calls share: q, k_cache, v_cache, block_table, starts, row_ends.
 struct Attention {
-    dsa_kv_cache c;
+    Cache cache;
+    const dsa_kv_cache& c = cache.c;
     at::Tensor q, out, lse;
     const int32_t *table, *starts, *ends;
     int64_t bt_stride, pages, requests, rows, heads;
     float* lse_ptr = nullptr;
     float scale;
 
-    Attention(PyObject* const* a, PyObject* scale_o, PyObject* out_o, PyObject* want_lse) {
-        at::ScalarType type;
-        c = cache_of(a[1], a[2], &type);
-        q = rows_of(a[0], type, c.dim, "q must be [rows, heads, dim] of the cache's type with contiguous columns");
+    Attention(PyObject* const* a, PyObject* scale_o, PyObject* out_o, PyObject* want_lse)
+        : cache(cache_of(a[1], a[2])) {
+        q = rows_of(a[0], cache, "q must be [rows, heads, dim] of the cache's type with contiguous columns");
         constexpr const char* bt = "block_table must be int32 [requests, pages] with contiguous rows";
-        const at::Tensor& t = tensor(a[3], bt);
+        const at::Tensor& t = tensor(a[3], cache.device, bt);
         need(t.scalar_type() == at::kInt && t.dim() == 2 && (t.numel() == 0 || t.stride(1) == 1), bt);
         requests = t.size(0), pages = t.size(1), bt_stride = t.stride(0);
         rows = q.size(0), heads = q.size(1);
         table = static_cast<const int32_t*>(pointer(t));
         starts = static_cast<const int32_t*>(pointer(list_of(
-            a[4], at::kInt, requests + 1, "starts must be contiguous int32, one entry per request and one more")));
-        ends = static_cast<const int32_t*>(
-            pointer(list_of(a[5], at::kInt, rows, "row_ends must be contiguous int32, one bound per query row")));
+            a[4], cache.device, at::kInt, requests + 1, "starts must be contiguous int32, one entry per request and one more")));
+        ends = static_cast<const int32_t*>(pointer(list_of(
+            a[5], cache.device, at::kInt, rows, "row_ends must be contiguous int32, one bound per query row")));
         scale = given(scale_o) ? static_cast<float>(PyFloat_AsDouble(scale_o))
                                : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.dim)));
         if (PyErr_Occurred()) {
@@ -193,7 +218,11 @@ struct Attention {
     }
 
     at::Tensor workspace(PyObject* o, int64_t max_query_len, int64_t k) const {
-        if (given(o)) return tensor(o, "workspace must be a tensor");
+        if (given(o)) {
+            const at::Tensor& t = tensor(o, cache.device, "workspace must be a tensor");
+            need(t.is_contiguous(), "workspace must be contiguous");
+            return t;
+        }
         const size_t n = dsa_attend_workspace_size(rows, requests, heads, c.heads, c.dim, max_query_len, k);
         return at::zeros({static_cast<int64_t>(n < 256 ? 256 : n)}, q.options().dtype(at::kByte));
     }
@@ -217,15 +246,17 @@ PyObject* attend_paged(PyObject* const* a) {
     const int32_t* prefix = nullptr;
     if (prefix_len != 0) {
         constexpr const char* what = "prefix_pages must be contiguous int32 and hold prefix_len keys";
-        const at::Tensor& t = tensor(a[7], what);
+        const at::Tensor& t = tensor(a[7], x.cache.device, what);
         need(t.scalar_type() == at::kInt && t.is_contiguous() && t.numel() * DSA_PAGE_TOKENS >= prefix_len, what);
         prefix = static_cast<const int32_t*>(pointer(t));
     }
+    int32_t* const status = status_word(a[13], x.cache.device);
     const at::Tensor ws = x.workspace(a[12], max_query_len, 0);
+    const OnDevice on(x.cache.device);
     check(dsa_attend_paged(&x.c, pointer(x.q), x.q.stride(0), x.q.stride(1), x.heads, x.table, x.bt_stride, x.pages,
                            x.starts, x.ends, x.requests, x.rows, max_query_len, prefix, prefix_len, x.scale,
                            pointer(x.out), x.out.stride(0), x.out.stride(1), x.lse_ptr, pointer(ws), ws.nbytes(),
-                           status_word(a[13]), stream_of(THPVariable_Unpack(a[1]))),
+                           status, on.stream),
           "dsa_attend_paged");
     return x.result(a[10]);
 }
@@ -234,15 +265,17 @@ PyObject* attend_paged(PyObject* const* a) {
 PyObject* attend_selected(PyObject* const* a) {
     const Attention x(a, a[7], a[8], a[9]);
     constexpr const char* what = "topk must be int32 [rows, k] with contiguous rows";
-    const at::Tensor& t = tensor(a[6], what);
+    const at::Tensor& t = tensor(a[6], x.cache.device, what);
     need(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == x.rows && (t.numel() == 0 || t.stride(1) == 1),
          what);
     const int64_t k = t.size(1);
+    int32_t* const status = status_word(a[11], x.cache.device);
     const at::Tensor ws = x.workspace(a[10], 1, k > 0 ? k : 1);
+    const OnDevice on(x.cache.device);
     check(dsa_attend_selected(&x.c, pointer(x.q), x.q.stride(0), x.q.stride(1), x.heads, x.table, x.bt_stride, x.pages,
                               x.starts, x.ends, x.requests, x.rows, static_cast<const int32_t*>(pointer(t)),
                               t.stride(0), k, x.scale, pointer(x.out), x.out.stride(0), x.out.stride(1), x.lse_ptr,
-                              pointer(ws), ws.nbytes(), status_word(a[11]), stream_of(THPVariable_Unpack(a[1]))),
+                              pointer(ws), ws.nbytes(), status, on.stream),
           "dsa_attend_selected");
     return x.result(a[8]);
 }
