@@ -498,6 +498,8 @@ __device__ __forceinline__ float2 unpack2(uint64_t r) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
     return v;
 }
+// a b + c.  (A packed product and a packed sum, both rounded to nearest as written,
+// came out as one fused operation; a product that is to be rounded adds a zero.)
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -524,6 +526,19 @@ struct Facts<Fp16> {
     static constexpr uint32_t mma = 0, expo = 0x7C00u;
     static constexpr float shift = 7.0f;
 };
+
+// What is added to a row's scores (in powers of two) before they are raised.  Its
+// negative is the reference of the row's weights and of their sum: past 2^17 or so
+// m and the shift no longer add up in 32 bits, and only what was added counts.
+// Rounded down, here and in the test, so that no weight passes 2^(slack + shift).
+// A score is rounded by its scale before this is added (no fused multiply-add), as
+// the maximum is: otherwise half a step of the scaled score stays in the exponent,
+// a factor of two from 2^24 on, and weights overflow (FP16 there, BF16 at 2^31).
+template <typename T>
+__device__ __forceinline__ float base_of(float m) {
+    return m == -INFINITY ? 0.0f : __fadd_rd(Facts<T>::shift, -m);
+}
+__device__ __forceinline__ bool passes(float mx, float m) { return mx > __fadd_rd(m, kSlack); }
 
 template <typename T>
 __device__ __forceinline__ bool half_wild(uint32_t h) {
@@ -1067,7 +1082,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         };
         int64_t t = t0;
         while (t < t1 && ok) {
-            float m_ref = -INFINITY, l = 0.0f;
+            float m_ref = -INFINITY, base = 0.0f, l = 0.0f;
             int ntiles = 1, tile0 = 0, bound = 0;
             bool on = false;
             const Piece& pc = sh.piece[slot][npiece % kPieces];
@@ -1099,12 +1114,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         m4[x] = fmaxf(fmaxf(m4[x], __uint_as_float(w[j + x])), __uint_as_float(w[j + x + 4]));
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-                const bool up = mx > m_ref + kSlack;
+                const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), c);
+                const bool up = passes(mx, m_ref);
                 if (__any_sync(0xFFFFFFFFu, up)) {
-                    const float nm = up ? mx : m_ref;
-                    const float f = up ? ex2(m_ref - nm) : 1.0f;
-                    m_ref = nm;
+                    const float nb = up ? base_of<T>(mx) : base;
+                    const float f = !up ? 1.0f : m_ref == -INFINITY ? 0.0f : ex2(nb - base);
+                    if (up) m_ref = mx;
+                    base = nb;
                     l *= f;
                     if (i > 0) {
                         // every product of this slot so far is done (they precede this tile's scores)
@@ -1118,13 +1134,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                         }
                     }
                 }
-                const float base = m_ref == -INFINITY ? 0.0f : Facts<T>::shift - m_ref;
                 const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
                 uint64_t s0 = 0, s1 = 0;
                 uint32_t h[16];
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    const float2 e = unpack2(fma2(pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), c2, b2));
+                    const uint64_t s2 = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+                    const float2 e = unpack2(add2(fma2(s2, c2, 0), b2));
                     const float p0 = ex2(e.x), p1 = ex2(e.y);
                     if (j & 2) s1 = add2(s1, pack2(p0, p1));
                     else s0 = add2(s0, pack2(p0, p1));
@@ -1153,7 +1169,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             // (Loops stay rolled and accesses are 16 bytes wide: this code runs once a piece, and instructions
             // that are not in the cache cost more than what they do.)  A thread writes its row's strip and adds
             // four columns of row `r`, each strip brought to the row's common reference.
-            ml[quarter * 32 + lane] = make_float2(m_ref, l);
+            ml[quarter * 32 + lane] = make_float2(m_ref == -INFINITY ? -INFINITY : -base, l);
             if (!meet()) break;
             const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
             const bool direct = pc.direct, own = pc.req >= 0 || kSelected;
@@ -1170,7 +1186,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 f[x] = e[x].x == -INFINITY ? 0.0f : ex2(e[x].x - top);
                 sum += e[x].y * f[x];
             }
-            const float ref = top == -INFINITY ? -INFINITY : top - Facts<T>::shift;
             const int row = pc.row0 + ri, head = pc.kvh * p.group + rg;
             uint16_t* out = p.out + row * p.orow + head * p.ohead;
             const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + r;
@@ -1182,10 +1197,10 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             }
             if (r_on && col4 == 0) {
                 if (!direct)
-                    (own ? p.pml : p.xml)[at] = make_float2(ref, sum);
+                    (own ? p.pml : p.xml)[at] = make_float2(top, sum);
                 else if (p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
-                        sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
+                        sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
             }
 #pragma unroll 1
             for (int x = 0; x < p.dim; x += mcols) {
@@ -1264,7 +1279,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         };
         int64_t t = t0;
         while (t < t1 && ok) {
-            float m_ref = -INFINITY, l = 0.0f;
+            float m_ref = -INFINITY, base = 0.0f, l = 0.0f;
             int steps = 1, ntiles = 1, tile0 = 0, bound = 0;
             bool on = false, warp_on = false;
             const Piece& pc = sh.piece[slot][npiece % kPieces];
@@ -1303,20 +1318,21 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             m4[x] = fmaxf(fmaxf(m4[x], __uint_as_float(w[y + x])), __uint_as_float(w[y + x + 4]));
-                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+                    float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), c);
                     // The two warps meet in any case: both have read their scores, so the weights may take the
                     // scores' columns.  Where a row's reference has to rise, they agree on it.
-                    const int raise = meet_any(mx > m_ref + kSlack);
+                    const int raise = meet_any(passes(mx, m_ref));
                     if (raise < 0) break;
                     if (raise) {
                         sh.half[slot][half][m] = mx;
                         if (!meet()) break;
                         mx = fmaxf(mx, sh.half[slot][half ^ 1][m]);
                         if (!meet()) break;
-                        const bool up = mx > m_ref + kSlack;
-                        const float nm = up ? mx : m_ref;
-                        const float f = up ? ex2(m_ref - nm) : 1.0f;
-                        m_ref = nm;
+                        const bool up = passes(mx, m_ref);
+                        const float nb = up ? base_of<T>(mx) : base;
+                        const float f = !up ? 1.0f : m_ref == -INFINITY ? 0.0f : ex2(nb - base);
+                        if (up) m_ref = mx;
+                        base = nb;
                         l *= f;
                         if (j > 0) {
                             // the products of the half tile before may still be running
@@ -1334,13 +1350,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                             }
                         }
                     }
-                    const float base = m_ref == -INFINITY ? 0.0f : Facts<T>::shift - m_ref;
                     const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
                     uint64_t s0 = 0, s1 = 0;
                     uint32_t e16[16];
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
-                        const float2 e = unpack2(fma2(pack2(__uint_as_float(w[x]), __uint_as_float(w[x + 1])), c2, b2));
+                        const uint64_t s2 = pack2(__uint_as_float(w[x]), __uint_as_float(w[x + 1]));
+                        const float2 e = unpack2(add2(fma2(s2, c2, 0), b2));
                         const float p0 = ex2(e.x), p1 = ex2(e.y);
                         if (x & 2) s1 = add2(s1, pack2(p0, p1));
                         else s0 = add2(s0, pack2(p0, p1));
@@ -1366,7 +1382,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 if (!meet()) break;
                 l = sh.half[slot][0][m] + sh.half[slot][1][m];
                 const bool poison = *reinterpret_cast<const volatile int*>(&pc.poison) != 0;
-                const float ref = m_ref == -INFINITY ? -INFINITY : m_ref - Facts<T>::shift;
+                const float ref = m_ref == -INFINITY ? -INFINITY : -base;
                 const int row = pc.row0 + mi, head = pc.kvh * p.group + mg;
                 const bool direct = pc.direct;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
