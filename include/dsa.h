@@ -561,8 +561,10 @@ size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t hea
  *                 -inf for a row that sees no key.
  *   workspace     dsa_attend_workspace_size(...) bytes, 256-byte aligned.
  * Keys a row may not see do not reach its output, whatever their bits (the cache
- * past a request's end may hold NaN); a visible key or value that is not finite
- * makes what it enters not finite (infinite or NaN).  A page outside the pool is not read
+ * past a request's end may hold NaN).  Visible values that are not finite make the
+ * output columns they enter infinite where they are of one sign, else NaN; visible
+ * keys that are not finite make what they enter not finite, or drop out where their
+ * score is -inf.  A page outside the pool is not read
  * (DSA_STATUS_BAD_PAGE; rows that see it are unspecified).  Products accumulate in
  * FP32; the softmax weights are rounded to the cache's type before they meet the
  * values.  dim a multiple of 16 up to 128, else DSA_ERR_UNSUPPORTED.

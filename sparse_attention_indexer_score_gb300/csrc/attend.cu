@@ -574,18 +574,48 @@ struct Ring {
     }
 };
 
-// The values that were taken out of the products because some rows must not see
-// them, added to a row that does: columns x .. x + 15.
-template <typename T>
-__device__ __noinline__ void add_wild(const AttParams& p, const Piece& pc, int bound, int x, uint32_t (&o)[16]) {
-    const int from = max(pc.minb, pc.tile0 * kTile), to = min(bound, (pc.tile0 + pc.ntiles) * kTile);
-    for (int k = from; k < to; ++k) {
-        const int page = p.bt[pc.req * p.bt_stride + k / kPage];
-        if (page < 0 || page >= p.num_pages) continue;
-        const uint16_t* v = p.vbase + page * p.vp + (k % kPage) * p.vt + pc.kvh * p.vh + x;
+// The columns of a row's outputs, as the calling thread has written them for a piece
+// (n from x0, x0 + step, ... on; `out` 16-bit outputs, else `part`), in which a value
+// that the row sees is not finite: the sum of those values takes the output's place,
+// since finite terms do not change it.  The products cannot give it:
+// such values were taken out where some rows must not see them, and an infinite one
+// times a weight of zero (another strip's key, or one too small for 16 bits) is NaN.
+template <typename T, bool kSelected>
+__device__ __noinline__ void put_wild(const AttParams& p, const Piece& pc, int row, int bound, int x0, int n, int step,
+                                      uint16_t* out, float* part) {
+    const int from = pc.tile0 * kTile, to = min(bound, (pc.tile0 + pc.ntiles) * kTile);
+    const int32_t* pages = pc.req < 0 ? p.prefix_pages : p.bt + pc.req * p.bt_stride;
+    const int* list = p.list + static_cast<int64_t>(row) * p.kpad;
+    for (int y = 0; x0 + y / n * step < p.dim; y += 4) {
+        const int x = x0 + y / n * step + y % n;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t found = 0;
+#pragma unroll 4
+        for (int k = from; k < to; ++k) {
+            int page, token = k % kPage;
+            if (kSelected) {
+                const int id = list[k];
+                page = id < 0 ? -1 : id / kPage, token = id % kPage;
+            } else {
+                page = pages[k / kPage];
+            }
+            uint2 v = {0, 0};
+            if (page >= 0 && page < p.num_pages)
+                v = *reinterpret_cast<const uint2*>(p.vbase + page * p.vp + token * p.vt + pc.kvh * p.vh + x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (half_wild<T>(v[j])) o[j] = __float_as_uint(__uint_as_float(o[j]) + T::unpack(v[j]).x);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t e = (j < 2 ? v.x : v.y) >> (j & 1) * 16;
+                if (half_wild<T>(e)) sum[j] += T::unpack(e).x, found |= 1u << j;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!(found >> j & 1)) continue;
+            if (out)
+                out[x + j] = static_cast<uint16_t>(T::pack(sum[j], 0.0f));
+            else
+                part[x + j] = sum[j];
+        }
     }
 }
 
@@ -1202,6 +1232,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
                         sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
             }
+            float wild = poison ? NAN : 0.0f;
 #pragma unroll 1
             for (int x = 0; x < p.dim; x += mcols) {
                 if (x > 0 && !meet()) break;                            // the buffer has been read
@@ -1211,14 +1242,6 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     uint32_t o[16];
                     tc_ld_32x32b_x16(a_o + x + y, o);
                     tc_wait_ld16(o);
-                    if (!kSelected && poison && on && quarter == 0) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = o[j];
-                        add_wild<T>(p, pc, bound, x + y, w);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = w[j];
-                    }
                     if (lane < mrows) {
                         uint4* to = reinterpret_cast<uint4*>(buf + quarter * kMergeFloats + lane * (mcols + 4) + y);
 #pragma unroll
@@ -1234,6 +1257,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     v.x += u.x * f[y], v.y += u.y * f[y], v.z += u.z * f[y], v.w += u.w * f[y];
                 }
                 if (r_on && x + col4 < p.dim) {
+                    // (NaN once an output is not finite)
+                    wild = fmaf(v.x, 0.0f, fmaf(v.y, 0.0f, fmaf(v.z, 0.0f, fmaf(v.w, 0.0f, wild))));
                     if (direct)
                         *reinterpret_cast<uint2*>(out + x + col4) =
                             make_uint2(T::pack(v.x, v.y), T::pack(v.z, v.w));
@@ -1242,6 +1267,10 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 }
             }
             if (!ok) break;
+            if (r_on && wild != 0.0f && sum > 0.0f) {
+                const int sees = pc.minb == pc.keys ? pc.keys : min(max(p.row_ends[row], 0), p.max_keys);
+                put_wild<T, kSelected>(p, pc, row, sees, col4, 4, mcols, direct ? out : nullptr, part);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.ofree[slot]);
@@ -1401,18 +1430,13 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 if (on && direct && half == 0 && p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
                         l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                float wild = poison ? NAN : 0.0f;                       // (NaN once an output is not finite)
                 for (int x = half * 16; x < p.dim; x += 32) {
                     uint32_t o[16];
                     tc_ld_32x32b_x16(a_o + x, o);
                     tc_wait_ld16(o);
-                    if (!kSelected && poison && on) {
-                        uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = o[j];
-                        add_wild<T>(p, pc, bound, x, w);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = w[j];
-                    }
+                    for (int j = 0; j < 16; ++j) wild = fmaf(__uint_as_float(o[j]), 0.0f, wild);
                     if (on && direct) {
                         uint32_t h[8];
 #pragma unroll
@@ -1426,6 +1450,8 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                             *reinterpret_cast<uint4*>(part + x + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
+                if (on && wild != 0.0f && l > 0.0f)
+                    put_wild<T, kSelected>(p, pc, row, bound, half * 16, 16, 32, direct ? out : nullptr, part);
             }
             tc_fence_before();
             __syncwarp();
