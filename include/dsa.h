@@ -531,8 +531,10 @@ int dsa_kv_append(const dsa_kv_cache* cache, const void* k, int64_t k_token_stri
 /*
  * dsa_attend_workspace_size - bytes of scratch dsa_attend_paged (k = 0) or
  * dsa_attend_selected (k = list length, 1 for empty lists; max_query_len is not
- * used) needs for these sizes; 0 for sizes the calls refuse.  Zero-fill the workspace before its first use; every completed
- * call leaves it ready for the next, of any sizes that fit.
+ * used) needs for these sizes; 0 for sizes the calls refuse.  An attention
+ * workspace needs no clearing, whatever was in it before, and any sizes that fit
+ * may follow each other in it.  It is NOT left zero-filled: memory that attention
+ * has used is zero-filled again before it serves a scoring or top-k call.
  */
 size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
                                  int64_t max_query_len, int64_t k);

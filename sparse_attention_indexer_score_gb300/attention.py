@@ -42,7 +42,8 @@ class DecodeAttention:
         requests = indexer.block_table.shape[0]
         size = max(dsa.attend_workspace_size(max_rows, requests, heads, kv_heads, dim, self.max_query_len),
                    dsa.attend_workspace_size(max_rows, requests, heads, kv_heads, dim, 1, max(indexer.k, 1)))
-        self.workspace = dsa.new_workspace(size, dev)
+        # (not the indexer's, which has to stay clear; this one needs no clearing)
+        self.workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
                q: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:

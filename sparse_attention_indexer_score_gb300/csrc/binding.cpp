@@ -9,7 +9,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -224,7 +223,7 @@ struct Attention {
             return t;
         }
         const size_t n = dsa_attend_workspace_size(rows, requests, heads, c.heads, c.dim, max_query_len, k);
-        return at::zeros({static_cast<int64_t>(n < 256 ? 256 : n)}, q.options().dtype(at::kByte));
+        return at::empty({static_cast<int64_t>(n < 256 ? 256 : n)}, q.options().dtype(at::kByte));
     }
 
     PyObject* result(PyObject* out_o) const {

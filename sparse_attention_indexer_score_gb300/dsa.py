@@ -333,7 +333,9 @@ def topk_workspace_size(rows: int, k: int) -> int:
 
 
 def new_workspace(nbytes: int, device) -> torch.Tensor:
-    """A zero-filled workspace (the library leaves it zero-filled after each call)."""
+    """A zero-filled workspace.  Scoring and top-k calls need it so and leave it so;
+    attention calls take any bytes and leave any, so a workspace that attention has
+    used is cleared before it serves a scoring or top-k call."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
@@ -450,7 +452,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: to
 def attend_workspace_size(rows: int, num_requests: int, heads: int, kv_heads: int, dim: int, max_query_len: int,
                           k: int = 0) -> int:
     """Bytes of scratch of ``attend_paged`` (k = 0) or ``attend_selected`` (k =
-    the list length, 1 for empty lists)."""
+    the list length, 1 for empty lists).  It needs no clearing and is not left
+    clear: scoring and top-k calls have workspaces of their own."""
     return int(lib().dsa_attend_workspace_size(rows, num_requests, heads, kv_heads, dim, max_query_len, k))
 
 
