@@ -264,8 +264,11 @@ int dsa_query_norm(const void* x, int64_t x_row_stride, const void* w, float eps
 /*
  * dsa_workspace_size - bytes of scratch dsa_score_paged needs for these sizes
  * (rows query rows, num_requests requests, max_pages block-table columns, top-k k).
- * The workspace must be zero-filled before its first use; every call that
- * completes leaves it zero-filled again, so it can be reused without clearing.
+ * The workspace must be zero-filled before its first use.  Every call that
+ * completes leaves it ready for the next scoring, top-k or merge call of at most
+ * the rows and max_pages it was sized for, in any order, without clearing: give
+ * every call the whole workspace (the same workspace_bytes).  Calls that share one
+ * are sized together, by the most rows and the most max_pages of any of them.
  */
 size_t dsa_workspace_size(int fmt, int64_t rows, int64_t num_requests,
                           int64_t max_pages, int64_t k);
@@ -390,7 +393,7 @@ int dsa_score_paged_heads(int fmt, int64_t heads, const void* payload, const voi
 
 /*
  * dsa_topk_workspace_size - bytes of scratch dsa_topk needs (zero-filled before
- * first use, left zero-filled by every completed call).
+ * first use, left ready for calls of at most as many rows, as dsa_workspace_size).
  */
 size_t dsa_topk_workspace_size(int64_t rows, int64_t k);
 
@@ -428,7 +431,7 @@ int dsa_topk(const float* logits, int64_t ld, const int32_t* row_ends,
  *   rank, out_local  optional (out_local may be NULL): rank-local positions of
  *              the selected keys that `rank` owns, -1 elsewhere.
  *   workspace  at least dsa_topk_workspace_size(rows, k_out) bytes, 256-byte
- *              aligned, zero-filled before first use (left zero-filled).
+ *              aligned, zero-filled before first use (left ready).
  * Errors (DSA_ERR_INVALID): negative sizes, world < 1, interleave < 1, short
  * leading dimensions, null pointers, rank outside [0, world) with out_local.
  */
@@ -533,8 +536,8 @@ int dsa_kv_append(const dsa_kv_cache* cache, const void* k, int64_t k_token_stri
  * dsa_attend_selected (k = list length, 1 for empty lists; max_query_len is not
  * used) needs for these sizes; 0 for sizes the calls refuse.  An attention
  * workspace needs no clearing, whatever was in it before, and any sizes that fit
- * may follow each other in it.  It is NOT left zero-filled: memory that attention
- * has used is zero-filled again before it serves a scoring or top-k call.
+ * may follow each other in it.  It is NOT left as scoring and top-k need theirs:
+ * memory that attention has used is zero-filled before it serves such a call.
  */
 size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
                                  int64_t max_query_len, int64_t k);

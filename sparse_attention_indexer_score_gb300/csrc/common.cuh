@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "../../include/dsa.h"
+#include "workspace.h"
 
 namespace dsa {
 
@@ -30,11 +31,6 @@ constexpr int kRgQuerySlots = 64;
 __host__ __device__ __forceinline__ bool fmt_fp4(int fmt) {
     return fmt == DSA_FMT_MXFP4 || fmt == DSA_FMT_MXFP4_RG;
 }
-
-// Top-k: 11-bit histogram of the order-preserving score bits.
-constexpr int kHistBits = 11;
-constexpr int kHistBins = 1 << kHistBits;
-constexpr int kCandCap = 8192;    // level-1 candidates kept per split row
 
 // Bounded waits give up after this long (ns) and flag DSA_STATUS_TIMEOUT.
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;

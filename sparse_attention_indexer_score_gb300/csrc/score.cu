@@ -1242,7 +1242,7 @@ static int score_paged_impl(int fmt, const QueryOperands& qo, const void* cache,
     if (logits && (logits_ld < width || !aligned(logits, 4))) return DSA_ERR_INVALID;
     const bool want_topk = (k > 0 && topk != nullptr);
     if (k > (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
-    const WsLayout L = workspace_layout(rows, width, true, logits == nullptr);
+    const WsLayout L = workspace_layout(rows, width, true, logits == nullptr, workspace_bytes);
     if (workspace_bytes < L.total) return DSA_ERR_INVALID;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* out_logits = logits ? logits : reinterpret_cast<float*>(ws + L.logits);

@@ -519,34 +519,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
 }
 
 // ----------------------------------------------------------------- host utilities
-static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-WsLayout workspace_layout(int64_t rows, int64_t width, bool with_plan, bool with_logits) {
-    WsLayout L{};
-    size_t off = 0;
-    const size_t r = static_cast<size_t>(rows);
-    L.info = off;
-    off = align256(off + (with_plan ? 8 * sizeof(int) : 0));
-    L.segs = off;
-    off = align256(off + (with_plan ? (r + 1) * sizeof(int4) : 0));
-    L.seg_prefix = off;
-    off = align256(off + (with_plan ? (r + 2) * sizeof(int) : 0));
-    L.eff_end = off;
-    off = align256(off + (with_plan ? r * sizeof(int) : 0));
-    L.cta = off;
-    off = align256(off + (with_plan ? kMaxScoreCtas * sizeof(int4) : 0));
-    L.hist = off;
-    off = align256(off + r * kHistBins * sizeof(unsigned));
-    L.counters = off;
-    off = align256(off + r * 4 * sizeof(int));
-    L.cand = off;
-    off = align256(off + r * kCandCap * sizeof(uint2));
-    L.logits = off;
-    off = align256(off + (with_logits ? r * static_cast<size_t>(width) * sizeof(float) : 0));
-    L.total = off;
-    return L;
-}
-
 int device_sm_count() {
     static int cache[64] = {0};
     int dev = 0;
@@ -652,7 +624,7 @@ extern "C" int dsa_topk(const float* logits, int64_t ld, const int32_t* row_ends
     if (!row_ends || !out || !workspace || (width > 0 && !logits)) return DSA_ERR_INVALID;
     if (reinterpret_cast<uintptr_t>(workspace) % 256) return DSA_ERR_INVALID;
     if (k > (int64_t(1) << 30) || width > (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
-    const WsLayout L = workspace_layout(rows, 0, false, false);
+    const WsLayout L = workspace_layout(rows, 0, false, false, workspace_bytes);
     if (workspace_bytes < L.total) return DSA_ERR_INVALID;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int64_t chunks = (width + kChunk - 1) / kChunk;
@@ -715,10 +687,10 @@ extern "C" int dsa_topk_noalloc(const float* logits, int64_t ld, const int32_t* 
     uint8_t* ws = nullptr;
     const int rc = noalloc_scratch(&ws);
     if (rc != DSA_OK) return rc;
-    const WsLayout L = workspace_layout(rows, 0, false, false);
+    const WsLayout L = workspace_layout(rows, 0, false, false, kNoAllocBytes);
     if (L.total > kNoAllocBytes) return DSA_ERR_UNSUPPORTED;
     // The array keeps the last call's contents: clear the histograms and counters.
-    if (cudaMemsetAsync(ws + L.hist, 0, L.cand - L.hist, stream) != cudaSuccess) return DSA_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, L.zeroed, stream) != cudaSuccess) return DSA_ERR_CUDA;
     if (chunks > 0) {
         if (launch_pdl(hist_kernel, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(chunks)),
                        dim3(kSelThreads), 0, stream, logits, ld, width, row_ends, static_cast<int>(k),
@@ -776,7 +748,7 @@ extern "C" int dsa_topk_merge(const float* scores, int64_t scores_ld, const int3
     if (k_out > (int64_t(1) << 30) || width > (int64_t(1) << 30) || interleave > (int64_t(1) << 30) ||
         world > (int64_t(1) << 20))
         return DSA_ERR_UNSUPPORTED;
-    const WsLayout L = workspace_layout(rows, 0, false, false);
+    const WsLayout L = workspace_layout(rows, 0, false, false, workspace_bytes);
     if (workspace_bytes < L.total) return DSA_ERR_INVALID;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int64_t chunks = (width + kChunk - 1) / kChunk;

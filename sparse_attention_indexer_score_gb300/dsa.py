@@ -333,8 +333,9 @@ def topk_workspace_size(rows: int, k: int) -> int:
 
 
 def new_workspace(nbytes: int, device) -> torch.Tensor:
-    """A zero-filled workspace.  Scoring and top-k calls need it so and leave it so;
-    attention calls take any bytes and leave any, so a workspace that attention has
+    """A zero-filled workspace, as scoring and top-k calls need theirs at first; they
+    leave it ready for the next call of at most the rows and pages it was sized for.
+    Attention calls take any bytes and leave any, so a workspace that attention has
     used is cleared before it serves a scoring or top-k call."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
