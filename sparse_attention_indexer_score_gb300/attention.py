@@ -51,15 +51,21 @@ class DecodeAttention:
         return dsa.kv_append(k, v, slots, self.k_cache, self.v_cache, positions, self.cos_sin, q=q,
                              interleaved=self.interleaved, status=self.indexer.status)
 
+    def _table(self, starts: torch.Tensor) -> torch.Tensor:
+        """The block table of the step's requests, the first of the indexer's."""
+        table, requests = self.indexer.block_table, starts.numel() - 1
+        return table if table.shape[0] == requests else table[:requests]
+
     def step(self, iq: torch.Tensor, wv: torch.Tensor, ikeys: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
              v: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor, seq_lens: torch.Tensor,
              query_lens: torch.Tensor) -> Tuple[torch.Tensor, StepOutput]:
         """iq [rows, 32, 128], wv [rows, 32], ikeys [rows, 128]: the indexer's projections; q [rows, heads, dim],
-        k and v [rows, kv_heads, dim]: the layer's; slots and positions int64 [rows] (slot -1: padding).
+        k and v [rows, kv_heads, dim]: the layer's; slots and positions int64 [rows] (slot -1: padding); a request for
+        each of the block table's rows or of its first.
         Returns (attention output [rows, heads, dim], the indexer's step)."""
         chosen = self.indexer.step(iq, wv, ikeys, slots, seq_lens, query_lens, self.max_query_len)
         q = self.append(k, v, slots, positions, q)
-        out, _ = dsa.attend_selected(q, self.k_cache, self.v_cache, self.indexer.block_table, chosen.starts,
+        out, _ = dsa.attend_selected(q, self.k_cache, self.v_cache, self._table(chosen.starts), chosen.starts,
                                      chosen.row_ends, chosen.topk, scale=self.scale, workspace=self.workspace,
                                      status=self.indexer.status)
         return out, chosen
@@ -69,7 +75,7 @@ class DecodeAttention:
                    prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0) -> torch.Tensor:
         """Append, then attention over the shared prefix and all own keys below ``row_ends``."""
         q = self.append(k, v, slots, positions, q)
-        out, _ = dsa.attend_paged(q, self.k_cache, self.v_cache, self.indexer.block_table, starts, row_ends,
+        out, _ = dsa.attend_paged(q, self.k_cache, self.v_cache, self._table(starts), starts, row_ends,
                                   self.max_query_len, prefix_pages=prefix_pages, prefix_len=prefix_len,
                                   scale=self.scale, workspace=self.workspace, status=self.indexer.status)
         return out
