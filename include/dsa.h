@@ -552,7 +552,8 @@ size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t hea
  * query head h reading key/value head h / (heads / kv_heads).  The prefix's keys
  * are read once for the rows of the whole batch.
  *
- *   q             [rows][heads][dim] of the cache's type (strides in elements).
+ *   q             [rows][heads][dim] of the cache's type (strides in elements; a
+ *                 stride of 0 over several rows or heads is DSA_ERR_UNSUPPORTED).
  *   heads         a multiple of cache->heads, at most 128 per key/value head.
  *   block_table, bt_stride, max_pages, starts, row_ends, num_requests, rows
  *                 as dsa_score_paged.  Rows outside every request see no keys.

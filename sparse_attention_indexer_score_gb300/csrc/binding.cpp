@@ -45,6 +45,12 @@ const at::Tensor& tensor(PyObject* o, const at::Device& device, const char* what
 
 bool given(PyObject* o) { return o != Py_None; }
 
+// A dimension of one element (or none) may come with any stride, which the C calls would check: another in its place.
+int64_t stride(const at::Tensor& t, int64_t d, int64_t instead = 0) { return t.size(d) > 1 ? t.stride(d) : instead; }
+
+// Whether a dimension's elements lie one behind the other.
+bool dense(const at::Tensor& t, int64_t d) { return t.numel() == 0 || t.size(d) == 1 || t.stride(d) == 1; }
+
 int64_t whole(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) {
@@ -103,9 +109,9 @@ Cache cache_of(PyObject* k_cache, PyObject* v_cache) {
     need(k.stride(3) == 1 && v.stride(3) == 1, "cache columns must be contiguous");
     dsa_kv_cache c;
     c.k = pointer(k), c.v = pointer(v);
-    c.k_page_stride = k.stride(0), c.k_token_stride = k.stride(1), c.k_head_stride = k.stride(2);
-    c.v_page_stride = v.stride(0), c.v_token_stride = v.stride(1), c.v_head_stride = v.stride(2);
     c.num_pages = k.size(0), c.heads = k.size(2), c.dim = k.size(3);
+    c.k_page_stride = stride(k, 0), c.k_token_stride = stride(k, 1), c.k_head_stride = stride(k, 2);
+    c.v_page_stride = stride(v, 0), c.v_token_stride = stride(v, 1), c.v_head_stride = stride(v, 2);
     c.dtype = type == at::kBFloat16 ? DSA_BF16 : DSA_FP16;
     return Cache{c, type, k.device()};
 }
@@ -139,18 +145,19 @@ PyObject* kv_append(PyObject* const* a) {
     const at::Tensor &k = rows_of(a[0], cache, kv), &v = rows_of(a[1], cache, kv);
     need(k.size(1) == c.heads && v.sizes() == k.sizes(), kv);
     const int64_t n = k.size(0);
-    const at::Tensor& slots = list_of(a[2], cache.device, at::kLong, n, "slots must be contiguous int64 [n], one per key");
+    const at::Tensor& slots =
+        list_of(a[2], cache.device, at::kLong, n, "slots must be contiguous int64 [n], one per key");
     const int64_t* positions = nullptr;
     const float* cos_sin = nullptr;
     int64_t rot = 0, max_pos = 0, cs_stride = 0;
     if (given(a[6])) {
         constexpr const char* angles = "cos_sin must be FP32 [positions, rot] with contiguous rows";
         const at::Tensor& t = tensor(a[6], cache.device, angles);
-        need(t.scalar_type() == at::kFloat && t.dim() == 2 && (t.size(1) == 0 || t.stride(1) == 1), angles);
+        need(t.scalar_type() == at::kFloat && t.dim() == 2 && dense(t, 1), angles);
         positions = static_cast<const int64_t*>(
             pointer(list_of(a[5], cache.device, at::kLong, n, "positions must be contiguous int64 [n]")));
         cos_sin = static_cast<const float*>(pointer(t));
-        max_pos = t.size(0), rot = t.size(1), cs_stride = t.stride(0);
+        max_pos = t.size(0), rot = t.size(1), cs_stride = stride(t, 0, rot);
     }
     const void* q_ptr = nullptr;
     void* out_ptr = nullptr;
@@ -161,16 +168,16 @@ PyObject* kv_append(PyObject* const* a) {
         const at::Tensor& q = rows_of(a[7], cache, qs);
         need(q.size(0) == n, qs);
         out = output(a[8], q, "q_out must match q");
-        q_heads = q.size(1), qt = q.stride(0), qh = q.stride(1), ot = out.stride(0), oh = out.stride(1);
+        q_heads = q.size(1), qt = stride(q, 0), qh = stride(q, 1), ot = stride(out, 0), oh = stride(out, 1);
         q_ptr = pointer(q), out_ptr = pointer(out);
     } else {
         need(!given(a[8]), "q_out needs q");
     }
     int32_t* const status = status_word(a[10], cache.device);
     const OnDevice on(cache.device);
-    check(dsa_kv_append(&c, pointer(k), k.stride(0), k.stride(1), pointer(v), v.stride(0), v.stride(1), q_ptr, qt, qh,
-                        q_heads, out_ptr, ot, oh, n, static_cast<const int64_t*>(pointer(slots)), positions, cos_sin,
-                        cs_stride, max_pos, rot, truth(a[9]), status, on.stream),
+    check(dsa_kv_append(&c, pointer(k), stride(k, 0), stride(k, 1), pointer(v), stride(v, 0), stride(v, 1),
+                        q_ptr, qt, qh, q_heads, out_ptr, ot, oh, n, static_cast<const int64_t*>(pointer(slots)),
+                        positions, cos_sin, cs_stride, max_pos, rot, truth(a[9]), status, on.stream),
           "dsa_kv_append");
     if (!out.defined()) Py_RETURN_NONE;
     if (given(a[8])) {
@@ -195,12 +202,13 @@ struct Attention {
         q = rows_of(a[0], cache, "q must be [rows, heads, dim] of the cache's type with contiguous columns");
         constexpr const char* bt = "block_table must be int32 [requests, pages] with contiguous rows";
         const at::Tensor& t = tensor(a[3], cache.device, bt);
-        need(t.scalar_type() == at::kInt && t.dim() == 2 && (t.numel() == 0 || t.stride(1) == 1), bt);
-        requests = t.size(0), pages = t.size(1), bt_stride = t.stride(0);
+        need(t.scalar_type() == at::kInt && t.dim() == 2 && dense(t, 1), bt);
+        requests = t.size(0), pages = t.size(1), bt_stride = stride(t, 0, pages);
         rows = q.size(0), heads = q.size(1);
         table = static_cast<const int32_t*>(pointer(t));
-        starts = static_cast<const int32_t*>(pointer(list_of(
-            a[4], cache.device, at::kInt, requests + 1, "starts must be contiguous int32, one entry per request and one more")));
+        starts = static_cast<const int32_t*>(
+            pointer(list_of(a[4], cache.device, at::kInt, requests + 1,
+                            "starts must be contiguous int32, one entry per request and one more")));
         ends = static_cast<const int32_t*>(pointer(list_of(
             a[5], cache.device, at::kInt, rows, "row_ends must be contiguous int32, one bound per query row")));
         scale = given(scale_o) ? static_cast<float>(PyFloat_AsDouble(scale_o))
@@ -252,9 +260,9 @@ PyObject* attend_paged(PyObject* const* a) {
     int32_t* const status = status_word(a[13], x.cache.device);
     const at::Tensor ws = x.workspace(a[12], max_query_len, 0);
     const OnDevice on(x.cache.device);
-    check(dsa_attend_paged(&x.c, pointer(x.q), x.q.stride(0), x.q.stride(1), x.heads, x.table, x.bt_stride, x.pages,
+    check(dsa_attend_paged(&x.c, pointer(x.q), stride(x.q, 0), stride(x.q, 1), x.heads, x.table, x.bt_stride, x.pages,
                            x.starts, x.ends, x.requests, x.rows, max_query_len, prefix, prefix_len, x.scale,
-                           pointer(x.out), x.out.stride(0), x.out.stride(1), x.lse_ptr, pointer(ws), ws.nbytes(),
+                           pointer(x.out), stride(x.out, 0), stride(x.out, 1), x.lse_ptr, pointer(ws), ws.nbytes(),
                            status, on.stream),
           "dsa_attend_paged");
     return x.result(a[10]);
@@ -265,16 +273,15 @@ PyObject* attend_selected(PyObject* const* a) {
     const Attention x(a, a[7], a[8], a[9]);
     constexpr const char* what = "topk must be int32 [rows, k] with contiguous rows";
     const at::Tensor& t = tensor(a[6], x.cache.device, what);
-    need(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == x.rows && (t.numel() == 0 || t.stride(1) == 1),
-         what);
+    need(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == x.rows && dense(t, 1), what);
     const int64_t k = t.size(1);
     int32_t* const status = status_word(a[11], x.cache.device);
     const at::Tensor ws = x.workspace(a[10], 1, k > 0 ? k : 1);
     const OnDevice on(x.cache.device);
-    check(dsa_attend_selected(&x.c, pointer(x.q), x.q.stride(0), x.q.stride(1), x.heads, x.table, x.bt_stride, x.pages,
-                              x.starts, x.ends, x.requests, x.rows, static_cast<const int32_t*>(pointer(t)),
-                              t.stride(0), k, x.scale, pointer(x.out), x.out.stride(0), x.out.stride(1), x.lse_ptr,
-                              pointer(ws), ws.nbytes(), status, on.stream),
+    check(dsa_attend_selected(&x.c, pointer(x.q), stride(x.q, 0), stride(x.q, 1), x.heads, x.table, x.bt_stride,
+                              x.pages, x.starts, x.ends, x.requests, x.rows, static_cast<const int32_t*>(pointer(t)),
+                              stride(t, 0, k), k, x.scale, pointer(x.out), stride(x.out, 0), stride(x.out, 1),
+                              x.lse_ptr, pointer(ws), ws.nbytes(), status, on.stream),
           "dsa_attend_selected");
     return x.result(a[8]);
 }
