@@ -60,7 +60,14 @@ int64_t whole(PyObject* o) {
     return v;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {   // a tensor of several elements, say
+        PyErr_Clear();
+        throw BadArgument("flags must be true or false");
+    }
+    return v == 1;
+}
 
 void* pointer(const at::Tensor& t) { return t.data_ptr(); }
 
@@ -173,11 +180,12 @@ PyObject* kv_append(PyObject* const* a) {
     } else {
         need(!given(a[8]), "q_out needs q");
     }
+    const bool interleaved = truth(a[9]);
     int32_t* const status = status_word(a[10], cache.device);
     const OnDevice on(cache.device);
     check(dsa_kv_append(&c, pointer(k), stride(k, 0), stride(k, 1), pointer(v), stride(v, 0), stride(v, 1),
                         q_ptr, qt, qh, q_heads, out_ptr, ot, oh, n, static_cast<const int64_t*>(pointer(slots)),
-                        positions, cos_sin, cs_stride, max_pos, rot, truth(a[9]), status, on.stream),
+                        positions, cos_sin, cs_stride, max_pos, rot, interleaved, status, on.stream),
           "dsa_kv_append");
     if (!out.defined()) Py_RETURN_NONE;
     if (given(a[8])) {
