@@ -1221,7 +1221,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
             const int64_t at = static_cast<int64_t>(pc.slot) * (own ? p.own_cap : p.x_cap) + r;
             float* part = (own ? p.po : p.xo) + at * p.dim;
             if (direct) {
-                const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) f[x] *= inv;
             }
@@ -1230,7 +1230,7 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                     (own ? p.pml : p.xml)[at] = make_float2(top, sum);
                 else if (p.lse)
                     p.lse[static_cast<int64_t>(row) * p.heads + head] =
-                        sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+                        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
             float wild = poison ? NAN : 0.0f;
 #pragma unroll 1
