@@ -11,6 +11,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libdsa.so")
 BINDING = os.path.join(HERE, "_dsa_binding.so")
+BUILT_WITH = os.path.join(BUILD_DIR, "built_with.txt")
 SOURCES = ["quant.cu", "layout.cu", "score.cu", "topk.cu", "norm.cu", "probe.cu", "kvcache.cu", "attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -34,8 +36,21 @@ def nvcc() -> str:
     return found
 
 
+def _tools() -> str:
+    """What the extension is compiled against besides the sources: torch and Python, by version and place."""
+    import torch
+
+    return "\n".join([torch.__version__, torch.__file__, sys.version])
+
+
 def _stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
+        return True
+    try:
+        with open(BUILT_WITH) as f:
+            if f.read() != _tools():
+                return True
+    except OSError:
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "dsa.h")]
@@ -43,7 +58,8 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the libraries if any source is newer than them; return ``libdsa.so``'s path."""
+    """Compile the libraries if any source is newer than them, or torch or Python is another than they were
+    compiled for; return ``libdsa.so``'s path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -74,6 +90,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
     _link_binding(binding_obj)
+    with open(BUILT_WITH, "w") as f:
+        f.write(_tools())
     return LIB
 
 
