@@ -507,7 +507,8 @@ typedef struct {
  *
  *   k, v         [n][cache->heads][dim], token and head strides in elements.
  *   q            optional queries [n][q_heads][dim] (NULL: keys and values only).
- *   q_out        rotated queries, same shape, may be q itself; NULL iff q is.
+ *   q_out        rotated queries, same shape, may be q itself; NULL iff q is.  (q_out
+ *                and the caches have a stride of 0 over one element only.)
  *   slots        int64 [n]: slot = page * 64 + offset; < 0 = padding (nothing is
  *                cached; its query is still rotated); >= num_pages * 64 is skipped
  *                and flagged DSA_STATUS_BAD_SLOT.  Equal slots race.
@@ -561,8 +562,8 @@ size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t hea
  *                 tiles, any value gives the same results; the one the workspace
  *                 was sized with).
  *   scale         > 0 and finite.
- *   out           [rows][heads][dim] of the cache's type; a row that sees no key
- *                 gets zeros.
+ *   out           [rows][heads][dim] of the cache's type, no stride of 0 over several
+ *                 rows or heads; a row that sees no key gets zeros.
  *   lse           optional FP32 [rows][heads]: log(sum_t exp(scale * q . k_t)),
  *                 -inf for a row that sees no key.
  *   workspace     dsa_attend_workspace_size(...) bytes, 256-byte aligned.

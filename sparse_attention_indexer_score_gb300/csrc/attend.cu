@@ -1658,6 +1658,7 @@ static int check_attend(const dsa_kv_cache* cache, const void* q, int64_t q_row_
     if (((q_row_stride | q_head_stride | out_row_stride | out_head_stride) & 7) || q_row_stride < 0 ||
         q_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0)
         return DSA_ERR_INVALID;
+    if ((rows > 1 && out_row_stride == 0) || (heads > 1 && out_head_stride == 0)) return DSA_ERR_INVALID;   // one place
     return DSA_OK;
 }
 

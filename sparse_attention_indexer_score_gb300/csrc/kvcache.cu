@@ -212,6 +212,13 @@ extern "C" int dsa_kv_append(const dsa_kv_cache* cache, const void* k, int64_t k
     const int64_t strides = k_token_stride | k_head_stride | v_token_stride | v_head_stride |
                             (q ? q_token_stride | q_head_stride | qo_token_stride | qo_head_stride : 0);
     if ((ptrs & 15) || (strides & 7)) return DSA_ERR_INVALID;
+    // tokens, heads or pages written to one place
+    auto one = [](int64_t extent, int64_t stride) { return extent > 1 && stride == 0; };
+    if ((q && (one(n, qo_token_stride) || one(q_heads, qo_head_stride))) || one(cache->num_pages, cache->k_page_stride) ||
+        one(cache->num_pages, cache->v_page_stride) || one(kPage, cache->k_token_stride) ||
+        one(kPage, cache->v_token_stride) || one(cache->heads, cache->k_head_stride) ||
+        one(cache->heads, cache->v_head_stride))
+        return DSA_ERR_INVALID;
 
     AppendArgs a;
     a.k = static_cast<const uint16_t*>(k);
