@@ -588,25 +588,28 @@ __device__ __noinline__ void put_wild(const AttParams& p, const Piece& pc, int r
     const int* list = p.list + static_cast<int64_t>(row) * p.kpad;
     for (int y = 0; x0 + y / n * step < p.dim; y += 4) {
         const int x = x0 + y / n * step + y % n;
+        bool finite = true;
+        for (int j = 0; j < 4; ++j) finite &= out ? !half_wild<T>(out[x + j]) : isfinite(part[x + j]);
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t found = 0;
-#pragma unroll 4
-        for (int k = from; k < to; ++k) {
-            int page, token = k % kPage;
-            if (kSelected) {
-                const int id = list[k];
-                page = id < 0 ? -1 : id / kPage, token = id % kPage;
-            } else {
-                page = pages[k / kPage];
-            }
-            uint2 v = {0, 0};
-            if (page >= 0 && page < p.num_pages)
-                v = *reinterpret_cast<const uint2*>(p.vbase + page * p.vp + token * p.vt + pc.kvh * p.vh + x);
+        // (where the outputs are finite only a value that was taken out can change them; nothing changes four NaNs)
+        for (int k = finite ? max(from, pc.minb) : from; k < to;) {
+            const int end = min(to, (k | (kPage - 1)) + 1);
+            const int of_page = kSelected ? 0 : pages[k / kPage];
+#pragma unroll 8
+            for (; k < end; ++k) {
+                const int id = kSelected ? list[k] : 0;
+                const int page = !kSelected ? of_page : id < 0 ? -1 : id / kPage, token = (kSelected ? id : k) % kPage;
+                uint2 v = {0, 0};
+                if (page >= 0 && page < p.num_pages)
+                    v = *reinterpret_cast<const uint2*>(p.vbase + page * p.vp + token * p.vt + pc.kvh * p.vh + x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t e = (j < 2 ? v.x : v.y) >> (j & 1) * 16;
-                if (half_wild<T>(e)) sum[j] += T::unpack(e).x, found |= 1u << j;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t e = (j < 2 ? v.x : v.y) >> (j & 1) * 16;
+                    if (half_wild<T>(e)) sum[j] += T::unpack(e).x, found |= 1u << j;
+                }
             }
+            if (isnan(sum[0]) && isnan(sum[1]) && isnan(sum[2]) && isnan(sum[3])) break;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

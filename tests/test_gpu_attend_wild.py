@@ -108,3 +108,16 @@ def test_an_infinite_value_of_a_small_weight(cuda_lib, hq, hkv):
     before = c.paged(cuda_lib)
     want = plant(c, [(0, 64, 0, 7, INF), (0, 64, hkv - 1, 8, -INF)])
     check(c, before, c.paged(cuda_lib), want, lambda r, j: True)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (128, 1)])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_a_cache_full_of_one_such_value(cuda_lib, value, hq, hkv):
+    """Every column of every row, long pieces among them, without a wait running out."""
+    c = Case([30000, 100], [1, 2], prefix=5000, hq=hq, hkv=hkv, dim=128)
+    topk = choose(c, 2000)
+    c.v.fill_(value)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for out, _ in (c.paged(cuda_lib, status=status), c.selected(cuda_lib, topk, status=status)):
+        assert torch.isnan(out).all() if value != value else (out == value).all()
+    assert int(status) == 0
