@@ -560,7 +560,9 @@ size_t dsa_attend_workspace_size(int64_t rows, int64_t num_requests, int64_t hea
  *                 as dsa_score_paged.  Rows outside every request see no keys.
  *   max_query_len largest row count of a request (>= 0; a hint that sizes the
  *                 tiles, any value gives the same results; the one the workspace
- *                 was sized with).
+ *                 was sized with).  Meant for decode and verify rows and for
+ *                 chunks of a prompt of up to 4096 rows a call: past that a single
+ *                 thread reads a request's bounds from global memory.
  *   scale         > 0 and finite.
  *   out           [rows][heads][dim] of the cache's type, no stride of 0 over several
  *                 rows or heads; a row that sees no key gets zeros.

@@ -17,13 +17,14 @@
 //
 // What bounds it: a key and its value are 4 d bytes and cost each row that shares
 // them 4 d flops, one flop a byte, so memory bounds it until some 270 rows share a
-// key; a prefix under hundreds of rows and heads is bound by the tensor cores.  Measured on GB300 (BF16, whole calls,
-// 6.8 TB/s and 1.85 PFLOP/s by copy and matrix product): 64 requests of 4096 to
-// 8192 keys, 32 heads over 8: 242 us, 6.7 TB/s.  64 rows of 2048 listed keys:
-// 97 us, 5.5 TB/s (the kernel alone 87 us).  320 rows of 64 heads over 8 behind
-// 32768 keys: 276 us for the prefix, 1.25 PFLOP/s.  One row of 1000 keys: 11 us, a
-// chain of latencies (4600 cycles to the first scores, 2750 for the join of the
-// strips, then the pieces' join as a launch).
+// key; a prefix under hundreds of rows and heads is bound by the tensor cores.
+// Measured on GB300 (BF16, whole calls, 6.8 TB/s and 1.95 PFLOP/s by copy and matrix
+// product): 64 requests of 4096 to 8192 keys, 32 heads over 8: 237 to 241 us,
+// 6.7 TB/s.  64 rows of 2048 listed keys: 97 us, 5.5 TB/s (the kernel alone 87 us).
+// 320 rows of 64 heads over 8 behind 32768 keys: 276 us for the prefix,
+// 1.25 PFLOP/s.  One row of 1000 keys: 10 us, a chain of latencies (4600 cycles to
+// the first scores, 2750 for the join of the strips, then the pieces' join as a
+// launch).
 #include <math.h>
 
 #include "elem16.cuh"
@@ -140,7 +141,8 @@ __device__ __forceinline__ int64_t share_start(int64_t w, int64_t T, int64_t W) 
 }
 __device__ __forceinline__ int worker_of(int64_t t, int64_t T, int64_t W) {
     if (T * W < (int64_t(1) << 32))   // (a 64-bit division takes about five times the instructions)
-        return static_cast<int>((static_cast<uint32_t>(t + 1) * static_cast<uint32_t>(W) - 1) / static_cast<uint32_t>(T));
+        return static_cast<int>((static_cast<uint32_t>(t + 1) * static_cast<uint32_t>(W) - 1) /
+                                static_cast<uint32_t>(T));
     return static_cast<int>(((t + 1) * W - 1) / T);
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
@@ -512,8 +514,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // Per-type facts: MMA type code, the exponent bits that mark a value that is
-// not finite, and a shift of the weights.  FP16 weights are kept 2^7 larger (at
-// most 2^15 with the slack) so that small ones stay out of the subnormals.
+// not finite, and a shift of the weights.
+//
+// Weights are rounded to the cache's type before they meet the values (their sum
+// takes them unrounded): both operands of the product have one type, and 16 bits
+// more of each weight would be a second product of the same size.  It costs half a
+// step of a weight each, independent of one another: against 64 bits outputs of
+// 64 requests are 0.0020 off in BF16 where 32-bit weights leave 0.0017 (the
+// rounding of the output itself), 0.00025 and 0.00021 in FP16.  FP16 weights are
+// kept 2^7 larger (at most 2^15 with the slack) so that small ones stay out of the
+// subnormals.
 template <typename T>
 struct Facts;
 template <>
@@ -1023,37 +1033,38 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
                 if (h == 0) {
                     ok = warp_wait(&sh.full[rs][at_v.st], at_v.ph, abort, p.status);
                     if (!ok) break;
-                if (!kSelected) {
-                    // Values no row may see are zeroed (0 x NaN is NaN); values only some rows may see
-                    // are searched for such, which the softmax warps then add by hand.
-                    const int left = keys - (tile0 + i) * kTile;       // keys of this tile
-                    const int all = minb - (tile0 + i) * kTile;        // ... that every row sees
-                    if (left < kTile || all < left) {
-                        const int from = min(max(all, 0), min(left, kTile));
-                        for (int x = lane; x < (kTile - from) * DH * 8; x += 32) {
-                            const int r = from + x / (DH * 8), c = x % (DH * 8);
-                            uint4* at16 = reinterpret_cast<uint4*>(va + (c >> 3) * kTile * 128 + r * 128 + (c & 7) * 16);
-                            if (r >= left) {
-                                *at16 = make_uint4(0, 0, 0, 0);
-                            } else {
-                                uint4 v = *at16;
-                                uint32_t* w = &v.x;
-                                bool wild = false;
+                    if (!kSelected) {
+                        // Values no row may see are zeroed (0 x NaN is NaN); values only some rows may see
+                        // are searched for such, which the softmax warps then look up themselves.
+                        const int left = keys - (tile0 + i) * kTile;       // keys of this tile
+                        const int all = minb - (tile0 + i) * kTile;        // ... that every row sees
+                        if (left < kTile || all < left) {
+                            const int from = min(max(all, 0), min(left, kTile));
+                            for (int x = lane; x < (kTile - from) * DH * 8; x += 32) {
+                                const int r = from + x / (DH * 8), c = x % (DH * 8);
+                                uint8_t* at8 = va + (c >> 3) * kTile * 128 + r * 128 + (c & 7) * 16;
+                                uint4* at16 = reinterpret_cast<uint4*>(at8);
+                                if (r >= left) {
+                                    *at16 = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    uint4 v = *at16;
+                                    uint32_t* w = &v.x;
+                                    bool wild = false;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (half_wild<T>(w[j])) w[j] &= 0xFFFF0000u, wild = true;
-                                    if (half_wild<T>(w[j] >> 16)) w[j] &= 0x0000FFFFu, wild = true;
-                                }
-                                if (wild) {
-                                    *at16 = v;
-                                    pc.poison = 1;
+                                    for (int j = 0; j < 4; ++j) {
+                                        if (half_wild<T>(w[j])) w[j] &= 0xFFFF0000u, wild = true;
+                                        if (half_wild<T>(w[j] >> 16)) w[j] &= 0x0000FFFFu, wild = true;
+                                    }
+                                    if (wild) {
+                                        *at16 = v;
+                                        pc.poison = 1;
+                                    }
                                 }
                             }
+                            fence_proxy_async_smem();
+                            __syncwarp();
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
                     }
-                }
                 }
                 ok = warp_wait(&sh.pfull[slot][h], (ph_p >> h) & 1, abort, p.status);
                 if (!ok) break;
@@ -1292,7 +1303,9 @@ __global__ void __launch_bounds__(att_threads<kSelected, kNarrow>(), 1)
         uint32_t steps_done = 0;
         int npiece = 0;
         bool ok = true;
-        // The row's two warps meet; bounded, as every wait is that another role may leave unanswered.
+        // The row's two warps meet; bounded, as every wait is that another role may leave unanswered.  (At a named
+        // barrier, which has no limit, 320 rows behind 32768 keys took 476 us, so 484; 17 rows behind 4001 keys 16.4
+        // and 17.0.)
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.xch[slot][quarter]);
@@ -1900,7 +1913,8 @@ extern "C" int dsa_attend_paged(const dsa_kv_cache* cache, const void* q, int64_
     p.lse = lse, p.status = status;
     p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
     p.kv_heads = static_cast<int>(cache->heads), p.dim = static_cast<int>(cache->dim);
-    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0, p.num_pages = static_cast<int>(cache->num_pages);
+    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
+    p.num_pages = static_cast<int>(cache->num_pages);
     p.prefix_len = static_cast<int>(prefix_len);
     p.scale_log2 = scale * kLog2e;
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
@@ -1952,7 +1966,8 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
                           row_ends, num_requests, rows, scale, out, out_row_stride, out_head_stride, workspace);
     if (rc != DSA_OK) return rc;
     if (k < 0 || (k > 0 && rows > 0 && (!topk || topk_stride < k))) return DSA_ERR_INVALID;
-    if (k > (int64_t(1) << 24) || (k / kTile + 1) * cache->heads > 0x7FFFFFFF || cache->num_pages > (1 << 25)) return DSA_ERR_UNSUPPORTED;
+    if (k > (int64_t(1) << 24) || (k / kTile + 1) * cache->heads > 0x7FFFFFFF || cache->num_pages > (1 << 25))
+        return DSA_ERR_UNSUPPORTED;
     if (rows == 0) return DSA_OK;
     AttCall a = {};
     // (an empty list is one key long in the workspace: the rows still need their zeros)
@@ -1965,7 +1980,8 @@ extern "C" int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int
     p.lse = lse, p.status = status;
     p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
     p.kv_heads = static_cast<int>(cache->heads), p.dim = static_cast<int>(cache->dim);
-    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0, p.num_pages = static_cast<int>(cache->num_pages);
+    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
+    p.num_pages = static_cast<int>(cache->num_pages);
     p.scale_log2 = scale * kLog2e;
     fill_params(a, cache, static_cast<uint8_t*>(workspace));
     rc = query_map(&a.q, cache, q, q_row_stride, q_head_stride, rows, heads, 1);
