@@ -210,7 +210,8 @@ __device__ int64_t lay_out(const AttParams& p, const Axis& ax, int64_t* tmp, int
                 s1 = min(max(b, s0), p.rows);
             }
             const int nseg = (s1 - s0 + p.own_rps - 1) / p.own_rps;
-            const int at = carry + static_cast<int>(block_scan64(nseg, tmp, total)) - nseg;
+            // (requests that overlap may claim more segments than 32 bits count)
+            const int64_t at = carry + block_scan64(nseg, tmp, total) - nseg;
             for (int i = 0; i < nseg; ++i) {
                 if (at + i >= p.max_segs) {   // overlapping requests
                     bad = true;
