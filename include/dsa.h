@@ -604,6 +604,113 @@ int dsa_attend_selected(const dsa_kv_cache* cache, const void* q, int64_t q_row_
                         int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
                         size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The same cache in 4 bits: the append quantises, the attention reads codes.
+ */
+
+/*
+ * A paged key/value cache in NVFP4: E2M1 codes with one E4M3 scale for every 16
+ * columns of a token's head, and an FP32 scale for all keys and one for all
+ * values.  A code c under the scale s stands for (c * s) * k_scale (values:
+ * v_scale).  Head h of page p (64 tokens) is one section of
+ * dsa_kv_section_bytes_fp4(dim) = 64 (dim + 2 R) bytes, R = 4 ceil(dim / 64), at
+ * data + p * page_stride + h * head_stride:
+ *   64 rows of dim / 2 bytes  key codes, column 2j in the low half of byte j
+ *   64 rows of dim / 2 bytes  value codes, likewise
+ *   64 rows of 2 R bytes      the key's dim / 16 scales at byte 0, the value's at byte R
+ *                             (the other bytes of a row are neither read nor written)
+ * data 16-byte aligned; strides in bytes, multiples of 16 (layers may share a
+ * pool).  dim a multiple of 16 up to 128, else DSA_ERR_UNSUPPORTED.
+ * 2^-64 <= k_scale, v_scale <= 2^64; the largest magnitude that the cache holds is
+ * 2688 times its scale, and a scale of (largest |x|) / 2688 uses the range best.
+ */
+typedef struct {
+    void* data;
+    int64_t page_stride, head_stride;
+    int64_t num_pages;
+    int64_t heads;   /* key/value heads */
+    int64_t dim;     /* columns per head */
+    float k_scale, v_scale;
+} dsa_kv_cache_fp4;
+
+/* dsa_kv_section_bytes_fp4 - bytes of one head of one page; 0 for a dim the calls refuse. */
+size_t dsa_kv_section_bytes_fp4(int64_t dim);
+
+/*
+ * dsa_kv_append_fp4 - dsa_kv_append into a 4-bit cache: keys (rotated) and values
+ * are quantised as they are written.
+ *
+ * Arguments, padding, status bits and refusals as dsa_kv_append; dtype is that of
+ * k, v, q and q_out.  Rotated queries are rounded to dtype as there; a rotated key
+ * stays in FP32 until it is quantised.  A block of 16 columns x gets
+ *   s = E4M3(max |x| / (6 g)), codes E2M1(x / (s g)), g = k_scale or v_scale,
+ * products and quotients correctly rounded in FP32, conversions to nearest (ties to
+ * even) and to the largest magnitude where a value is past it; s = 0 makes every
+ * code a zero.  A block with a NaN gets the scale NaN (it reads as NaN) and codes of
+ * the largest magnitude; an infinite value becomes the largest magnitude of its block, 2688 g.
+ */
+int dsa_kv_append_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* k, int64_t k_token_stride,
+                      int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                      const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, void* q_out,
+                      int64_t qo_token_stride, int64_t qo_head_stride, int64_t n, const int64_t* slots,
+                      const int64_t* positions, const float* cos_sin, int64_t cs_stride, int64_t max_pos,
+                      int64_t rot_dim, int interleaved, int32_t* status, void* stream);
+
+/*
+ * dsa_kv_read_fp4 - the keys and values that a 4-bit cache holds in slots.
+ *
+ *   slots         int64 [n]: slot = page * 64 + offset; < 0 = padding, whose rows are
+ *                 written zero; >= num_pages * 64 likewise, flagged DSA_STATUS_BAD_SLOT.
+ *   k_out, v_out  [n][cache->heads][dim] of dtype, (c * s) * g in FP32 rounded once; token
+ *                 and head strides in elements, multiples of 8, 0 over one element only;
+ *                 16-byte aligned.
+ */
+int dsa_kv_read_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const int64_t* slots, int64_t n, void* k_out,
+                    int64_t k_token_stride, int64_t k_head_stride, void* v_out, int64_t v_token_stride,
+                    int64_t v_head_stride, int32_t* status, void* stream);
+
+/*
+ * dsa_attend_workspace_size_fp4 - bytes of scratch dsa_attend_paged_fp4 (k = 0) or
+ * dsa_attend_selected_fp4 (k = list length, 1 for empty lists; max_query_len is not
+ * used) needs; otherwise as dsa_attend_workspace_size.
+ */
+size_t dsa_attend_workspace_size_fp4(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads, int64_t dim,
+                                     int64_t max_query_len, int64_t k);
+
+/*
+ * dsa_attend_paged_fp4 - dsa_attend_paged over a 4-bit cache, without a prefix.
+ *
+ * Arguments as dsa_attend_paged; dtype is that of q and out.  The codes enter the
+ * products as the FP16 values they stand for without their cache's FP32 scale
+ * (exact), queries as FP16 after a power of two that puts a head's largest |q| next
+ * to 2^14 (columns under 2^-28 of it lose bits), softmax weights rounded to FP16;
+ * sums are FP32.
+ * Keys a row may not see do not reach its output.  A visible scale that is NaN
+ * makes what it enters NaN: a key's the whole row, a value's its 16 output columns.
+ * Queries are finite (else the rows of the tile's head are unspecified).  Keys of
+ * a page outside the pool are skipped (DSA_STATUS_BAD_PAGE).
+ */
+int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* q, int64_t q_row_stride,
+                         int64_t q_head_stride, int64_t heads, const int32_t* block_table, int64_t bt_stride,
+                         int64_t max_pages, const int32_t* starts, const int32_t* row_ends, int64_t num_requests,
+                         int64_t rows, int64_t max_query_len, float scale, void* out, int64_t out_row_stride,
+                         int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                         int32_t* status, void* stream);
+
+/*
+ * dsa_attend_selected_fp4 - dsa_attend_selected over a 4-bit cache.
+ *
+ * Lists as dsa_attend_selected (negative entries are empty, entries past the bound
+ * flagged and skipped, a position listed twice counts twice); the rest as
+ * dsa_attend_paged_fp4.
+ */
+int dsa_attend_selected_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* q, int64_t q_row_stride,
+                            int64_t q_head_stride, int64_t heads, const int32_t* block_table, int64_t bt_stride,
+                            int64_t max_pages, const int32_t* starts, const int32_t* row_ends, int64_t num_requests,
+                            int64_t rows, const int32_t* topk, int64_t topk_stride, int64_t k, float scale, void* out,
+                            int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream);
+
 /*
  * dsa_set_score_timing - profiling hook: when both events are non-NULL,
  * dsa_score_paged records `before` just ahead of its scoring kernel and

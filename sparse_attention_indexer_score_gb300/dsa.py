@@ -68,6 +68,15 @@ _SIGS = {
                                     _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
     "dsa_attend_selected": (_c.c_int, [_P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I64,
                                        _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
+    "dsa_kv_section_bytes_fp4": (_c.c_size_t, [_I64]),
+    "dsa_kv_append_fp4": (_c.c_int, [_P, _c.c_int32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64,
+                                     _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _c.c_int, _P, _P]),
+    "dsa_kv_read_fp4": (_c.c_int, [_P, _c.c_int32, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]),
+    "dsa_attend_workspace_size_fp4": (_c.c_size_t, [_I64] * 7),
+    "dsa_attend_paged_fp4": (_c.c_int, [_P, _c.c_int32, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64,
+                                        _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
+    "dsa_attend_selected_fp4": (_c.c_int, [_P, _c.c_int32, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64,
+                                           _P, _I64, _I64, _c.c_float, _P, _I64, _I64, _P, _P, _c.c_size_t, _P, _P]),
 }
 
 
@@ -481,6 +490,76 @@ def attend_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     arguments and results as ``attend_paged``."""
     return (_binding or _native()).attend_selected(q, k_cache, v_cache, block_table, starts, row_ends, topk, scale,
                                                    out, want_lse, workspace, status)
+
+
+class KvCacheFp4(_c.Structure):
+    """``dsa_kv_cache_fp4``: the pool of sections with its strides in bytes, and its two FP32 scales."""
+
+    _fields_ = [("data", _P), ("page_stride", _I64), ("head_stride", _I64), ("num_pages", _I64), ("heads", _I64),
+                ("dim", _I64), ("k_scale", _c.c_float), ("v_scale", _c.c_float)]
+
+
+def kv_section_bytes_fp4(dim: int) -> int:
+    """Bytes that 64 tokens' keys and values of one head of ``dim`` columns take in the 4-bit cache."""
+    n = int(lib().dsa_kv_section_bytes_fp4(dim))
+    if n == 0:
+        raise ValueError("a 4-bit cache's heads have a multiple of 16 columns, at most 128")
+    return n
+
+
+def new_kv_cache_fp4(num_pages: int, heads: int, dim: int, device) -> torch.Tensor:
+    """A zero-filled 4-bit cache, uint8 [pages, heads, section] (NVFP4: E2M1 codes, an E4M3 scale per 16 columns;
+    the layout of a section stands at ``dsa_kv_cache_fp4`` in ``include/dsa.h``)."""
+    return torch.zeros((max(int(num_pages), 0), heads, kv_section_bytes_fp4(dim)), dtype=torch.uint8, device=device)
+
+
+def kv_append_fp4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  k_scale: float = 1.0, v_scale: float = 1.0,
+                  status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """``kv_append`` into a 4-bit cache (``new_kv_cache_fp4``, or a view of a larger one): keys, rotated, and values
+    are quantised as they are written.  ``k_scale`` and ``v_scale`` are the cache's FP32 scales, which every call on
+    it gets alike: it holds magnitudes of up to 2688 times its scale."""
+    return (_binding or _native()).kv_append_fp4(k, v, slots, cache, positions, cos_sin, q, q_out, interleaved, k_scale,
+                                                 v_scale, status)
+
+
+def kv_read_fp4(slots: torch.Tensor, cache: torch.Tensor, dim: int, dtype: torch.dtype = torch.bfloat16,
+                k_scale: float = 1.0, v_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
+                v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """The keys and values [n, heads, dim] that a 4-bit cache holds in slots (int64 [n]; < 0 is padding, whose rows
+    are zeros), in BF16 or FP16.  Returns (k, v), which are ``k_out`` and ``v_out`` where given."""
+    return (_binding or _native()).kv_read_fp4(slots, cache, dim, dtype, k_scale, v_scale, k_out, v_out, status)
+
+
+def attend_workspace_size_fp4(rows: int, num_requests: int, heads: int, kv_heads: int, dim: int, max_query_len: int,
+                              k: int = 0) -> int:
+    """Bytes of scratch of ``attend_paged_fp4`` (k = 0) or ``attend_selected_fp4`` (k = the list length, 1 for empty
+    lists); a workspace is kept and shared as ``attend_workspace_size``'s."""
+    return int(lib().dsa_attend_workspace_size_fp4(rows, num_requests, heads, kv_heads, dim, max_query_len, k))
+
+
+def attend_paged_fp4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, starts: torch.Tensor,
+                     row_ends: torch.Tensor, max_query_len: int, scale: Optional[float] = None, k_scale: float = 1.0,
+                     v_scale: float = 1.0, out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                     workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """``attend_paged`` over a 4-bit cache, without a shared prefix: decode rows q [rows, heads, dim] (BF16 or FP16,
+    the type of the output) see keys t < row_ends[r] of their request.  Returns (out, lse FP32 [rows, heads] or
+    None)."""
+    return (_binding or _native()).attend_paged_fp4(q, cache, block_table, starts, row_ends, max_query_len, scale,
+                                                    k_scale, v_scale, out, want_lse, workspace, status)
+
+
+def attend_selected_fp4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, starts: torch.Tensor,
+                        row_ends: torch.Tensor, topk: torch.Tensor, scale: Optional[float] = None,
+                        k_scale: float = 1.0, v_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                        want_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None):
+    """``attend_selected`` over a 4-bit cache: the key positions of ``topk`` (int32 [rows, k], the indexer's
+    selection; negative entries are empty).  Other arguments and results as ``attend_paged_fp4``."""
+    return (_binding or _native()).attend_selected_fp4(q, cache, block_table, starts, row_ends, topk, scale, k_scale,
+                                                       v_scale, out, want_lse, workspace, status)
 
 
 class TimingEvent:
