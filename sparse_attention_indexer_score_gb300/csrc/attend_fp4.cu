@@ -28,6 +28,7 @@ namespace dsa {
 
 constexpr int kUnit = kPage;            // keys of a unit
 constexpr int kMaxCtas4 = 160;          // workspaces are sized for at most this many CTAs
+constexpr int kMaxWorkers4 = 12;        // ... of this many workers
 constexpr int kCtaRequests = 512;       // up to this many requests every CTA lays out the axis itself
 constexpr int kPlan4Threads = 512;
 constexpr float kLog2e4 = 1.4426950408889634f;
@@ -74,7 +75,7 @@ struct Att4Params {
     int32_t* status;
     int R, rows, heads, group, kv_heads, dim, max_keys, num_pages;
     int k, list_units, list_tiles;   // listed keys: units an item, row tiles a head
-    int nt, cap, warps;              // warps: of the whole grid
+    int nt, cap, workers;            // workers: of the whole grid
     int bf16;                        // type of q and out (else FP16)
     int section, stage;              // bytes of a section, and of a ring stage
     int plan_in_cta;
@@ -173,28 +174,35 @@ __global__ void __launch_bounds__(kPlan4Threads) attend_fp4_plan_kernel(const At
 }
 
 // ----------------------------------------------------------------- attention
-// The forms of a head: 128 columns, 64 columns, any other (in the place of 128).
-enum Form { kForm128 = 0, kForm64 = 1, kFormAny = 2 };
+constexpr int kSmemMost4 = 227 * 1024;
 
-template <int NT, bool kSelected>
+// The forms of a head: 128 columns, 64 columns, others up to 128, others up to 64.
+enum Form { kForm128 = 0, kForm64 = 1, kFormAny128 = 2, kFormAny64 = 3 };
+constexpr bool wide(Form f) { return f == kForm128 || f == kFormAny128; }
+
+// NT column tiles of 8 query rows.  A worker is a warp, or for wide heads under
+// more than 8 query rows a team of two: each scores half of a unit's keys and has
+// the values of half of the columns, so that neither the codes are converted twice
+// nor the accumulators (8 NT registers for 16 columns) leave the registers.
+template <Form kForm, int NT, bool kSelected>
 struct Shape4 {
-    static constexpr bool kQShared = NT > 2;               // query operands in shared memory, not in registers
-    static constexpr int kWarps = NT == 1 ? 12 : 8;
-    static constexpr int kStages = NT == 2 ? 3 : 2;
-    static constexpr int kMT = NT > 2 ? 2 : 4;             // key tiles of 16 whose scores are in registers at once
+    static constexpr int kTeam = NT > 1 && wide(kForm) ? 2 : 1;
+    static constexpr int kWarps = kTeam == 2 ? (NT == 2 ? 16 : 12) : NT == 4 ? 8 : 12;
+    static constexpr int kStages = 2;
+    static constexpr int kWorkers = kWarps / kTeam;
+    static constexpr int kLead = kTeam == 2 ? kStages - 1 : kStages;   // units whose copies are ahead of the one begun
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ float ex2_4(float x) {
@@ -202,91 +210,102 @@ __device__ __forceinline__ float ex2_4(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint32_t v;
-    asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void sts8(uint32_t a, uint32_t x) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+template <typename V>
+__device__ __forceinline__ V lds(const uint8_t* a) {
+    return *reinterpret_cast<const V*>(a);
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async16s(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 // NaN among four E4M3 bytes (not zero if so).
 __device__ __forceinline__ uint32_t nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// A unit of a warp's share: worked out by a lane, read by the warp.
-struct __align__(16) Unit4 {
-    int page;               // its page, -1: none in the pool (listed keys: the row's request, -1: none)
-    int at, n;              // unit of its item, units of the item
-    int kvh;                // key head
-    int row0, first, nq;    // first query row of the request; first (row, head) of the tile, how many
-    int bound;              // listed keys: positions from here on are not the row's
-    uint64_t listed;        // which of the unit's keys are listed
-    uint64_t pad;
+// A unit of a worker's share, as a lane works it out.
+struct Unit4 {
+    int page;           // its page, -1: none in the pool (listed keys: the row's request, -1: none)
+    int kvh;            // key head
+    int at, row;        // listed keys: its place in its item, the row,
+    int bound;          // ... and the positions from which on keys are not the row's
+};
+
+// An item: query rows (row0 + (first + n) / group, head kvh * group + (first + n) % group), n < nq.
+struct Item4 {
+    int row0, first, nq, kvh;
+    int at, n;          // the unit asked for, and the item's units
+};
+
+// What a worker keeps in shared memory besides its ring.
+template <int kSteps, int NT>
+struct QueryDesk {
+    uint2 q[kSteps][NT][32];              // query operands: step, column tile, lane
+};
+template <int kSteps>
+struct QueryDesk<kSteps, 1> {};           // (one column tile's are in registers)
+template <int NT, bool kTeamed>
+struct TeamDesk {
+    uint2 p[4][NT][32];                   // weights as operands: key tile, column tile, lane
+    float top[2][8 * NT], sum[2][8 * NT]; // maxima and sums of the two warps' keys
+};
+template <int NT>
+struct TeamDesk<NT, false> {};
+template <bool kSelected>
+struct ListDesk {
+    int64_t rows[kSelected ? kUnit : 1];  // where listed tokens' codes are
+};
+
+template <Form kForm, int NT, bool kSelected>
+struct Desk4 : QueryDesk<wide(kForm) ? 8 : 4, NT>,
+               TeamDesk<NT, Shape4<kForm, NT, kSelected>::kTeam == 2>,
+               ListDesk<kSelected> {
+    float c[8 * NT];                      // log2(e) scale of the query rows' scores
+    int ends[8 * NT];                     // their bounds
+    uint64_t full[Shape4<kForm, NT, kSelected>::kStages];       // pages: copies that landed
+    uint32_t listed[Shape4<kForm, NT, kSelected>::kStages][2];  // which of a unit's keys are listed
+    int abort;
 };
 
 template <Form kForm, int NT, bool kSelected>
 struct Worker4 {
-    using S4 = Shape4<NT, kSelected>;
-    static constexpr int kBlocks = kForm == kForm64 ? 4 : 8;   // blocks of 16 columns in registers
-    static constexpr int kSteps = kBlocks;                     // steps of 16 columns of the scores' product
-    static constexpr int kOT = kBlocks;                        // tiles of 16 value columns
-    static constexpr int kQ = S4::kQShared ? 1 : kSteps;
+    using S4 = Shape4<kForm, NT, kSelected>;
+    using Desk = Desk4<kForm, NT, kSelected>;
+    static constexpr int kTeam = S4::kTeam;
+    static constexpr int kBlocks = wide(kForm) ? 8 : 4;        // blocks of 16 columns in the scores' product
+    static constexpr int kSteps = kBlocks;                     // ... a step each
+    static constexpr int kMT = kUnit / 16 / kTeam;             // key tiles of 16 that the warp scores
+    static constexpr int kOT = kBlocks / kTeam;                // tiles of 16 value columns that it has
 
     const Att4Params& p;
-    int lane, g, t;
-    // the item
-    uint32_t qf[kQ][S4::kQShared ? 1 : NT][2];
-    uint32_t q_smem;                  // query operands in shared memory
+    Desk& desk;
+    int lane, g, t, half;
+    uint2 q1[NT == 1 ? kSteps : 1];   // query operands of one column tile
     float o[kOT][NT][4];
     float m[NT][2], l[NT][2], c[NT][2];
-    int end[NT][2];
-    int row0, first, nq, kvh;         // first query row of the request, first (row, head) of the tile, how many, key head
-    int least, most;                  // bounds of the tile's rows
+    Item4 item;
+    int least;                        // the smallest bound of the item's rows
 
-    __device__ __forceinline__ explicit Worker4(const Att4Params& params) : p(params) {
+    __device__ __forceinline__ Worker4(const Att4Params& params, Desk& d) : p(params), desk(d) {
         lane = threadIdx.x & 31;
         g = lane >> 2, t = lane & 3;
+        half = kTeam == 2 ? (threadIdx.x >> 5) & 1 : 0;
     }
 
     __device__ __forceinline__ int nblk() const { return kForm == kForm128 ? 8 : kForm == kForm64 ? 4 : p.dim / 16; }
-    __device__ __forceinline__ int row_bytes() const { return kForm == kForm128 ? 64 : kForm == kForm64 ? 32 : p.dim / 2; }
-    __device__ __forceinline__ int scale_row() const { return kForm == kForm128 ? 8 : kForm == kForm64 ? 4 : fp4_scale_row(p.dim); }
-    // The bytes of a scale row's word from `first` on that are scales (the row's padding holds anything).
-    __device__ __forceinline__ uint32_t scale_bytes(int first) const {
-        return kForm != kFormAny || nblk() >= first + 4 ? ~0u : (1u << 8 * (nblk() - first)) - 1;
+    __device__ __forceinline__ int row_bytes() const { return 8 * nblk(); }
+    __device__ __forceinline__ int scale_row() const { return wide(kForm) ? 8 : 4; }
+    __device__ __forceinline__ int codes_bytes() const { return kPage * row_bytes(); }
+    __device__ __forceinline__ int v_off() const { return codes_bytes(); }
+    __device__ __forceinline__ int s_off() const { return 2 * codes_bytes(); }
+
+    // The warps of the worker have all come here.
+    __device__ __forceinline__ void meet() const {
+        if constexpr (kTeam == 2)
+            asm volatile("bar.sync %0, 64;" ::"r"(static_cast<int>(threadIdx.x >> 6) + 1) : "memory");
+        else
+            __syncwarp();
     }
-    __device__ __forceinline__ int k_off() const { return 0; }
-    __device__ __forceinline__ int v_off() const { return kPage * row_bytes(); }
-    __device__ __forceinline__ int s_off() const { return 2 * kPage * row_bytes(); }
 
     // Which key of eight is operand row i: neighbours differ in parity, and so do those two apart
     // (rows of keys and of values then meet in fewer banks).
@@ -294,110 +313,111 @@ struct Worker4 {
 
     // The block of 16 columns that a thread has in step s of the scores' product (four columns of it).
     __device__ __forceinline__ int step_block(int s) const {
-        return kForm == kForm128 ? 2 * t + (s >> 2) : kForm == kForm64 ? t : t + (s & 4);
+        return kForm == kForm128 ? 2 * t + (s >> 2) : t + (s & 4);
     }
+    // The thread's value columns, 2 kOT one behind the other, and their block.
+    __device__ __forceinline__ int columns() const { return half * 64 + g * 2 * kOT; }
+    __device__ __forceinline__ int block() const { return kOT == 8 ? g : half * 4 + (g >> 1); }
 
-    // Query operands, bounds and factors of the item: rows first .. first + nq - 1 of (row, head) pairs of the
-    // request whose rows start at row0.
-    __device__ __forceinline__ void begin(int row0_, int first_, int nq_, int kvh_) {
-        row0 = row0_, first = first_, nq = nq_, kvh = kvh_;
-        least = 0x7FFFFFFF, most = 0;
+    // Query operands, bounds and factors of an item.
+    __device__ __forceinline__ void begin(const Item4& x) {
+        item = x;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j0 = 0; j0 < NT; j0 += kTeam) {
+            const int j = j0 + half;
             const int n = 8 * j + g;
-            const bool on = n < nq;
-            const int at = first + (on ? n : 0);
-            const int row = row0 + at / p.group, head = kvh * p.group + at % p.group;
+            const bool on = n < x.nq;
+            const int at = x.first + (on ? n : 0);
+            const int row = x.row0 + at / p.group, head = x.kvh * p.group + at % p.group;
             const uint16_t* src = p.q + row * p.qrow + head * p.qhead;
             float f[kSteps][4];
             uint32_t top = 0;
 #pragma unroll
             for (int b = 0; b < kBlocks / 4; ++b) {   // the thread's blocks: steps 4b .. 4b + 3
-                const int block = step_block(4 * b);
+                const int blk = step_block(4 * b);
                 uint4 w[2] = {};
-                if (on && block < nblk()) {
-                    w[0] = __ldg(reinterpret_cast<const uint4*>(src + 16 * block));
-                    w[1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * block + 8));
+                if (on && blk < nblk()) {
+                    w[0] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk));
+                    w[1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk + 8));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 x = unpack2(p, (&w[i >> 2].x)[i & 3]);
-                    f[4 * b + i / 2][2 * (i & 1)] = x.x;
-                    f[4 * b + i / 2][2 * (i & 1) + 1] = x.y;
-                    top = max(top, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
+                    const float2 y = unpack2(p, (&w[i >> 2].x)[i & 3]);
+                    f[4 * b + i / 2][2 * (i & 1)] = y.x;
+                    f[4 * b + i / 2][2 * (i & 1) + 1] = y.y;
+                    top = max(top, max(__float_as_uint(y.x) & 0x7FFFFFFFu, __float_as_uint(y.y) & 0x7FFFFFFFu));
                 }
             }
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // 2^(14 - x) for the exponent x of the head's largest |q|
-            const int x = max(static_cast<int>(top >> 23) - 127, -112);
-            const float up = __int_as_float((127 + 14 - x) << 23);
-            const float down = x >= 14 ? __int_as_float((127 + x - 14) << 23) : 1.0f / up;
+            // 2^(14 - power) for the exponent of the head's largest |q|
+            const int power = max(static_cast<int>(top >> 23) - 127, -112);
+            const float up = __int_as_float((127 + 14 - power) << 23);
+            const float down = power >= 14 ? __int_as_float((127 + power - 14) << 23) : 1.0f / up;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const uint32_t b0 = Fp16::pack(f[s][0] * up, f[s][1] * up), b1 = Fp16::pack(f[s][2] * up, f[s][3] * up);
-                if constexpr (S4::kQShared) {
-                    sts64(q_smem + ((s * NT + j) * 32 + lane) * 8, b0, b1);
-                } else {
-                    qf[s][j][0] = b0, qf[s][j][1] = b1;
-                }
+            for (int s = 0; s < kSteps; ++s)
+            {
+                const uint2 b =
+                    make_uint2(Fp16::pack(f[s][0] * up, f[s][1] * up), Fp16::pack(f[s][2] * up, f[s][3] * up));
+                if constexpr (NT == 1) q1[s] = b;
+                else desk.q[s][j][lane] = b;
             }
-            const float cj = fminf(fmaxf(p.c * down, 1e-37f), 3e38f);
-            int e = 0;
-            if (on) {
-                e = min(max(p.row_ends[row], 0), p.max_keys);
-                least = min(least, e);
-                most = max(most, e);
+            if (t == 0) {
+                desk.c[n] = fminf(fmaxf(p.c * down, 1e-37f), 3e38f);
+                desk.ends[n] = on ? min(max(p.row_ends[row], 0), p.max_keys) : 0x7FFFFFFF;
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                c[j][i] = __shfl_sync(0xFFFFFFFFu, cj, (2 * t + i) * 4);
-                end[j][i] = __shfl_sync(0xFFFFFFFFu, e, (2 * t + i) * 4);
-                m[j][i] = -INFINITY;
-                l[j][i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < kOT; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
         }
+        meet();
+        least = 0x7FFFFFFF;
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        }
-        __syncwarp();
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = 8 * j + 2 * t + e;
+                c[j][e] = desk.c[n];
+                least = min(least, desk.ends[n]);
+                m[j][e] = -INFINITY;
+                l[j][e] = 0.0f;
+            }
+        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, 1));
+        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, 2));
+#pragma unroll
+        for (int i = 0; i < kOT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
     }
 
-    // A key's codes as operands of a step: two FP16 pairs of the thread's columns.
-    // Keys key0 .. of the stage, MT tiles of 16; scores in s.
-    __device__ __forceinline__ void scores(uint32_t stage, int key0, int nt, float (&s)[S4::kMT][NT][4]) {
+    // The scores of the warp's keys under the first N column tiles.
+    template <int N>
+    __device__ __forceinline__ void scores(const uint8_t* stage, float (&s)[kMT][N][4]) {
 #pragma unroll
-        for (int i = 0; i < S4::kMT; ++i)
+        for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
-        uint32_t w[S4::kMT][2][kBlocks / 2];   // words of 8 codes: rows g and g + 8
-        uint32_t sc[S4::kMT][2][kBlocks / 4];  // a scale twice
+            for (int j = 0; j < N; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
+        uint32_t w[kMT][2][kBlocks / 2];   // words of 8 codes: rows g and g + 8
+        uint32_t sc[kMT][2][kBlocks / 4];  // a scale twice
 #pragma unroll
-        for (int i = 0; i < S4::kMT; ++i)
+        for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int key = key0 + 16 * i + 8 * h + key_of(g);
-                const uint32_t row = stage + k_off() + key * row_bytes();
-                const uint32_t scales = stage + s_off() + key * 2 * scale_row();
+                const int key = 16 * (half * kMT + i) + 8 * h + key_of(g);
+                const uint8_t* row = stage + key * row_bytes();
+                const uint8_t* scales = stage + s_off() + key * 2 * scale_row();
                 if constexpr (kForm == kForm128) {
-                    const uint4 x = lds128(row + 16 * t);
+                    const uint4 x = lds<uint4>(row + 16 * t);
                     w[i][h][0] = x.x, w[i][h][1] = x.y, w[i][h][2] = x.z, w[i][h][3] = x.w;
-                    const uint32_t two = e4m3x2_f16(lds16(scales + 2 * t));
+                    const uint32_t two = e4m3x2_f16(lds<uint16_t>(scales + 2 * t));
                     sc[i][h][0] = __byte_perm(two, 0, 0x1010);
                     sc[i][h][1] = __byte_perm(two, 0, 0x3232);
                 } else {
 #pragma unroll
                     for (int b = 0; b < kBlocks / 4; ++b) {
-                        const int block = t + 4 * b;
+                        const int blk = t + 4 * b;
                         uint2 x = {0, 0};
                         uint32_t one = 0;
-                        if (kForm == kForm64 || block < nblk()) {
-                            x = lds64(row + 8 * block);
-                            one = lds8(scales + block);
+                        if (kForm == kForm64 || blk < nblk()) {
+                            x = lds<uint2>(row + 8 * blk);
+                            one = lds<uint8_t>(scales + blk);
                         }
                         w[i][h][2 * b] = x.x, w[i][h][2 * b + 1] = x.y;
                         sc[i][h][b] = __byte_perm(e4m3x2_f16(one), 0, 0x1010);
@@ -406,9 +426,16 @@ struct Worker4 {
             }
 #pragma unroll
         for (int x = 0; x < kSteps / 2; ++x) {   // a word: two steps
-            if (kForm == kFormAny && x >= 2 && nblk() <= 4) break;
+            uint2 qs[2][N];
 #pragma unroll
-            for (int i = 0; i < S4::kMT; ++i) {
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if constexpr (NT == 1) qs[z][j] = q1[2 * x + z];
+                    else qs[z][j] = desk.q[2 * x + z][j][lane];
+                }
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) {
                 uint32_t a[4], b[4];
                 e2m1x8(w[i][0][x], a);
                 e2m1x8(w[i][1][x], b);
@@ -420,46 +447,67 @@ struct Worker4 {
 #pragma unroll
                 for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j > 0 && j >= nt) break;
-                        uint2 qb;
-                        if constexpr (S4::kQShared) {
-                            qb = lds64(q_smem + (((2 * x + z) * NT + j) * 32 + lane) * 8);
-                        } else {
-                            qb = make_uint2(qf[2 * x + z][j][0], qf[2 * x + z][j][1]);
-                        }
-                        mma16816(s[i][j], a[2 * z], b[2 * z], a[2 * z + 1], b[2 * z + 1], qb.x, qb.y);
-                    }
+                    for (int j = 0; j < N; ++j)
+                        mma16816(s[i][j], a[2 * z], b[2 * z], a[2 * z + 1], b[2 * z + 1], qs[z][j].x, qs[z][j].y);
             }
         }
     }
 
-    // Weights of the scores, and the values under them.
-    __device__ __forceinline__ void values(uint32_t stage, int key0, int nt, float (&s)[S4::kMT][NT][4]) {
-        bool raised = false;
-        float ref[NT][2], keep[NT][2];
+    __device__ __forceinline__ bool sees(int j, int e, int key, int key_base, uint64_t listed) const {
+        return kSelected ? (listed >> key & 1) : key_base + key < desk.ends[8 * j + 2 * t + e];
+    }
+
+    // Scores of keys that a row does not see.
+    template <int N>
+    __device__ __forceinline__ void mask(int key_base, uint64_t listed, float (&s)[kMT][N][4]) {
+        if (kSelected ? listed == ~0ull : key_base + kUnit <= least) return;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j > 0 && j >= nt) break;
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 16 * (half * kMT + i) + 8 * (e >> 1) + key_of(g);
+                    if (!sees(j, e & 1, key, key_base, listed)) s[i][j][e] = -INFINITY;
+                }
+    }
+
+    // The largest score of each column among the warp's keys.
+    template <int N>
+    __device__ __forceinline__ void maxima(const float (&s)[kMT][N][4], float (&x)[N][2]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(s[0][j][e], s[0][j][e + 2]);
+                x[j][e] = fmaxf(s[0][j][e], s[0][j][e + 2]);
 #pragma unroll
-                for (int i = 1; i < S4::kMT; ++i) x = fmaxf(x, fmaxf(s[i][j][e], s[i][j][e + 2]));
-                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                x = fmaxf(x, m[j][e]);
-                raised |= x > m[j][e];
-                ref[j][e] = x == -INFINITY ? 0.0f : x;
-                keep[j][e] = ex2_4((m[j][e] - ref[j][e]) * c[j][e]);
-                m[j][e] = x;
+                for (int i = 1; i < kMT; ++i) x[j][e] = fmaxf(x[j][e], fmaxf(s[i][j][e], s[i][j][e + 2]));
+                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 4));
+                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 8));
+                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 16));
             }
-        }
+    }
+
+    // The weights of the warp's keys as operands, under the columns' maxima x of the unit; what there is so far is
+    // brought to the new maxima.
+    template <int N>
+    __device__ __forceinline__ void weights(const float (&s)[kMT][N][4], const float (&x)[N][2],
+                                            uint2 (&pb)[kMT][N]) {
+        bool raised = false;
+        float ref[N][2], keep[N][2];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float top = fmaxf(x[j][e], m[j][e]);
+                raised |= top > m[j][e];
+                ref[j][e] = top == -INFINITY ? 0.0f : top;
+                keep[j][e] = ex2_4((m[j][e] - ref[j][e]) * c[j][e]);
+                m[j][e] = top;
+            }
         if (__any_sync(0xFFFFFFFFu, raised)) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j > 0 && j >= nt) break;
+            for (int j = 0; j < N; ++j) {
                 l[j][0] *= keep[j][0], l[j][1] *= keep[j][1];
 #pragma unroll
                 for (int i = 0; i < kOT; ++i) {
@@ -468,12 +516,10 @@ struct Worker4 {
                 }
             }
         }
-        uint32_t pb[S4::kMT][NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j > 0 && j >= nt) break;
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int i = 0; i < S4::kMT; ++i) {
+            for (int i = 0; i < kMT; ++i) {
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -481,110 +527,153 @@ struct Worker4 {
                     w[e] = ex2_4(__fmaf_rn(s[i][j][e] - ref[j][e & 1], c[j][e & 1], kLift));
                     l[j][e & 1] += w[e];
                 }
-                pb[i][j][0] = transpose8x8(Fp16::pack(w[0], w[1]));
-                pb[i][j][1] = transpose8x8(Fp16::pack(w[2], w[3]));
+                pb[i][j] = make_uint2(transpose8x8(Fp16::pack(w[0], w[1])), transpose8x8(Fp16::pack(w[2], w[3])));
             }
-        }
-#pragma unroll
-        for (int i = 0; i < S4::kMT; ++i) {
-            uint2 v[4];          // codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 (operand rows), the thread's columns
-            uint32_t one[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int key = key0 + 16 * i + 8 * (z >> 1) + key_of(2 * t + (z & 1));
-                const uint32_t row = stage + v_off() + key * row_bytes();
-                const uint32_t scales = stage + s_off() + key * 2 * scale_row() + scale_row();
-                if constexpr (kForm == kForm64) {
-                    v[z] = make_uint2(lds32(row + 4 * g), 0);
-                    one[z] = lds8(scales + (g >> 1));
-                } else if (kForm == kForm128 || g < nblk()) {
-                    v[z] = lds64(row + 8 * g);
-                    one[z] = lds8(scales + g);
-                } else {
-                    v[z] = make_uint2(0, 0);
-                    one[z] = 0;
-                }
-            }
-            const uint32_t sa = e4m3x2_f16(one[0] | one[1] << 8), sb = e4m3x2_f16(one[2] | one[3] << 8);
-#pragma unroll
-            for (int x = 0; x < kOT / 4; ++x) {   // a word: four column tiles
-                const uint32_t k0 = x ? v[0].y : v[0].x, k1 = x ? v[1].y : v[1].x;
-                const uint32_t k2 = x ? v[2].y : v[2].x, k3 = x ? v[3].y : v[3].x;
-                uint32_t a0[4], a1[4], a2[4], a3[4];   // even columns (operand rows 0-7), odd columns (8-15)
-                e2m1x8((k0 & 0x0F0F0F0Fu) | (k1 << 4 & 0xF0F0F0F0u), a0);
-                e2m1x8((k0 >> 4 & 0x0F0F0F0Fu) | (k1 & 0xF0F0F0F0u), a1);
-                e2m1x8((k2 & 0x0F0F0F0Fu) | (k3 << 4 & 0xF0F0F0F0u), a2);
-                e2m1x8((k2 >> 4 & 0x0F0F0F0Fu) | (k3 & 0xF0F0F0F0u), a3);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    a0[z] = hmul2(a0[z], sa), a1[z] = hmul2(a1[z], sa);
-                    a2[z] = hmul2(a2[z], sb), a3[z] = hmul2(a3[z], sb);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j > 0 && j >= nt) break;
-                        mma16816(o[4 * x + z][j], a0[z], a1[z], a2[z], a3[z], pb[i][j][0], pb[i][j][1]);
-                    }
-                }
-            }
-        }
     }
 
-    __device__ __forceinline__ bool sees(int j, int e, int key, int key_base, uint64_t listed) const {
-        return kSelected ? (listed >> key & 1) : key_base + key < end[j][e];
+    // The values of key tile i under its weights.
+    template <int N>
+    __device__ __forceinline__ void values(const uint8_t* stage, int i, const uint2 (&pb)[N]) {
+        uint2 v[4];          // codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 (operand rows), the thread's columns
+        uint32_t one[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const int key = 16 * i + 8 * (z >> 1) + key_of(2 * t + (z & 1));
+            const uint8_t* row = stage + v_off() + key * row_bytes() + columns() / 2;
+            const uint8_t* scales = stage + s_off() + (key * 2 + 1) * scale_row();
+            v[z] = make_uint2(0, 0);
+            one[z] = 0;
+            if (kForm == kForm128 || kForm == kForm64 || block() < nblk()) {
+                if constexpr (kOT == 8) v[z] = lds<uint2>(row);
+                else v[z].x = lds<uint32_t>(row);
+                one[z] = lds<uint8_t>(scales + block());
+            }
+        }
+        const uint32_t sa = e4m3x2_f16(one[0] | one[1] << 8), sb = e4m3x2_f16(one[2] | one[3] << 8);
+#pragma unroll
+        for (int x = 0; x < kOT / 4; ++x) {   // a word: four column tiles
+            const uint32_t k0 = x ? v[0].y : v[0].x, k1 = x ? v[1].y : v[1].x;
+            const uint32_t k2 = x ? v[2].y : v[2].x, k3 = x ? v[3].y : v[3].x;
+            uint32_t a0[4], a1[4], a2[4], a3[4];   // even columns (operand rows 0-7), odd columns (8-15)
+            e2m1x8((k0 & 0x0F0F0F0Fu) | (k1 << 4 & 0xF0F0F0F0u), a0);
+            e2m1x8((k0 >> 4 & 0x0F0F0F0Fu) | (k1 & 0xF0F0F0F0u), a1);
+            e2m1x8((k2 & 0x0F0F0F0Fu) | (k3 << 4 & 0xF0F0F0F0u), a2);
+            e2m1x8((k2 >> 4 & 0x0F0F0F0Fu) | (k3 & 0xF0F0F0F0u), a3);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                a0[z] = hmul2(a0[z], sa), a1[z] = hmul2(a1[z], sa);
+                a2[z] = hmul2(a2[z], sb), a3[z] = hmul2(a3[z], sb);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    mma16816(o[4 * x + z][j], a0[z], a1[z], a2[z], a3[z], pb[j].x, pb[j].y);
+            }
+        }
     }
 
     // Value scales that are NaN: the columns they enter become NaN for the rows that see the key, and the bytes zero,
     // so that nobody else's do.
-    __device__ __forceinline__ void poison(uint32_t stage, int nt, int key_base, uint64_t listed) {
-        const int block = kForm == kForm64 ? g >> 1 : g;
+    template <int N>
+    __device__ __forceinline__ void poison(uint8_t* stage, int key_base, uint64_t listed) {
+        const int blk = block();
 #pragma unroll 1
         for (int key = 0; key < kUnit; ++key) {
-            const uint32_t at = stage + s_off() + (key * 2 + 1) * scale_row() + block;
-            const bool bad = block < nblk() && (lds8(at) & 0x7F) == 0x7F;
+            uint8_t* const at = stage + s_off() + (key * 2 + 1) * scale_row() + blk;
+            const bool bad = blk < nblk() && (lds<uint8_t>(at) & 0x7F) == 0x7F;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (bad && j < nt && sees(j, e, key, key_base, listed))
+                    if (bad && sees(j, e, key, key_base, listed))
 #pragma unroll
                         for (int i = 0; i < kOT; ++i) o[i][j][e] = o[i][j][e + 2] = __int_as_float(0x7FC00000);
             __syncwarp();
-            if (bad) sts8(at, 0);
+            if (bad) *at = 0;
         }
         __syncwarp();
         fence_proxy_async_smem();   // (the next copy into the stage is the asynchronous proxy's)
     }
 
-    // 64 keys of the stage; `listed`: which of them are listed.
-    __device__ __forceinline__ void unit(uint32_t stage, int key_base, uint64_t listed) {
-        const int nt = NT == 1 ? 1 : (nq + 7) / 8;
-        {   // two keys' value scales a lane
-            uint32_t bad = 0;
+    // Looks for value scales that are NaN among the warp's blocks, two keys a lane.
+    template <int N>
+    __device__ __forceinline__ void check(uint8_t* stage, int key_base, uint64_t listed) {
+        constexpr bool kBoth = wide(kForm) && kTeam == 1;   // two words of four blocks, or the warp's one
+        const int from = kTeam == 2 ? half * 4 : 0;
+        uint32_t bad = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t at = stage + s_off() + ((lane + 32 * h) * 2 + 1) * scale_row();
-                bad |= nan4(lds32(at) & scale_bytes(0));
-                if (kForm == kForm128 || (kForm == kFormAny && nblk() > 4)) bad |= nan4(lds32(at + 4) & scale_bytes(4));
-            }
-            if (__any_sync(0xFFFFFFFFu, bad != 0)) poison(stage, nt, key_base, listed);
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* at = stage + s_off() + ((lane + 32 * h) * 2 + 1) * scale_row();
+            bad |= nan4(lds<uint32_t>(at + from) & scale_bytes(from));
+            if (kBoth) bad |= nan4(lds<uint32_t>(at + 4) & scale_bytes(4));
         }
+        if (__any_sync(0xFFFFFFFFu, bad != 0)) poison<N>(stage, key_base, listed);
+    }
+    // The bytes of a scale row's word from `first` on that are scales (the row's padding holds anything).
+    __device__ __forceinline__ uint32_t scale_bytes(int first) const {
+        return kForm == kForm128 || kForm == kForm64 || nblk() >= first + 4 ? ~0u
+               : nblk() <= first                                             ? 0u
+                                                                             : (1u << 8 * (nblk() - first)) - 1;
+    }
+
+    // A unit that has landed in its stage (or not in time: true is returned).  `issue` orders the copies that the
+    // unit's progress makes room for.
+    template <int N, typename Issue>
+    __device__ __forceinline__ bool unit(uint8_t* stage, int key_base, uint64_t listed, bool any, Issue issue) {
+        float s[kMT][N][4], x[N][2];
+        uint2 pb[kMT][N];
+        if constexpr (kTeam == 1) {
+            __syncwarp();
+            if (!kSelected && *static_cast<volatile int*>(&desk.abort)) return true;
+            if (any) {
+                check<N>(stage, key_base, listed);
+                scores<N>(stage, s);
+                mask<N>(key_base, listed, s);
+                maxima<N>(s, x);
+                weights<N>(s, x, pb);
 #pragma unroll
-        for (int key0 = 0; key0 < kUnit; key0 += 16 * S4::kMT) {
-            float s[S4::kMT][NT][4];
-            scores(stage, key0, nt, s);
-            if (kSelected ? listed != ~0ull : key_base + kUnit > least) {
-#pragma unroll
-                for (int i = 0; i < S4::kMT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + 16 * i + 8 * (e >> 1) + key_of(g);
-                            if (!sees(j, e & 1, key, key_base, listed)) s[i][j][e] = -INFINITY;
-                        }
+                for (int i = 0; i < kMT; ++i) values<N>(stage, i, pb[i]);
             }
-            values(stage, key0, nt, s);
+            __syncwarp();
+            issue();
+            __syncwarp();
+        } else {
+            if (any) {
+                scores<N>(stage, s);
+                mask<N>(key_base, listed, s);
+                maxima<N>(s, x);
+                if (g == 0)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        *reinterpret_cast<float2*>(&desk.top[half][8 * j + 2 * t]) = make_float2(x[j][0], x[j][1]);
+            }
+            meet();
+            // (seen alike by both warps: neither waits for the next unit before they have met again)
+            const bool gave_up = !kSelected && *static_cast<volatile int*>(&desk.abort) != 0;
+            if (!gave_up) issue();
+            if (gave_up || !any) {
+                meet();
+                return gave_up;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float2 y = *reinterpret_cast<const float2*>(&desk.top[half ^ 1][8 * j + 2 * t]);
+                x[j][0] = fmaxf(x[j][0], y.x), x[j][1] = fmaxf(x[j][1], y.y);
+            }
+            check<N>(stage, key_base, listed);
+            weights<N>(s, x, pb);
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+#pragma unroll
+                for (int j = 0; j < N; ++j) desk.p[half * kMT + i][j][lane] = pb[i][j];
+            meet();
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i) {
+                uint2 w[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) w[j] = desk.p[i][j][lane];
+                values<N>(stage, i, w);
+            }
         }
+        return false;
     }
 
     // The item's result, or the partial one of a piece (slot >= 0).
@@ -593,27 +682,37 @@ struct Worker4 {
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[j][e];
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 4);
+                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 8);
+                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 16);
+                if constexpr (kTeam == 2)
+                    if (g == 0) desk.sum[half][8 * j + 2 * t + e] = l[j][e];
+            }
+        if constexpr (kTeam == 2) meet();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
                 const int n = 8 * j + 2 * t + e;
-                if (n >= nq) continue;
-                constexpr int kCols = 2 * kOT;   // the thread's columns, one behind the other
-                const bool cols = kForm != kFormAny || g < nblk();
+                if (n >= item.nq) continue;
+                float sum = l[j][e];
+                if constexpr (kTeam == 2) sum = desk.sum[0][n] + desk.sum[1][n];
+                const bool cols = kForm == kForm128 || kForm == kForm64 || block() < nblk();
+                const bool first = g == 0 && half == 0;
                 const float top = m[j][e] * c[j][e];
                 if (slot >= 0) {
-                    float* dst = p.po + (slot * p.cap + n) * p.dim + g * kCols;
+                    float* dst = p.po + (slot * p.cap + n) * p.dim + columns();
                     if (cols)
 #pragma unroll
                         for (int i = 0; i < kOT; i += 2)
                             *reinterpret_cast<float4*>(dst + 2 * i) =
                                 make_float4(o[i][j][e], o[i][j][e + 2], o[i + 1][j][e], o[i + 1][j][e + 2]);
-                    if (g == 0) p.pml[slot * p.cap + n] = make_float2(m[j][e] == -INFINITY ? -INFINITY : top, sum);
+                    if (first) p.pml[slot * p.cap + n] = make_float2(m[j][e] == -INFINITY ? -INFINITY : top, sum);
                 } else {
-                    const int row = row0 + (first + n) / p.group, head = kvh * p.group + (first + n) % p.group;
+                    const int row = item.row0 + (item.first + n) / p.group;
+                    const int head = item.kvh * p.group + (item.first + n) % p.group;
                     const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
-                    uint16_t* dst = p.out + row * p.orow + head * p.ohead + g * kCols;
+                    uint16_t* dst = p.out + row * p.orow + head * p.ohead + columns();
                     if (cols)
 #pragma unroll
                         for (int i = 0; i < kOT; i += 4)
@@ -622,7 +721,7 @@ struct Worker4 {
                                            pack2(p, o[i + 1][j][e] * inv, o[i + 1][j][e + 2] * inv),
                                            pack2(p, o[i + 2][j][e] * inv, o[i + 2][j][e + 2] * inv),
                                            pack2(p, o[i + 3][j][e] * inv, o[i + 3][j][e + 2] * inv));
-                    if (g == 0 && p.lse)
+                    if (first && p.lse)
                         p.lse[static_cast<int64_t>(row) * p.heads + head] =
                             sum == 0.0f ? -INFINITY : (top + log2f(sum) - kLift) * kLn2_4;
                 }
@@ -644,78 +743,85 @@ __device__ __forceinline__ int last_at_most(const I* starts, int n, I v) {
     return lo;
 }
 
-// Unit u of the axis.
-__device__ __forceinline__ Unit4 paged_unit(const Att4Params& p, const int64_t* prefix, const int* pages, int64_t u) {
+// Unit u of the axis: what a lane has to know of it, and its item.
+__device__ __forceinline__ Unit4 paged_unit(const Att4Params& p, const int64_t* prefix, const int* pages, int64_t u,
+                                            Item4* y = nullptr) {
     Unit4 x;
     const int j = last_at_most(prefix, p.R, u);
     const int64_t in = u - prefix[j];
-    x.n = pages[j];
-    const int item = in < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(x.n))
-                                             : static_cast<int>(in / x.n);
-    x.at = static_cast<int>(in - static_cast<int64_t>(item) * x.n);
+    const int n = pages[j];
+    const int item = in < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(n))
+                                             : static_cast<int>(in / n);
+    x.at = static_cast<int>(in - static_cast<int64_t>(item) * n);
+    const int row0 = min(max(p.starts[j], 0), p.rows);
+    const int all = (min(max(p.starts[j + 1], row0), p.rows) - row0) * p.group;
+    const int tiles = (all + p.cap - 1) / p.cap;
+    x.kvh = item / tiles;
+    if (y) {
+        const int first = (item - x.kvh * tiles) * p.cap;
+        *y = Item4{row0, first, min(p.cap, all - first), x.kvh, x.at, n};
+        return x;
+    }
     const int page = p.bt[j * p.bt_stride + x.at];
     x.page = page >= 0 && page < p.num_pages ? page : -1;
     if (x.page < 0 && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-    x.row0 = min(max(p.starts[j], 0), p.rows);
-    const int all = (min(max(p.starts[j + 1], x.row0), p.rows) - x.row0) * p.group;
-    const int tiles = (all + p.cap - 1) / p.cap;
-    x.kvh = item / tiles;
-    x.first = (item - x.kvh * tiles) * p.cap;
-    x.nq = min(p.cap, all - x.first);
-    x.bound = 0;
-    x.listed = 0;
+    x.row = x.bound = 0;
     return x;
 }
 
-__device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, int64_t u) {
+__device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, int64_t u, Item4* y = nullptr) {
     Unit4 x;
     const int per_row = p.kv_heads * p.list_tiles * p.list_units;
-    const int row = static_cast<int>(u / per_row);
-    const int in = static_cast<int>(u - static_cast<int64_t>(row) * per_row);
+    x.row = static_cast<int>(u / per_row);
+    const int in = static_cast<int>(u - static_cast<int64_t>(x.row) * per_row);
     const int item = in / p.list_units;
-    x.n = p.list_units;
     x.at = in - item * p.list_units;
     x.kvh = item / p.list_tiles;
-    x.first = (item - x.kvh * p.list_tiles) * p.cap;
-    x.nq = min(p.cap, p.group - x.first);
-    x.row0 = row;
-    const int j = p.R > 0 ? last_at_most(p.starts, p.R, row) : -1;
-    x.page = j >= 0 && p.starts[j] <= row && row < p.starts[j + 1] ? j : -1;
-    const int e = p.row_ends[row];
+    if (y) {
+        const int first = (item - x.kvh * p.list_tiles) * p.cap;
+        *y = Item4{x.row, first, min(p.cap, p.group - first), x.kvh, x.at, p.list_units};
+        return x;
+    }
+    const int j = p.R > 0 ? last_at_most(p.starts, p.R, x.row) : -1;
+    x.page = j >= 0 && p.starts[j] <= x.row && x.row < p.starts[j + 1] ? j : -1;
+    const int e = p.row_ends[x.row];
     x.bound = min(max(e, 0), p.max_keys);
     if (x.page >= 0 && e != x.bound && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
-    x.listed = 0;
     return x;
 }
 
+// Shared memory: the workers' rings, their desks, then the axis.
 template <Form kForm, int NT, bool kSelected>
-__global__ void __launch_bounds__((Shape4<NT, kSelected>::kWarps * 32), 1) attend_fp4_kernel(const Att4Params p) {
-    using S4 = Shape4<NT, kSelected>;
+__global__ void __launch_bounds__((Shape4<kForm, NT, kSelected>::kWarps * 32), 1)
+attend_fp4_kernel(const Att4Params p) {
+    using S4 = Shape4<kForm, NT, kSelected>;
     using W4 = Worker4<kForm, NT, kSelected>;
-    constexpr int kStages = S4::kStages, kWarps = S4::kWarps;
-    constexpr int kQBytes = S4::kQShared ? W4::kSteps * NT * 32 * 8 : 0;
+    using Desk = Desk4<kForm, NT, kSelected>;
+    constexpr int kTeam = S4::kTeam, kStages = S4::kStages, kLead = S4::kLead;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kWarps][kStages];
-    __shared__ Unit4 units[kWarps][kStages];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, worker = threadIdx.x / (32 * kTeam);
     pdl_wait();
     pdl_launch_dependents();
-    // ring stages, query operands, then the axis
-    uint8_t* const ring = smem + warp * kStages * p.stage;
-    uint8_t* const queries = smem + kWarps * kStages * p.stage;
-    if (!kSelected && lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
-        mbar_fence_init();
+    uint8_t* const ring = smem + worker * kStages * p.stage;
+    Desk& desk = reinterpret_cast<Desk*>(smem + S4::kWorkers * kStages * p.stage)[worker];
+    W4 k(p, desk);
+    const bool leads = k.half == 0;      // the warp that looks units up and orders pages
+    if (leads && lane == 0) {
+        if (!kSelected) {
+            for (int i = 0; i < kStages; ++i) mbar_init(&desk.full[i], 1);
+            mbar_fence_init();
+        }
+        desk.abort = 0;
     }
-    __syncwarp();
     const int64_t* prefix = p.prefix;
     const int* pages = p.pages;
     if (!kSelected && p.plan_in_cta) {
-        int64_t* const px = reinterpret_cast<int64_t*>(queries + kWarps * kQBytes);
+        int64_t* const px = reinterpret_cast<int64_t*>(smem + S4::kWorkers * (kStages * p.stage + sizeof(Desk)));
         int* const pg = reinterpret_cast<int*>(px + kCtaRequests + 1 + 33);
         lay_out4(p, px, pg, px + kCtaRequests + 1, blockIdx.x == 0);
         prefix = px, pages = pg;
     }
+    k.meet();
     if (kSelected && blockIdx.x == 0 && p.status) {
         bool bad = false;
         for (int j = threadIdx.x; j < p.R; j += blockDim.x) {
@@ -726,188 +832,182 @@ __global__ void __launch_bounds__((Shape4<NT, kSelected>::kWarps * 32), 1) atten
     }
     const int64_t total = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles * p.list_units
                                     : prefix[p.R];
-    const int64_t W = p.warps < total ? p.warps : total;
-    const int w = warp * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
+    const int64_t W = p.workers < total ? p.workers : total;
+    const int w = worker * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
     if (w >= W) return;
     const int64_t u0 = share4(w, total, W);
     const int count = static_cast<int>(share4(w + 1, total, W) - u0);
 
-    W4 k(p);
-    k.q_smem = smem_u32(queries) + warp * kQBytes;
-    // The share's units are looked up 32 at a time, one a lane; a unit's lane writes its record to its stage.
+    // The share's units are looked up 32 at a time, one a lane.
     Unit4 mine;
     auto look_up = [&](int base) {
         if (base + lane < count)
             mine = kSelected ? listed_unit(p, u0 + base + lane) : paged_unit(p, prefix, pages, u0 + base + lane);
     };
-    // Unit i of the share: its item's results so far, then its keys.
-    bool whole = true;   // the piece of the item begins with it
-    int begun = 0;       // ... and with this unit of the share
-    auto work = [&](int i, const Unit4& x, uint32_t stage, bool any) {
-        if (i == 0 || x.at == 0) {
-            whole = x.at == 0;
-            begun = i;
-            k.begin(x.row0, x.first, x.nq, x.kvh);
+    // A page's copy, by the unit's lane.
+    auto copy_page = [&](int i) {
+        if (i >= count) return;
+        if (i % 32 == 0) look_up(i);
+        if (lane == i % 32) {
+            uint64_t* const bar = &desk.full[i % kStages];
+            desk.listed[i % kStages][0] = mine.page >= 0;
+            if (mine.page >= 0) {
+                mbar_arrive_expect_tx(bar, p.section);
+                bulk_load(ring + (i % kStages) * p.stage, p.cache + mine.page * p.page_stride + mine.kvh * p.head_stride,
+                          p.section, bar);
+            } else {
+                mbar_arrive(bar);
+            }
         }
-        if (any) k.unit(stage, x.at * kUnit, x.listed);
-        // slot 2w: the piece that the share starts with; 2w + 1: one that starts inside it and does not end there
-        if (x.at == x.n - 1)
-            k.finish(whole ? -1 : 2 * static_cast<int64_t>(w));
-        else if (i == count - 1)
-            k.finish(2 * static_cast<int64_t>(w) + (begun > 0 ? 1 : 0));
     };
 
-    if constexpr (!kSelected) {
-        int abort = 0;
-        auto issue = [&](int i) {
-            if (i >= count) return;
-            if (i % 32 == 0) look_up(i);
-            if (lane == i % 32) {
-                const int s = i % kStages;
-                units[warp][s] = mine;
-                if (mine.page >= 0) {
-                    mbar_arrive_expect_tx(&full[warp][s], p.section);
-                    bulk_load(ring + s * p.stage, p.cache + mine.page * p.page_stride + mine.kvh * p.head_stride,
-                              p.section, &full[warp][s]);
-                } else {
-                    mbar_arrive(&full[warp][s]);
-                }
-            }
-        };
-        for (int i = 0; i < kStages; ++i) issue(i);
-        __syncwarp();
-        int i = 0;
-        for (; i < count; ++i) {
-            const int s = i % kStages;
-            const Unit4 x = units[warp][s];
-            const bool landed = mbar_wait(&full[warp][s], (i / kStages) & 1, &abort, p.status);
-            if (!__all_sync(0xFFFFFFFFu, landed)) break;
-            work(i, x, smem_u32(ring + s * p.stage), x.page >= 0);
-            __syncwarp();
-            issue(i + kStages);
-            __syncwarp();
+    // Listed keys: two tokens a lane, or one where two warps share them.  While a unit is in work, the pages of the
+    // unit kLead on are looked up and the positions of the one behind it loaded.
+    constexpr int kTokens = 2 / kTeam;
+    int pos[kTokens], page[kTokens], ahead[kTokens];
+    struct List {
+        int req, kvh, bound;
+    } next, later;                       // the units of pos / page, and of ahead
+    const int token0 = k.half * 32 + lane;
+    auto load_positions = [&](int i) {   // into ahead / later
+#pragma unroll
+        for (int h = 0; h < kTokens; ++h) ahead[h] = -1;
+        if (i >= count) return;
+        if (i % 32 == 0) look_up(i);
+        const int at = __shfl_sync(0xFFFFFFFFu, mine.at, i % 32), row = __shfl_sync(0xFFFFFFFFu, mine.row, i % 32);
+        later.req = __shfl_sync(0xFFFFFFFFu, mine.page, i % 32);
+        later.kvh = __shfl_sync(0xFFFFFFFFu, mine.kvh, i % 32);
+        later.bound = __shfl_sync(0xFFFFFFFFu, mine.bound, i % 32);
+        if (later.req < 0) return;
+        const int32_t* list = p.topk + row * p.topk_stride;
+#pragma unroll
+        for (int h = 0; h < kTokens; ++h) {
+            const int e = at * kUnit + token0 + 32 * h;
+            if (e < p.k) ahead[h] = list[e];
         }
-        if (i < count) {   // gave up: the copies in flight land before the CTA ends
-            const unsigned long long deadline = globaltimer() + kWaitLimitNs;
-            const int issued = min(i + kStages, count);
-            for (; i < issued; ++i) mbar_drain(&full[warp][i % kStages], (i / kStages) & 1, deadline, p.status);
+    };
+    auto load_pages = [&]() {            // ahead / later become pos, page / next
+        next = later;
+        bool bad = false;
+#pragma unroll
+        for (int h = 0; h < kTokens; ++h) {
+            pos[h] = ahead[h];
+            page[h] = -1;
+            if (pos[h] >= next.bound) {
+                bad |= pos[h] >= 0;
+                pos[h] = -1;
+            }
+            if (pos[h] >= 0) page[h] = p.bt[next.req * p.bt_stride + pos[h] / kPage];
         }
-    } else {
-        // Unit i + 2's rows of the pool are looked up and unit i + 3's positions loaded while unit i is in work.
-        int pos[2], page[2], ahead[2];
-        Unit4 next, later;   // the units of pos/page, and of ahead
-        auto shuffled = [&](int i) {
-            if (i % 32 == 0) look_up(i);
-            Unit4 x;
-            x.page = __shfl_sync(0xFFFFFFFFu, mine.page, i % 32);
-            x.at = __shfl_sync(0xFFFFFFFFu, mine.at, i % 32);
-            x.n = mine.n;
-            x.kvh = __shfl_sync(0xFFFFFFFFu, mine.kvh, i % 32);
-            x.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, i % 32);
-            x.first = __shfl_sync(0xFFFFFFFFu, mine.first, i % 32);
-            x.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, i % 32);
-            x.bound = __shfl_sync(0xFFFFFFFFu, mine.bound, i % 32);
-            x.listed = 0;
-            return x;
-        };
-        auto load_positions = [&](int i) {   // into ahead / later
-            ahead[0] = ahead[1] = -1;
-            if (i >= count) return;
-            later = shuffled(i);
-            if (later.page < 0) return;
-            const int32_t* list = p.topk + later.row0 * p.topk_stride;
+        if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    };
+    // Rows of codes are cut into pieces of 16 bytes (8 where rows are not multiples of 16).
+    constexpr int kPiece = kForm == kForm128 || kForm == kForm64 ? 16 : 8;
+    constexpr int kLanes = kForm == kForm128 ? 4 : kForm == kForm64 ? 2 : wide(kForm) ? 8 : 4;   // of a row
+    auto gather = [&](int i) {           // the unit of pos / page into its stage
+        if (i < count) {
+            uint8_t* const stage = ring + (i % kStages) * p.stage;
+            uint32_t any = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int e = later.at * kUnit + lane + 32 * h;
-                if (e < p.k) ahead[h] = list[e];
+            for (int h = 0; h < kTokens; ++h) {
+                const bool on = page[h] >= 0 && page[h] < p.num_pages;
+                if (pos[h] >= 0 && !on && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
+                // (tokens that are not there: any codes, and scales of zero)
+                const int token = pos[h] % kPage, sr = 2 * k.scale_row();
+                const int64_t section = on ? page[h] * p.page_stride + next.kvh * p.head_stride : 0;
+                desk.rows[token0 + 32 * h] = section + (on ? token * k.row_bytes() : 0);
+                const uint8_t* src = p.cache + section + k.s_off() + (on ? token * sr : 0);
+                const uint32_t to = smem_u32(stage + k.s_off() + (token0 + 32 * h) * sr);
+                if (p.num_pages > 0) {
+                    if (sr == 16) cp_async16s(to, src, on ? 16 : 0);
+                    else cp_async8(to, src, on ? 8 : 0);
+                }
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on);
+                any |= mask;
+                if (lane == 0) desk.listed[i % kStages][k.half + h] = mask;
             }
-        };
-        auto load_pages = [&]() {            // ahead / later become pos, page / next
-            next = later;
-            bool bad = false;
+            __syncwarp();
+            const int part = lane % kLanes;
+            if (any && part * kPiece < k.row_bytes()) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                pos[h] = ahead[h];
-                page[h] = -1;
-                if (pos[h] >= next.bound) {
-                    bad |= pos[h] >= 0;
-                    pos[h] = -1;
-                }
-                if (pos[h] >= 0) page[h] = p.bt[next.page * p.bt_stride + pos[h] / kPage];
-            }
-            if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
-        };
-        auto copy = [&](int i) {             // the rows of pos, page into the stage
-            if (i < count) {
-                const int s = i % kStages;
-                const uint32_t stage = smem_u32(ring + s * p.stage);
-                int64_t at[2];
-                bool on[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    on[h] = page[h] >= 0 && page[h] < p.num_pages;
-                    if (pos[h] >= 0 && !on[h] && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-                    at[h] = on[h] ? page[h] * p.page_stride + next.kvh * p.head_stride : 0;
-                }
-                const uint32_t lo = __ballot_sync(0xFFFFFFFFu, on[0]), hi = __ballot_sync(0xFFFFFFFFu, on[1]);
-                next.listed = static_cast<uint64_t>(hi) << 32 | lo;
-                if (lane == 0) {
-                    next.n = p.list_units;
-                    units[warp][s] = next;
-                }
-                if (next.listed) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int sr = 2 * k.scale_row();
-                        const uint8_t* src = p.cache + at[h] + (on[h] ? k.s_off() + (pos[h] % kPage) * sr : 0);
-                        const uint32_t dst = stage + k.s_off() + (lane + 32 * h) * sr;
-                        if (sr == 16) cp_async16s(dst, src, on[h] ? 16 : 0);
-                        else cp_async8(dst, src, on[h] ? 8 : 0);
-                        at[h] += on[h] ? (pos[h] % kPage) * k.row_bytes() : 0;
-                    }
-                    // rows of codes, cut into pieces of 16 bytes (8 where rows are not multiples of 16)
-                    constexpr int kPiece = kForm == kFormAny ? 8 : 16;
-                    constexpr int kLanes = kForm == kForm128 ? 4 : kForm == kForm64 ? 2 : 8;   // of a row
-                    const int part = lane & (kLanes - 1), row = lane / kLanes;
-                    const bool mine_too = part * kPiece < k.row_bytes();
-#pragma unroll 4
-                    for (int c = 0; c < kUnit / (32 / kLanes); ++c) {
-                        const int token = c * (32 / kLanes) + row;
-                        const int64_t a = __shfl_sync(0xFFFFFFFFu, c < kLanes ? at[0] : at[1], token & 31);
-                        const bool real = next.listed >> token & 1;
-                        const uint32_t dst = stage + token * k.row_bytes() + part * kPiece;
-                        const uint8_t* src = p.cache + a + (real ? part * kPiece : 0);
-                        if (mine_too) {
-                            if (kPiece == 16) {
-                                cp_async16s(dst, src, real ? 16 : 0);
-                                cp_async16s(dst + k.v_off(), src + (real ? k.v_off() : 0), real ? 16 : 0);
-                            } else {
-                                cp_async8(dst, src, real ? 8 : 0);
-                                cp_async8(dst + k.v_off(), src + (real ? k.v_off() : 0), real ? 8 : 0);
-                            }
-                        }
+                for (int c = 0; c < kTokens * kLanes; ++c) {
+                    const int token = k.half * 32 + c * (32 / kLanes) + lane / kLanes;
+                    const uint8_t* src = p.cache + desk.rows[token] + part * kPiece;
+                    const uint32_t to = smem_u32(stage + token * k.row_bytes() + part * kPiece);
+                    if (kPiece == 16) {
+                        cp_async16s(to, src, 16);
+                        cp_async16s(to + k.v_off(), src + k.v_off(), 16);
+                    } else {
+                        cp_async8(to, src, 8);
+                        cp_async8(to + k.v_off(), src + k.v_off(), 8);
                     }
                 }
             }
-            cp_async_commit();
-        };
-        for (int i = 0; i < kStages; ++i) {
+        }
+        cp_async_commit();
+    };
+
+    if constexpr (kSelected) {
+        for (int i = 0; i < kLead; ++i) {
             load_positions(i);
             load_pages();
-            copy(i);
+            gather(i);
         }
-        load_positions(kStages);
-        for (int i = 0; i < count; ++i) {
-            load_pages();                         // unit i + kStages
-            load_positions(i + kStages + 1);
-            cp_async_wait<kStages - 1>();
-            __syncwarp();
-            const Unit4 x = units[warp][i % kStages];
-            work(i, x, smem_u32(ring + (i % kStages) * p.stage), x.listed != 0);
-            __syncwarp();
-            copy(i + kStages);
+        load_positions(kLead);
+    } else if (leads) {
+        for (int i = 0; i < kLead; ++i) copy_page(i);
+    }
+    int i = 0;
+    bool gave_up = false;
+    while (i < count && !gave_up) {
+        // The part of an item that is in the share: units at .. until - 1 of its n.
+        const int begun = i;
+        Item4 x;
+        if (kSelected) listed_unit(p, u0 + i, &x);
+        else paged_unit(p, prefix, pages, u0 + i, &x);
+        k.begin(x);
+        const int until = min(x.n, x.at + count - i);
+        for (int at = x.at; at < until; ++at, ++i) {
+            uint8_t* const stage = ring + (i % kStages) * p.stage;
+            if constexpr (kSelected) {
+                load_pages();                     // of unit i + kLead
+                load_positions(i + kLead + 1);
+                cp_async_wait<kLead - 1>();
+                __syncwarp();
+            } else {
+                mbar_wait(&desk.full[i % kStages], (i / kStages) & 1, &desk.abort, p.status);
+            }
+            // (written where the unit's copies were ordered, and the worker has met since)
+            uint64_t listed = 0;
+            bool any;
+            if constexpr (kSelected) {
+                listed = static_cast<uint64_t>(desk.listed[i % kStages][1]) << 32 | desk.listed[i % kStages][0];
+                any = kTeam == 2 || listed != 0;
+            } else {
+                any = desk.listed[i % kStages][0] != 0;
+            }
+            auto issue = [&]() {
+                if constexpr (kSelected) gather(i + kLead);
+                else if (leads) copy_page(i + kLead);
+            };
+            if constexpr (NT == 4) {
+                gave_up = x.nq <= 16 ? k.template unit<2>(stage, at * kUnit, listed, any, issue)
+                                     : k.template unit<4>(stage, at * kUnit, listed, any, issue);
+            } else {
+                gave_up = k.template unit<NT>(stage, at * kUnit, listed, any, issue);
+            }
+            if (gave_up) break;
         }
+        // slot 2w: the piece that the share starts with; 2w + 1: one that starts inside it and does not end there
+        if (!gave_up) k.finish(x.at == 0 && until == x.n ? -1 : 2 * static_cast<int64_t>(w) + (begun > 0 ? 1 : 0));
+        k.meet();
+    }
+    if constexpr (kSelected) {
         cp_async_wait<0>();
+    } else if (gave_up && leads) {   // the copies in flight land before the CTA ends
+        const unsigned long long deadline = globaltimer() + kWaitLimitNs;
+        for (int j = i; j < min(i + kLead + 1, count); ++j)
+            mbar_drain(&desk.full[j % kStages], (j / kStages) & 1, deadline, p.status);
     }
 }
 
@@ -940,7 +1040,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
         const int n = ri.place * p.group + in_group;
         const int tile = n / p.cap;
         cap_row = n - tile * p.cap;
-        const int64_t W = p.warps < total ? p.warps : total;
+        const int64_t W = p.workers < total ? p.workers : total;
         const int64_t a = min(ri.first + (static_cast<int64_t>(kvh) * ri.tiles + tile) * ri.pages, total - 1);
         const int wa = warp_of(a, total, W), wb = warp_of(min(a + ri.pages, total) - 1, total, W);
         pieces = wb - wa + 1;
@@ -1027,7 +1127,7 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
     L.prefix = take(k > 0 ? 0 : (num_requests + 1) * 8);
     L.pages = take(k > 0 ? 0 : num_requests * 4);
     L.rows = take(k > 0 ? 0 : rows * static_cast<int64_t>(sizeof(Row4)));
-    const int64_t slots = 2 * kMaxCtas4 * (L.nt == 1 ? Shape4<1, false>::kWarps : Shape4<2, false>::kWarps);
+    const int64_t slots = 2 * kMaxCtas4 * kMaxWorkers4;
     L.po = take(slots * L.cap * dim * 4);
     L.pml = take(slots * L.cap * 8);
     L.total = at;
@@ -1067,20 +1167,20 @@ static int check_attend4(const dsa_kv_cache_fp4* cache, int32_t dtype, const voi
 
 template <Form kForm, int NT, bool kSelected>
 static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
-    using S4 = Shape4<NT, kSelected>;
-    using W4 = Worker4<kForm, NT, kSelected>;
+    static_assert(Shape4<kForm, NT, kSelected>::kWorkers <= kMaxWorkers4, "workspaces are sized for it");
+    using S4 = Shape4<kForm, NT, kSelected>;
     auto* kernel = attend_fp4_kernel<kForm, NT, kSelected>;
-    const int smem = S4::kWarps * (S4::kStages * p.stage + (S4::kQShared ? W4::kSteps * NT * 32 * 8 : 0)) +
+    const int smem = S4::kWorkers * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, NT, kSelected>))) +
                      (!kSelected && p.plan_in_cta ? kAxisBytes4 : 0);
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
     if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 230400) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost4) != cudaSuccess)
             return DSA_ERR_CUDA;
         attr_set[dev] = true;
     }
-    p.warps = ctas * S4::kWarps;
+    p.workers = ctas * S4::kWorkers;
     return launch_pdl(kernel, dim3(ctas), dim3(S4::kWarps * 32), smem, stream, p) == cudaSuccess ? DSA_OK
                                                                                                : DSA_ERR_CUDA;
 }
@@ -1089,7 +1189,8 @@ template <bool kSelected, int NT>
 static int launch_form4(Att4Params& p, int ctas, cudaStream_t stream) {
     return p.dim == 128  ? launch_attend4<kForm128, NT, kSelected>(p, ctas, stream)
            : p.dim == 64 ? launch_attend4<kForm64, NT, kSelected>(p, ctas, stream)
-                         : launch_attend4<kFormAny, NT, kSelected>(p, ctas, stream);
+           : p.dim > 64  ? launch_attend4<kFormAny128, NT, kSelected>(p, ctas, stream)
+                         : launch_attend4<kFormAny64, NT, kSelected>(p, ctas, stream);
 }
 
 template <bool kSelected>
