@@ -122,131 +122,174 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale_b
 // halves has vectors u and u + rot_units, which turn together, any other row or unit
 // 2u and 2u + 1.  In the first form a block's two vectors may be in two threads,
 // which tell each other their largest magnitudes.  A token has row_lanes x head_lanes
-// threads; a thread keeps its unit's eight angles and walks the token's query, key
-// and value heads in steps of head_lanes.
-template <typename T, bool kInterleaved, bool kStreams>
-__global__ void __launch_bounds__(kAppend4Threads) kv_append_fp4_kernel(const Append4Args a) {
-    pdl_wait();
-    pdl_launch_dependents();
+// threads; a thread keeps its unit's eight angles and walks the token's heads in steps
+// of head_lanes.  Queries and keys with values have CTAs of their own: the two take
+// different registers, and short code.
+struct Place4 {
+    int64_t tok, slot;
+    int unit, lane;            // of the row; row of the step
+    bool on, cached, turns;
+    int v0, v1;                // vectors of a rotated row
+};
+
+template <bool kInterleaved>
+__device__ __forceinline__ Place4 place(const Append4Args& a, int64_t block, bool flags, float (&c)[8], float (&s)[8]) {
+    Place4 x;
     const int per_token = a.row_lanes * a.head_lanes;
     const int sub = threadIdx.x / per_token;
-    const int64_t tok = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta + sub;
+    x.tok = block * a.tokens_per_cta + sub;
     const int in = threadIdx.x - sub * per_token;
-    const int unit = in & (a.row_lanes - 1), lane = in / a.row_lanes;
-    // (threads without work stay: the shuffles below are whole warps')
-    const bool on = sub < a.tokens_per_cta && tok < a.n && unit < a.units;
-    const int64_t slot = on ? a.slots[tok] : -1;
-    const bool cached = slot >= 0 && slot < a.num_slots;
-    if (slot >= a.num_slots && in == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_SLOT);
-    const bool turns = on && unit < a.rot_units;
-    const bool halves = turns && !kInterleaved;
-    // the unit's two vectors in a rotated row
-    const int v0 = halves ? unit : 2 * unit, v1 = halves ? unit + a.rot_units : 2 * unit + 1;
-    // where the other vectors of their blocks are: lane and vector of the pair there
-    const int row_base = (threadIdx.x & 31) - unit;
-    auto owner = [&](int v, int* second) {
-        const bool h = !kInterleaved && v < 2 * a.rot_units;
-        *second = h ? v >= a.rot_units : v & 1;
-        return row_base + (h ? (v >= a.rot_units ? v - a.rot_units : v) : v >> 1);
-    };
-    int mate0_second, mate1_second;
-    const int mate0 = owner(v0 ^ 1, &mate0_second), mate1 = owner(v1 ^ 1, &mate1_second);
-    float c[8], s[8];
-    if (turns) {
-        int64_t p = a.positions[tok];
+    x.unit = in & (a.row_lanes - 1), x.lane = in / a.row_lanes;
+    // (threads without work stay: rows' threads shuffle as whole warps)
+    x.on = sub < a.tokens_per_cta && x.tok < a.n && x.unit < a.units;
+    x.slot = x.on ? a.slots[x.tok] : -1;
+    x.cached = x.slot >= 0 && x.slot < a.num_slots;
+    if (flags && x.slot >= a.num_slots && in == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_SLOT);
+    x.turns = x.on && x.unit < a.rot_units;
+    const bool halves = x.turns && !kInterleaved;
+    x.v0 = halves ? x.unit : 2 * x.unit, x.v1 = halves ? x.unit + a.rot_units : 2 * x.unit + 1;
+    if (x.turns) {
+        int64_t p = a.positions[x.tok];
         if (p < 0 || p >= a.max_pos) {
-            if (slot >= 0 && in == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_GEOMETRY);
+            if (flags && x.slot >= 0 && in == 0 && a.status) atomicOr(a.status, DSA_STATUS_BAD_GEOMETRY);
             p = p < 0 ? 0 : a.max_pos - 1;
         }
-        const float* row = a.cos_sin + p * a.cs_stride + unit * 8;
+        const float* row = a.cos_sin + p * a.cs_stride + x.unit * 8;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             *reinterpret_cast<float4*>(c + i) = __ldg(reinterpret_cast<const float4*>(row + i));
             *reinterpret_cast<float4*>(s + i) = __ldg(reinterpret_cast<const float4*>(row + a.half + i));
         }
     }
-    const int off = static_cast<int>(slot & 63), sr = fp4_scale_row(a.dim);
-    uint8_t* const section = a.cache + (cached ? (slot >> 6) * a.page_stride : 0);
-    const int heads = a.q_heads + 2 * a.kv_heads;
-    const int kv0 = a.q_heads, v_first = a.q_heads + a.kv_heads;
-    for (int base = 0; base < heads; base += a.batch * a.head_lanes) {
-        uint4 x[kAppend4Batch], y[kAppend4Batch];
+    return x;
+}
+
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_row(float (&f)[8], float (&g)[8], const float (&c)[8], const float (&s)[8]) {
+    if (kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            turn(f[2 * j], f[2 * j + 1], c[j], s[j]);
+            turn(g[2 * j], g[2 * j + 1], c[4 + j], s[4 + j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turn(f[j], g[j], c[j], s[j]);
+    }
+}
+
+template <typename T, bool kInterleaved, bool kStreams>
+__device__ __forceinline__ void append_queries(const Append4Args& a, int64_t block) {
+    float c[8], s[8];
+    const Place4 x = place<kInterleaved>(a, block, false, c, s);
+    if (!x.on) return;
+    for (int base = x.lane; base < a.q_heads; base += a.batch * a.head_lanes) {
+        uint4 w[kAppend4Batch], y[kAppend4Batch];
 #pragma unroll
         for (int i = 0; i < kAppend4Batch; ++i) {
-            const int h = base + i * a.head_lanes + lane;
-            if (i >= a.batch || h >= heads || !on) continue;
-            const uint16_t* src;
-            int e0 = v0 * 8, e1 = v1 * 8;
-            if (h < kv0) {
-                src = a.q + tok * a.qt + h * a.qh;
-            } else if (!cached) {
-                continue;
-            } else if (h < v_first) {
-                src = a.k + tok * a.kt + (h - kv0) * a.kh;
-            } else {
-                src = a.v + tok * a.vt + (h - v_first) * a.vh;
-                e0 = unit * 16, e1 = e0 + 8;
-            }
-            x[i] = ld_row<kStreams>(src + e0);
-            y[i] = ld_row<kStreams>(src + e1);
+            const int h = base + i * a.head_lanes;
+            if (i >= a.batch || h >= a.q_heads) continue;
+            const uint16_t* src = a.q + x.tok * a.qt + h * a.qh;
+            w[i] = ld_row<kStreams>(src + x.v0 * 8);
+            y[i] = ld_row<kStreams>(src + x.v1 * 8);
         }
 #pragma unroll
         for (int i = 0; i < kAppend4Batch; ++i) {
-            const int h = base + i * a.head_lanes + lane;
-            const bool row = i < a.batch && h < heads && on;
-            const bool is_q = row && h < kv0, is_k = row && cached && h >= kv0 && h < v_first;
-            const bool is_v = row && cached && h >= v_first;
-            float f[8] = {}, g[8] = {};
-            if (is_q || is_k || is_v) {
-                unpack8<T>(x[i], f);
+            const int h = base + i * a.head_lanes;
+            if (i >= a.batch || h >= a.q_heads) continue;
+            if (x.turns) {
+                float f[8], g[8];
+                unpack8<T>(w[i], f);
                 unpack8<T>(y[i], g);
+                turn_row<kInterleaved>(f, g, c, s);
+                w[i] = pack8<T>(f);
+                y[i] = pack8<T>(g);
             }
-            if (turns && (is_q || is_k)) {
-                if (kInterleaved) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        turn(f[2 * j], f[2 * j + 1], c[j], s[j]);
-                        turn(g[2 * j], g[2 * j + 1], c[4 + j], s[4 + j]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) turn(f[j], g[j], c[j], s[j]);
-                }
-            }
-            if (is_q) {
-                uint16_t* dst = a.q_out + tok * a.ot + h * a.oh;
-                st_row<kStreams>(dst + v0 * 8, pack8<T>(f));
-                st_row<kStreams>(dst + v1 * 8, pack8<T>(g));
-            }
-            uint32_t m0 = amax8(f), m1 = amax8(g);
-            if (!kInterleaved && a.rot_units > 0 && __any_sync(0xFFFFFFFFu, is_k)) {
-                const uint32_t a0 = __shfl_sync(0xFFFFFFFFu, m0, mate0), a1 = __shfl_sync(0xFFFFFFFFu, m1, mate0);
-                const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, m0, mate1), b1 = __shfl_sync(0xFFFFFFFFu, m1, mate1);
-                if (is_k) {
-                    m0 = max(m0, mate0_second ? a1 : a0);
-                    m1 = max(m1, mate1_second ? b1 : b0);
-                }
-            }
-            if (is_v || (is_k && !halves)) m0 = m1 = max(m0, m1);
-            if (!is_k && !is_v) continue;
-            uint8_t* const at = section + (is_k ? h - kv0 : h - v_first) * a.head_stride;
-            const float scale = is_k ? a.k_scale : a.v_scale, six = is_k ? a.k_six : a.v_six;
-            const uint32_t s0 = block_scale(m0, six), s1 = is_k && halves ? block_scale(m1, six) : s0;
-            const uint32_t w0 = codes8(f, s0, scale), w1 = codes8(g, s1, scale);
-            uint8_t* const scales = at + fp4_scales(a.dim, off) + (is_k ? 0 : sr);
-            if (is_k && halves) {
-                uint8_t* const codes = at + fp4_k_row(a.dim, off);
-                *reinterpret_cast<uint32_t*>(codes + v0 * 4) = w0;
-                *reinterpret_cast<uint32_t*>(codes + v1 * 4) = w1;
-                if (!(v0 & 1)) scales[v0 >> 1] = static_cast<uint8_t>(s0);
-                if (!(v1 & 1)) scales[v1 >> 1] = static_cast<uint8_t>(s1);
-            } else {
-                uint8_t* const codes = at + (is_k ? fp4_k_row(a.dim, off) : fp4_v_row(a.dim, off));
-                *reinterpret_cast<uint2*>(codes + unit * 8) = make_uint2(w0, w1);
-                scales[unit] = static_cast<uint8_t>(s0);
-            }
+            uint16_t* dst = a.q_out + x.tok * a.ot + h * a.oh;
+            st_row<kStreams>(dst + x.v0 * 8, w[i]);
+            st_row<kStreams>(dst + x.v1 * 8, y[i]);
         }
     }
+}
+
+template <typename T, bool kInterleaved, bool kStreams>
+__device__ __forceinline__ void append_keys_values(const Append4Args& a, int64_t block) {
+    float c[8], s[8];
+    const Place4 x = place<kInterleaved>(a, block, true, c, s);
+    const bool halves = x.turns && !kInterleaved;
+    // where the other vectors of the thread's blocks are: lane and vector of the pair there
+    const int row_base = (threadIdx.x & 31) - x.unit;
+    auto owner = [&](int v, bool* second) {
+        const bool h = !kInterleaved && v < 2 * a.rot_units;
+        *second = h ? v >= a.rot_units : v & 1;
+        return row_base + (h ? (v >= a.rot_units ? v - a.rot_units : v) : v >> 1);
+    };
+    bool second0, second1;
+    const int mate0 = owner(x.v0 ^ 1, &second0), mate1 = owner(x.v1 ^ 1, &second1);
+    const int off = static_cast<int>(x.slot & 63), sr = fp4_scale_row(a.dim);
+    uint8_t* const section = a.cache + (x.cached ? (x.slot >> 6) * a.page_stride : 0);
+#pragma unroll 1
+    for (int base = 0; base < a.kv_heads; base += a.head_lanes) {
+        const int h = base + x.lane;
+        const bool on = x.cached && h < a.kv_heads;
+        uint4 kw = {}, ky = {}, vw = {}, vy = {};
+        if (on) {
+            const uint16_t* k = a.k + x.tok * a.kt + h * a.kh;
+            const uint16_t* v = a.v + x.tok * a.vt + h * a.vh + x.unit * 16;
+            kw = ld_row<kStreams>(k + x.v0 * 8);
+            ky = ld_row<kStreams>(k + x.v1 * 8);
+            vw = ld_row<kStreams>(v);
+            vy = ld_row<kStreams>(v + 8);
+        }
+        uint8_t* const at = section + h * a.head_stride;
+        uint8_t* const scales = at + fp4_scales(a.dim, off);
+        float f[8], g[8];
+        unpack8<T>(kw, f);
+        unpack8<T>(ky, g);
+        if (x.turns) turn_row<kInterleaved>(f, g, c, s);
+        uint32_t m0 = amax8(f), m1 = amax8(g);
+        if (!kInterleaved && a.rot_units > 0) {
+            const uint32_t a0 = __shfl_sync(0xFFFFFFFFu, m0, mate0), a1 = __shfl_sync(0xFFFFFFFFu, m1, mate0);
+            const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, m0, mate1), b1 = __shfl_sync(0xFFFFFFFFu, m1, mate1);
+            m0 = max(m0, second0 ? a1 : a0);
+            m1 = max(m1, second1 ? b1 : b0);
+        } else {
+            m0 = m1 = max(m0, m1);
+        }
+        if (!on) continue;
+        {
+            const uint32_t s0 = block_scale(m0, a.k_six), s1 = halves ? block_scale(m1, a.k_six) : s0;
+            const uint32_t w0 = codes8(f, s0, a.k_scale), w1 = codes8(g, s1, a.k_scale);
+            uint8_t* const codes = at + fp4_k_row(a.dim, off);
+            if (halves) {
+                *reinterpret_cast<uint32_t*>(codes + x.v0 * 4) = w0;
+                *reinterpret_cast<uint32_t*>(codes + x.v1 * 4) = w1;
+                if (!(x.v0 & 1)) scales[x.v0 >> 1] = static_cast<uint8_t>(s0);
+                if (!(x.v1 & 1)) scales[x.v1 >> 1] = static_cast<uint8_t>(s1);
+            } else {
+                *reinterpret_cast<uint2*>(codes + x.unit * 8) = make_uint2(w0, w1);
+                scales[x.unit] = static_cast<uint8_t>(s0);
+            }
+        }
+        unpack8<T>(vw, f);
+        unpack8<T>(vy, g);
+        const uint32_t s0 = block_scale(max(amax8(f), amax8(g)), a.v_six);
+        const uint32_t w0 = codes8(f, s0, a.v_scale), w1 = codes8(g, s0, a.v_scale);
+        *reinterpret_cast<uint2*>(at + fp4_v_row(a.dim, off) + x.unit * 8) = make_uint2(w0, w1);
+        scales[sr + x.unit] = static_cast<uint8_t>(s0);
+    }
+}
+
+template <typename T, bool kInterleaved, bool kStreams>
+__global__ void __launch_bounds__(kAppend4Threads) kv_append_fp4_kernel(const Append4Args a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    // every other CTA, so that both kinds are on the GPU together
+    const int64_t block = a.q ? blockIdx.x >> 1 : blockIdx.x;
+    if (a.q && blockIdx.x & 1)
+        append_queries<T, kInterleaved, kStreams>(a, block);
+    else
+        append_keys_values<T, kInterleaved, kStreams>(a, block);
 }
 
 struct Read4Args {
@@ -401,12 +444,12 @@ extern "C" int dsa_kv_append_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, c
     a.row_lanes = 1;
     while (a.row_lanes < a.units) a.row_lanes *= 2;
     a.head_lanes = want / a.row_lanes;
-    // the heads of a thread in equal rounds
-    const int each = (a.q_heads + 2 * a.kv_heads + a.head_lanes - 1) / a.head_lanes;
+    // the query heads of a thread in equal rounds
+    const int each = a.q ? (a.q_heads + a.head_lanes - 1) / a.head_lanes : 1;
     const int rounds = (each + kAppend4Batch - 1) / kAppend4Batch;
     a.batch = (each + rounds - 1) / rounds;
     a.tokens_per_cta = kAppend4Threads / want;
-    const int64_t blocks = (n + a.tokens_per_cta - 1) / a.tokens_per_cta;
+    const int64_t blocks = (n + a.tokens_per_cta - 1) / a.tokens_per_cta * (a.q ? 2 : 1);
     if (blocks > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const dim3 grid(static_cast<unsigned>(blocks));
