@@ -29,8 +29,11 @@ namespace dsa {
 constexpr int kUnit = kPage;            // keys of a unit
 constexpr int kMaxCtas4 = 160;          // workspaces are sized for at most this many CTAs
 constexpr int kMaxWorkers4 = 12;        // ... of this many workers
-constexpr int kCtaRequests = 512;       // up to this many requests every CTA lays out the axis itself
+constexpr int kCtaRequests = 256;       // up to this many requests every CTA lays out the axis itself
 constexpr int kPlan4Threads = 512;
+constexpr int kList4Threads = 256;
+constexpr int kBitmapKeys = 1 << 20;    // positions that a list is put in order by
+constexpr int64_t kPackBytes = 64 << 20;   // listed sections' bytes from which lists are put in order first
 constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr float kLn2_4 = 0.6931471805599453f;
 // Weights are kept times 2^6: FP16 then holds them from 2^-30 of the largest on.
@@ -38,18 +41,26 @@ constexpr float kLift = 6.0f;
 
 // Where the join finds a row's pieces.
 struct Row4 {
-    int64_t first;          // first unit of the row's request
+    int64_t first;          // where the row's request starts on the axis
     int pages, tiles;       // units an item, row tiles a head
-    int place, pad;         // the row's place in its request
+    int place, weight;      // the row's place in its request, what a unit of it takes of the axis
 };
 
 struct Att4Layout {
-    size_t info;            // int64: units on the axis
-    size_t prefix, pages;   // the axis in global memory: int64[R + 1], int[R]
+    size_t info;            // int64: the axis' length
+    size_t prefix, units, pages;   // the axis in global memory: int64[R + 1] twice, int[R]
+    size_t list;            // int[rows][kpad]: slots of the listed keys
     size_t rows;            // Row4[rows]
     size_t po, pml;         // float[slots][cap][dim], float2[slots][cap]: partial results
     size_t total;
     int nt, cap;            // column tiles of 8 query rows; rows of a slot
+};
+
+// The requests on the axis: where each starts, units before it, and pages an item of it has.
+struct Axis4 {
+    int64_t* prefix;
+    int64_t* units;
+    int* pages;
 };
 
 struct Att4Params {
@@ -67,14 +78,16 @@ struct Att4Params {
     const int32_t* topk;
     int64_t topk_stride;
     int64_t* info;
-    int64_t* prefix;
-    int* pages;
+    Axis4 axis;
+    int* list;
     Row4* row_info;
     float* po;
     float2* pml;
     int32_t* status;
     int R, rows, heads, group, kv_heads, dim, max_keys, num_pages;
     int k, list_units, list_tiles;   // listed keys: units an item, row tiles a head
+    int packed;                      // ... and slots in `list`, in order, instead of positions in `topk`
+    int light, heavy;                // what units of up to 16 query rows, and of more, take of the axis
     int nt, cap, workers;            // workers: of the whole grid
     int bf16;                        // type of q and out (else FP16)
     int section, stage;              // bytes of a section, and of a ring stage
@@ -91,27 +104,65 @@ __device__ __forceinline__ uint32_t pack2(const Att4Params& p, float lo, float h
 }
 
 // ----------------------------------------------------------------- the axis
-// Warp w of W takes units [w T / W, (w + 1) T / W).
+// Worker w of W has the units that start in [w T / W, (w + 1) T / W).
 __device__ __forceinline__ int64_t share4(int64_t w, int64_t T, int64_t W) {
     if ((w + 1) * T < (int64_t(1) << 32)) return static_cast<uint32_t>(w * T) / static_cast<uint32_t>(W);
     return w * T / W;
 }
-__device__ __forceinline__ int warp_of(int64_t u, int64_t T, int64_t W) {
+__device__ __forceinline__ int worker_at(int64_t u, int64_t T, int64_t W) {
     if ((u + 1) * W < (int64_t(1) << 32) && T < (int64_t(1) << 32))
         return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(W) - 1) /
                                 static_cast<uint32_t>(T));
     return static_cast<int>(((u + 1) * W - 1) / T);
 }
 
-// Lays out the requests (whole block): prefix[j] units before request j, pages[j].
-// `tmp`: 33 int64 of shared scratch.  `write`: also what the join reads.
-__device__ void lay_out4(const Att4Params& p, int64_t* prefix, int* pages, int64_t* tmp, bool write) {
+// How many workers share an axis of length T: no more than leave a unit's start to every share.
+__device__ __forceinline__ int64_t sharers(const Att4Params& p, int64_t T) {
+    return max(min(static_cast<int64_t>(p.workers), T / p.heavy), static_cast<int64_t>(T > 0));
+}
+
+// The last request that starts at or before v.
+template <typename I>
+__device__ __forceinline__ int last_at_most(const I* starts, int n, I v) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (starts[mid] <= v) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// (Row, head) pairs of a key head in request j, from row *row0 on.
+__device__ __forceinline__ int pairs_of(const Att4Params& p, int j, int* row0) {
+    *row0 = min(max(p.starts[j], 0), p.rows);
+    return (min(max(p.starts[j + 1], *row0), p.rows) - *row0) * p.group;
+}
+
+// Units before the first that starts at or behind place c of the axis.
+__device__ __forceinline__ int64_t unit_at(const Att4Params& p, const Axis4& x, int64_t c) {
+    if (c >= x.prefix[p.R]) return x.units[p.R];
+    const int j = last_at_most(x.prefix, p.R, c);
+    int row0;
+    const int weight = pairs_of(p, j, &row0) <= 16 ? p.light : p.heavy;
+    const int64_t in = c - x.prefix[j] + weight - 1;
+    return x.units[j] + (weight == 1                 ? in
+                         : in < (int64_t(1) << 32) ? static_cast<uint32_t>(in) / static_cast<uint32_t>(weight)
+                                                   : in / weight);
+}
+
+// Lays out the requests (whole block).  `tmp`: 66 int64 of shared scratch.
+// `write`: also what the join reads.
+__device__ void lay_out4(const Att4Params& p, const Axis4& x, int64_t* tmp, bool write) {
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
+    // (on their way while the starts are read)
+    for (int r = threadIdx.x * 32; r < p.rows; r += nt * 32)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_ends + r));
     if (write)
-        for (int r = threadIdx.x; r < p.rows; r += nt) p.row_info[r] = Row4{0, 0, 1, 0, 0};
-    int64_t carry = 0;
-    __syncthreads();
+        for (int r = threadIdx.x; r < p.rows; r += nt) p.row_info[r] = Row4{0, 0, 1, 0, 1};
+    int64_t carry = 0, carry_units = 0;
+    if (write) __syncthreads();
     for (int base = 0; base < p.R; base += nt) {
         const int j = base + threadIdx.x;
         int s0 = 0, s1 = 0, most = 0;
@@ -127,39 +178,44 @@ __device__ void lay_out4(const Att4Params& p, int64_t* prefix, int* pages, int64
             }
         }
         const int n = (most + kUnit - 1) / kUnit;
-        const int tiles = static_cast<int>((static_cast<int64_t>(s1 - s0) * p.group + p.cap - 1) / p.cap);
-        const int64_t units = static_cast<int64_t>(n) * tiles * p.kv_heads;
-        int64_t v = units;
+        const int64_t all = static_cast<int64_t>(s1 - s0) * p.group;
+        const int tiles = static_cast<int>((all + p.cap - 1) / p.cap), weight = all <= 16 ? p.light : p.heavy;
+        const int64_t units = static_cast<int64_t>(n) * tiles * p.kv_heads, cost = units * weight;
+        int64_t v = cost, y = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-            if (lane >= d) v += o;
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d), q = __shfl_up_sync(0xFFFFFFFFu, y, d);
+            if (lane >= d) v += o, y += q;
         }
-        if (lane == 31) tmp[warp] = v;
+        if (lane == 31) tmp[warp] = v, tmp[33 + warp] = y;
         __syncthreads();
-        if (warp == 0) {
-            int64_t s = lane < nt / 32 ? tmp[lane] : 0;
+        if (warp < 2) {
+            int64_t* const t = tmp + 33 * warp;
+            int64_t z = lane < nt / 32 ? t[lane] : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-                if (lane >= d) s += o;
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, z, d);
+                if (lane >= d) z += o;
             }
-            tmp[lane] = s;
-            if (lane == 31) tmp[32] = s;
+            t[lane] = z;
+            if (lane == 31) t[32] = z;
         }
         __syncthreads();
-        const int64_t before = carry + v - units + (warp > 0 ? tmp[warp - 1] : 0);
+        const int64_t before = carry + v - cost + (warp > 0 ? tmp[warp - 1] : 0);
         if (j < p.R) {
-            prefix[j] = before;
-            pages[j] = n;
+            x.prefix[j] = before;
+            x.units[j] = carry_units + y - units + (warp > 0 ? tmp[33 + warp - 1] : 0);
+            x.pages[j] = n;
             if (write)
-                for (int r = s0; r < s1; ++r) p.row_info[r] = Row4{before, n, max(tiles, 1), r - s0, 0};
+                for (int r = s0; r < s1; ++r) p.row_info[r] = Row4{before, n, max(tiles, 1), r - s0, weight};
         }
         carry += tmp[32];
+        carry_units += tmp[65];
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        prefix[p.R] = carry;
+        x.prefix[p.R] = carry;
+        x.units[p.R] = carry_units;
         if (write) p.info[0] = carry;
     }
     if (write && bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
@@ -169,8 +225,95 @@ __device__ void lay_out4(const Att4Params& p, int64_t* prefix, int* pages, int64
 __global__ void __launch_bounds__(kPlan4Threads) attend_fp4_plan_kernel(const Att4Params p) {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ int64_t tmp[33];
-    lay_out4(p, p.prefix, p.pages, tmp, true);
+    __shared__ int64_t tmp[66];
+    lay_out4(p, p.axis, tmp, true);
+}
+
+// Listed keys as slots (page * 64 + token), in the order of their positions, so that
+// neighbours in a page are read one behind the other: 64 rows of 2048 out of 4096 to
+// 8192 keys take DRAM 15 us less than in a random order.  One CTA a row.  The order
+// comes from a bitmap of the row's positions; where a position is listed twice (it
+// counts twice), or where there are more positions than the bitmap holds, the slots
+// stay in the list's order.
+__global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const Att4Params p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    extern __shared__ uint32_t bitmap[];
+    __shared__ int sums[kList4Threads / 32 + 1];
+    __shared__ int s_req, s_twice;
+    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t* src = p.topk + row * p.topk_stride;
+    int* const dst = p.list + static_cast<int64_t>(row) * p.list_units * kUnit;
+    const int e = p.row_ends[row], bound = min(max(e, 0), p.max_keys);
+    const bool ordered = p.max_keys <= kBitmapKeys;
+    const int words = ordered ? (bound + 31) / 32 : 0;
+    if (threadIdx.x == 0) s_req = -1, s_twice = 0;
+    for (int i = threadIdx.x; i < words; i += kList4Threads) bitmap[i] = 0;
+    __syncthreads();
+    bool bad = false, bad_page = false;
+    for (int j = threadIdx.x; j < p.R; j += kList4Threads) {
+        const int a = p.starts[j], b = p.starts[j + 1];
+        if (a < 0 || b < a || b > p.rows) bad = true;
+        if (a <= row && row < b) atomicMax(&s_req, j);
+    }
+    if (ordered)
+        for (int i = threadIdx.x; i < p.k; i += kList4Threads) {
+            const int t = src[i];
+            if (t >= 0 && t < bound && (atomicOr(&bitmap[t >> 5], 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
+        }
+    __syncthreads();
+    const int req = s_req;
+    const int32_t* const table = p.bt + (req >= 0 ? req : 0) * p.bt_stride;
+    auto slot_of = [&](int t) {
+        const int page = table[t / kPage];
+        const bool ok = page >= 0 && page < p.num_pages;
+        bad_page |= !ok;
+        return ok ? page * kPage + t % kPage : -1;
+    };
+    int count = 0;
+    if (req >= 0) {
+        if (e != bound) bad = true;
+        const bool by_map = ordered && !s_twice;
+        // positions: a run of the bitmap's words a thread; entries: one a thread and round
+        const int each = (words + kList4Threads - 1) / kList4Threads;
+        const int from = min(threadIdx.x * each, words), to = min(from + each, words);
+        const int rounds = by_map ? 1 : (p.k + kList4Threads - 1) / kList4Threads;
+        for (int round = 0; round < rounds; ++round) {
+            int n = 0, t = -1;
+            if (by_map) {
+                for (int i = from; i < to; ++i) n += __popc(bitmap[i]);
+            } else if (round * kList4Threads + threadIdx.x < p.k) {
+                t = src[round * kList4Threads + threadIdx.x];
+                n = t >= 0 && t < bound;
+            }
+            int inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            if (lane == 31) sums[warp] = inc;
+            __syncthreads();
+            int before = count + inc - n, all = count;
+            for (int i = 0; i < kList4Threads / 32; ++i) {
+                if (i < warp) before += sums[i];
+                all += sums[i];
+            }
+            if (by_map) {
+                for (int i = from; i < to; ++i)
+                    for (uint32_t bits = bitmap[i]; bits; bits &= bits - 1)
+                        dst[before++] = slot_of(i * 32 + __ffs(bits) - 1);
+            } else if (n) {
+                dst[before] = slot_of(t);
+            }
+            count = all;
+            __syncthreads();
+        }
+        for (int i = threadIdx.x; i < p.k; i += kList4Threads) bad |= src[i] >= bound;
+    }
+    for (int i = count + threadIdx.x; i < p.list_units * kUnit; i += kList4Threads) dst[i] = -1;
+    if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+    if (bad_page && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
 }
 
 // ----------------------------------------------------------------- attention
@@ -227,7 +370,7 @@ __device__ __forceinline__ uint32_t nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu)
 struct Unit4 {
     int page;           // its page, -1: none in the pool (listed keys: the row's request, -1: none)
     int kvh;            // key head
-    int at, row;        // listed keys: its place in its item, the row,
+    int at, row;        // listed keys: its place in its item, the row (pages: row tiles that read it),
     int bound;          // ... and the positions from which on keys are not the row's
 };
 
@@ -729,47 +872,35 @@ struct Worker4 {
     }
 };
 
-constexpr int kAxisBytes4 = (kCtaRequests + 1 + 33) * 8 + kCtaRequests * 4;
+constexpr int kAxisBytes4 = (2 * (kCtaRequests + 1) + 66) * 8 + kCtaRequests * 4;
 
-// The last request that starts at or before v.
-template <typename I>
-__device__ __forceinline__ int last_at_most(const I* starts, int n, I v) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (starts[mid] <= v) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
-// Unit u of the axis: what a lane has to know of it, and its item.
-__device__ __forceinline__ Unit4 paged_unit(const Att4Params& p, const int64_t* prefix, const int* pages, int64_t u,
-                                            Item4* y = nullptr) {
+// Unit u: what a lane has to know of it, and its item.
+__device__ __forceinline__ Unit4 paged_unit(const Att4Params& p, const Axis4& axis, int64_t u, Item4* y = nullptr) {
     Unit4 x;
-    const int j = last_at_most(prefix, p.R, u);
-    const int64_t in = u - prefix[j];
-    const int n = pages[j];
+    const int j = last_at_most(axis.units, p.R, u);
+    const int64_t in = u - axis.units[j];
+    const int n = axis.pages[j];
     const int item = in < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(n))
                                              : static_cast<int>(in / n);
     x.at = static_cast<int>(in - static_cast<int64_t>(item) * n);
-    const int row0 = min(max(p.starts[j], 0), p.rows);
-    const int all = (min(max(p.starts[j + 1], row0), p.rows) - row0) * p.group;
-    const int tiles = (all + p.cap - 1) / p.cap;
+    int page = 0;
+    if (!y) page = p.bt[j * p.bt_stride + x.at];
+    int row0;
+    const int all = pairs_of(p, j, &row0), tiles = (all + p.cap - 1) / p.cap;
     x.kvh = item / tiles;
     if (y) {
         const int first = (item - x.kvh * tiles) * p.cap;
         *y = Item4{row0, first, min(p.cap, all - first), x.kvh, x.at, n};
         return x;
     }
-    const int page = p.bt[j * p.bt_stride + x.at];
     x.page = page >= 0 && page < p.num_pages ? page : -1;
     if (x.page < 0 && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-    x.row = x.bound = 0;
+    x.row = tiles;
+    x.bound = 0;
     return x;
 }
 
-__device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, int64_t u, Item4* y = nullptr) {
+__device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, const int* starts, int64_t u, Item4* y = nullptr) {
     Unit4 x;
     const int per_row = p.kv_heads * p.list_tiles * p.list_units;
     x.row = static_cast<int>(u / per_row);
@@ -782,9 +913,11 @@ __device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, int64_t u, Ite
         *y = Item4{x.row, first, min(p.cap, p.group - first), x.kvh, x.at, p.list_units};
         return x;
     }
-    const int j = p.R > 0 ? last_at_most(p.starts, p.R, x.row) : -1;
-    x.page = j >= 0 && p.starts[j] <= x.row && x.row < p.starts[j + 1] ? j : -1;
+    x.page = x.bound = 0;
+    if (p.packed) return x;
     const int e = p.row_ends[x.row];
+    const int j = p.R > 0 ? last_at_most(starts, p.R, x.row) : -1;
+    x.page = j >= 0 && starts[j] <= x.row && x.row < starts[j + 1] ? j : -1;
     x.bound = min(max(e, 0), p.max_keys);
     if (x.page >= 0 && e != x.bound && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
     return x;
@@ -813,37 +946,44 @@ attend_fp4_kernel(const Att4Params p) {
         }
         desk.abort = 0;
     }
-    const int64_t* prefix = p.prefix;
-    const int* pages = p.pages;
+    Axis4 axis = p.axis;
+    const int* starts = p.starts;
+    uint8_t* const table = smem + S4::kWorkers * (kStages * p.stage + sizeof(Desk));
     if (!kSelected && p.plan_in_cta) {
-        int64_t* const px = reinterpret_cast<int64_t*>(smem + S4::kWorkers * (kStages * p.stage + sizeof(Desk)));
-        int* const pg = reinterpret_cast<int*>(px + kCtaRequests + 1 + 33);
-        lay_out4(p, px, pg, px + kCtaRequests + 1, blockIdx.x == 0);
-        prefix = px, pages = pg;
+        axis.prefix = reinterpret_cast<int64_t*>(table);
+        axis.units = axis.prefix + kCtaRequests + 1;
+        axis.pages = reinterpret_cast<int*>(axis.units + kCtaRequests + 1 + 66);
+        lay_out4(p, axis, axis.units + kCtaRequests + 1, blockIdx.x == 0);
+    }
+    if (kSelected && !p.packed) {
+        bool bad = false;
+        if (p.R <= kCtaRequests) starts = reinterpret_cast<int*>(table);
+        if (p.R <= kCtaRequests || blockIdx.x == 0)
+            for (int j = threadIdx.x; j <= p.R; j += blockDim.x) {
+                const int a = p.starts[j];
+                if (p.R <= kCtaRequests) reinterpret_cast<int*>(table)[j] = a;
+                if (blockIdx.x == 0) bad |= a < 0 || (j > 0 && a < p.starts[j - 1]) || a > p.rows;
+            }
+        if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+        __syncthreads();
     }
     k.meet();
-    if (kSelected && blockIdx.x == 0 && p.status) {
-        bool bad = false;
-        for (int j = threadIdx.x; j < p.R; j += blockDim.x) {
-            const int a = p.starts[j], b = p.starts[j + 1];
-            bad |= a < 0 || b < a || b > p.rows;
-        }
-        if (bad) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
-    }
     const int64_t total = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles * p.list_units
-                                    : prefix[p.R];
-    const int64_t W = p.workers < total ? p.workers : total;
+                                    : axis.prefix[p.R];
+    const int64_t W = sharers(p, total);
     const int w = worker * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
     if (w >= W) return;
-    const int64_t u0 = share4(w, total, W);
-    const int count = static_cast<int>(share4(w + 1, total, W) - u0);
+    int64_t u0 = share4(w, total, W), u1 = share4(w + 1, total, W);
+    if (!kSelected) u0 = unit_at(p, axis, u0), u1 = unit_at(p, axis, u1);
+    const int count = static_cast<int>(u1 - u0);
 
     // The share's units are looked up 32 at a time, one a lane.
     Unit4 mine;
     auto look_up = [&](int base) {
         if (base + lane < count)
-            mine = kSelected ? listed_unit(p, u0 + base + lane) : paged_unit(p, prefix, pages, u0 + base + lane);
+            mine = kSelected ? listed_unit(p, starts, u0 + base + lane) : paged_unit(p, axis, u0 + base + lane);
     };
+    const uint64_t once = l2_evict_first_policy();
     // A page's copy, by the unit's lane.
     auto copy_page = [&](int i) {
         if (i >= count) return;
@@ -853,8 +993,10 @@ attend_fp4_kernel(const Att4Params p) {
             desk.listed[i % kStages][0] = mine.page >= 0;
             if (mine.page >= 0) {
                 mbar_arrive_expect_tx(bar, p.section);
-                bulk_load(ring + (i % kStages) * p.stage, p.cache + mine.page * p.page_stride + mine.kvh * p.head_stride,
-                          p.section, bar);
+                const uint8_t* src = p.cache + mine.page * p.page_stride + mine.kvh * p.head_stride;
+                // (a page that one row tile reads is not needed again in this call)
+                if (mine.row == 1) bulk_load_hint(ring + (i % kStages) * p.stage, src, p.section, bar, once);
+                else bulk_load(ring + (i % kStages) * p.stage, src, p.section, bar);
             } else {
                 mbar_arrive(bar);
             }
@@ -879,11 +1021,13 @@ attend_fp4_kernel(const Att4Params p) {
         later.kvh = __shfl_sync(0xFFFFFFFFu, mine.kvh, i % 32);
         later.bound = __shfl_sync(0xFFFFFFFFu, mine.bound, i % 32);
         if (later.req < 0) return;
-        const int32_t* list = p.topk + row * p.topk_stride;
+        const int32_t* list =
+            p.packed ? p.list + static_cast<int64_t>(row) * p.list_units * kUnit : p.topk + row * p.topk_stride;
+        const int most = p.packed ? p.list_units * kUnit : p.k;
 #pragma unroll
         for (int h = 0; h < kTokens; ++h) {
             const int e = at * kUnit + token0 + 32 * h;
-            if (e < p.k) ahead[h] = list[e];
+            if (e < most) ahead[h] = list[e];
         }
     };
     auto load_pages = [&]() {            // ahead / later become pos, page / next
@@ -893,6 +1037,10 @@ attend_fp4_kernel(const Att4Params p) {
         for (int h = 0; h < kTokens; ++h) {
             pos[h] = ahead[h];
             page[h] = -1;
+            if (p.packed) {   // a slot
+                if (pos[h] >= 0) page[h] = pos[h] / kPage;
+                continue;
+            }
             if (pos[h] >= next.bound) {
                 bad |= pos[h] >= 0;
                 pos[h] = -1;
@@ -961,10 +1109,9 @@ attend_fp4_kernel(const Att4Params p) {
     bool gave_up = false;
     while (i < count && !gave_up) {
         // The part of an item that is in the share: units at .. until - 1 of its n.
-        const int begun = i;
         Item4 x;
-        if (kSelected) listed_unit(p, u0 + i, &x);
-        else paged_unit(p, prefix, pages, u0 + i, &x);
+        if (kSelected) listed_unit(p, starts, u0 + i, &x);
+        else paged_unit(p, axis, u0 + i, &x);
         k.begin(x);
         const int until = min(x.n, x.at + count - i);
         for (int at = x.at; at < until; ++at, ++i) {
@@ -998,8 +1145,8 @@ attend_fp4_kernel(const Att4Params p) {
             }
             if (gave_up) break;
         }
-        // slot 2w: the piece that the share starts with; 2w + 1: one that starts inside it and does not end there
-        if (!gave_up) k.finish(x.at == 0 && until == x.n ? -1 : 2 * static_cast<int64_t>(w) + (begun > 0 ? 1 : 0));
+        // slot 2w + 1: the item's first piece; 2w: a later one (a share has at most one of each)
+        if (!gave_up) k.finish(x.at == 0 && until == x.n ? -1 : 2 * static_cast<int64_t>(w) + (x.at == 0 ? 1 : 0));
         k.meet();
     }
     if constexpr (kSelected) {
@@ -1029,24 +1176,25 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
     if (kSelected) {
         const int64_t per_row = static_cast<int64_t>(p.kv_heads) * p.list_tiles * p.list_units;
         total = p.rows * per_row;
-        ri = Row4{row * per_row, p.list_units, p.list_tiles, 0, 0};
+        ri = Row4{row * per_row, p.list_units, p.list_tiles, 0, 1};
     } else {
         ri = p.row_info[row];
         total = p.info[0];
     }
     int pieces = 0, cap_row = 0;
-    int64_t slot = 0, second = 0;   // slots of the first piece and of the second
+    int64_t slot = 0;   // of the second piece; the first's is the one before
     if (ri.pages > 0 && total > 0) {
         const int n = ri.place * p.group + in_group;
         const int tile = n / p.cap;
         cap_row = n - tile * p.cap;
-        const int64_t W = p.workers < total ? p.workers : total;
-        const int64_t a = min(ri.first + (static_cast<int64_t>(kvh) * ri.tiles + tile) * ri.pages, total - 1);
-        const int wa = warp_of(a, total, W), wb = warp_of(min(a + ri.pages, total) - 1, total, W);
+        const int64_t W = sharers(p, total);
+        const int64_t a =
+            min(ri.first + (static_cast<int64_t>(kvh) * ri.tiles + tile) * ri.pages * ri.weight, total - 1);
+        const int64_t last = min(a + static_cast<int64_t>(ri.pages - 1) * ri.weight, total - 1);
+        const int wa = worker_at(a, total, W), wb = worker_at(last, total, W);
         pieces = wb - wa + 1;
         if (pieces == 1) return;   // written by the attention kernel
-        slot = 2 * static_cast<int64_t>(wa) + (share4(wa, total, W) < a ? 1 : 0);
-        second = 2 * static_cast<int64_t>(wa + 1);
+        slot = 2 * static_cast<int64_t>(wa + 1);
     }
     const bool on = lane * 4 < p.dim;
     constexpr int kAhead = 4;
@@ -1061,7 +1209,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
             e[j] = make_float2(-INFINITY, 0.0f);
             v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (i < pieces) {
-                const int64_t at = (i == 0 ? slot : second + 2 * (i - 1)) * p.cap + cap_row;
+                const int64_t at = (i == 0 ? slot - 1 : slot + 2 * (i - 1)) * p.cap + cap_row;
                 e[j] = p.pml[at];
                 if (on) v[j] = *reinterpret_cast<const float4*>(p.po + at * p.dim + lane * 4);
             }
@@ -1125,6 +1273,8 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
     };
     L.info = take(8);
     L.prefix = take(k > 0 ? 0 : (num_requests + 1) * 8);
+    L.units = take(k > 0 ? 0 : (num_requests + 1) * 8);
+    L.list = take(k > 0 ? rows * ((k + kUnit - 1) / kUnit * kUnit) * 4 : 0);
     L.pages = take(k > 0 ? 0 : num_requests * 4);
     L.rows = take(k > 0 ? 0 : rows * static_cast<int64_t>(sizeof(Row4)));
     const int64_t slots = 2 * kMaxCtas4 * kMaxWorkers4;
@@ -1171,7 +1321,7 @@ static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
     using S4 = Shape4<kForm, NT, kSelected>;
     auto* kernel = attend_fp4_kernel<kForm, NT, kSelected>;
     const int smem = S4::kWorkers * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, NT, kSelected>))) +
-                     (!kSelected && p.plan_in_cta ? kAxisBytes4 : 0);
+                     (kSelected ? (kCtaRequests + 1) * 4 : p.plan_in_cta ? kAxisBytes4 : 0);
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
@@ -1197,6 +1347,20 @@ template <bool kSelected>
 static int launch_all4(Att4Params& p, cudaStream_t stream) {
     int ctas = device_sm_count();
     if (ctas > kMaxCtas4) ctas = kMaxCtas4;
+    if (kSelected && p.packed) {
+        const int bitmap = p.max_keys <= kBitmapKeys ? (p.max_keys + 31) / 32 * 4 : 0;
+        static bool attr_set[64] = {false};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(attend_fp4_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kBitmapKeys / 8) != cudaSuccess)
+                return DSA_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+        if (launch_pdl(attend_fp4_list_kernel, dim3(p.rows), dim3(kList4Threads), bitmap, stream, p) != cudaSuccess)
+            return DSA_ERR_CUDA;
+    }
     if (!kSelected && !p.plan_in_cta &&
         launch_pdl(attend_fp4_plan_kernel, dim3(1), dim3(kPlan4Threads), 0, stream, p) != cudaSuccess)
         return DSA_ERR_CUDA;
@@ -1224,8 +1388,10 @@ static Att4Params params4(const dsa_kv_cache_fp4* c, const Att4Layout& L, uint8_
     p.section = fp4_section_bytes(p.dim);
     p.stage = (p.section + 127) / 128 * 128;
     p.info = reinterpret_cast<int64_t*>(ws + L.info);
-    p.prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
-    p.pages = reinterpret_cast<int*>(ws + L.pages);
+    p.axis = Axis4{reinterpret_cast<int64_t*>(ws + L.prefix), reinterpret_cast<int64_t*>(ws + L.units),
+                   reinterpret_cast<int*>(ws + L.pages)};
+    p.list = reinterpret_cast<int*>(ws + L.list);
+    p.light = p.heavy = 1;
     p.row_info = reinterpret_cast<Row4*>(ws + L.rows);
     p.po = reinterpret_cast<float*>(ws + L.po);
     p.pml = reinterpret_cast<float2*>(ws + L.pml);
@@ -1271,6 +1437,7 @@ extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype
     p.group = p.heads / p.kv_heads;
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
     p.plan_in_cta = p.R <= kCtaRequests && p.rows <= 4096;
+    if (p.nt == 4) p.light = 2, p.heavy = 3;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return launch_all4<false>(p, stream);
 }
@@ -1304,7 +1471,9 @@ extern "C" int dsa_attend_selected_fp4(const dsa_kv_cache_fp4* cache, int32_t dt
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
     p.list_units = static_cast<int>((k + kUnit - 1) / kUnit);
     p.list_tiles = (p.group + p.cap - 1) / p.cap;
-    if (static_cast<int64_t>(p.kv_heads) * p.list_tiles * p.list_units > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
+    const int64_t per_row = static_cast<int64_t>(p.kv_heads) * p.list_tiles * p.list_units;
+    if (per_row > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
+    p.packed = cache->num_pages <= (1 << 25) && per_row * rows * p.section >= kPackBytes;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return launch_all4<true>(p, stream);
 }

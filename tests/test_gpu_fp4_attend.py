@@ -49,7 +49,7 @@ def test_scales(cuda_lib, k_scale, v_scale):
     c.check(c.paged(cuda_lib, scale=0.01), scale=0.01)
 
 
-@pytest.mark.parametrize("requests", [511, 512, 513, 700])
+@pytest.mark.parametrize("requests", [255, 256, 257, 511, 512, 513, 700])
 def test_many_requests(cuda_lib, requests):
     c = Case([(53 * j) % 301 for j in range(requests)], [j % 3 for j in range(requests)], hq=4, hkv=2, dim=64)
     c.check(c.paged(cuda_lib), rows=range(0, c.q.shape[0], 7))
