@@ -28,7 +28,7 @@ namespace dsa {
 
 constexpr int kUnit = kPage;            // keys of a unit
 constexpr int kMaxCtas4 = 160;          // workspaces are sized for at most this many CTAs
-constexpr int kMaxWorkers4 = 12;        // ... of this many workers
+constexpr int kMaxWarps4 = 12;        // ... of this many warps
 constexpr int kCtaRequests = 256;       // up to this many requests every CTA lays out the axis itself
 constexpr int kPlan4Threads = 512;
 constexpr int kList4Threads = 256;
@@ -38,6 +38,9 @@ constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr float kLn2_4 = 0.6931471805599453f;
 // Weights are kept times 2^6: FP16 then holds them from 2^-30 of the largest on.
 constexpr float kLift = 6.0f;
+// ... and a row's reference is raised when a score passes it by 2^8, which leaves
+// them below 2^14; until then what there is needs no rescaling.
+constexpr float kSlack4 = 8.0f;
 
 // Where the join finds a row's pieces.
 struct Row4 {
@@ -53,7 +56,7 @@ struct Att4Layout {
     size_t rows;            // Row4[rows]
     size_t po, pml;         // float[slots][cap][dim], float2[slots][cap]: partial results
     size_t total;
-    int nt, cap;            // column tiles of 8 query rows; rows of a slot
+    int cap;                // query rows of a tile, and of a slot
 };
 
 // The requests on the axis: where each starts, units before it, and pages an item of it has.
@@ -88,7 +91,7 @@ struct Att4Params {
     int k, list_units, list_tiles;   // listed keys: units an item, row tiles a head
     int packed;                      // ... and slots in `list`, in order, instead of positions in `topk`
     int light, heavy;                // what units of up to 16 query rows, and of more, take of the axis
-    int nt, cap, workers;            // workers: of the whole grid
+    int cap, warps;                  // query rows of a tile; warps of the whole grid
     int bf16;                        // type of q and out (else FP16)
     int section, stage;              // bytes of a section, and of a ring stage
     int plan_in_cta;
@@ -118,7 +121,7 @@ __device__ __forceinline__ int worker_at(int64_t u, int64_t T, int64_t W) {
 
 // How many workers share an axis of length T: no more than leave a unit's start to every share.
 __device__ __forceinline__ int64_t sharers(const Att4Params& p, int64_t T) {
-    return max(min(static_cast<int64_t>(p.workers), T / p.heavy), static_cast<int64_t>(T > 0));
+    return max(min(static_cast<int64_t>(p.warps), T / p.heavy), static_cast<int64_t>(T > 0));
 }
 
 // The last request that starts at or before v.
@@ -323,17 +326,11 @@ constexpr int kSmemMost4 = 227 * 1024;
 enum Form { kForm128 = 0, kForm64 = 1, kFormAny128 = 2, kFormAny64 = 3 };
 constexpr bool wide(Form f) { return f == kForm128 || f == kFormAny128; }
 
-// NT column tiles of 8 query rows.  A worker is a warp, or for wide heads under
-// more than 8 query rows a team of two: each scores half of a unit's keys and has
-// the values of half of the columns, so that neither the codes are converted twice
-// nor the accumulators (8 NT registers for 16 columns) leave the registers.
-template <Form kForm, int NT, bool kSelected>
+// Tiles of 8, 16 or 32 query rows; warps of a CTA and stages of a warp's ring.
+template <Form kForm, int kRows>
 struct Shape4 {
-    static constexpr int kTeam = NT > 1 && wide(kForm) ? 2 : 1;
-    static constexpr int kWarps = kTeam == 2 ? (NT == 2 ? 16 : 12) : NT == 4 ? 8 : 12;
+    static constexpr int kWarps = kRows == 8 ? 12 : kRows == 16 ? (wide(kForm) ? 10 : 12) : 8;
     static constexpr int kStages = 2;
-    static constexpr int kWorkers = kWarps / kTeam;
-    static constexpr int kLead = kTeam == 2 ? kStages - 1 : kStages;   // units whose copies are ahead of the one begun
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -380,77 +377,50 @@ struct Item4 {
     int at, n;          // the unit asked for, and the item's units
 };
 
-// What a worker keeps in shared memory besides its ring.
-template <int kSteps, int NT>
+// What a warp keeps in shared memory besides its ring.
+template <int kSteps, int kRows>
 struct QueryDesk {
-    uint2 q[kSteps][NT][32];              // query operands: step, column tile, lane
+    uint4 q[kSteps][kRows / 16][32];      // query operands: step, tile of 16 rows, lane
 };
 template <int kSteps>
-struct QueryDesk<kSteps, 1> {};           // (one column tile's are in registers)
-template <int NT, bool kTeamed>
-struct TeamDesk {
-    uint2 p[4][NT][32];                   // weights as operands: key tile, column tile, lane
-    float top[2][8 * NT], sum[2][8 * NT]; // maxima and sums of the two warps' keys
-};
-template <int NT>
-struct TeamDesk<NT, false> {};
-template <bool kSelected>
-struct ListDesk {
-    int64_t rows[kSelected ? kUnit : 1];  // where listed tokens' codes are
-};
+struct QueryDesk<kSteps, 8> {};           // (those of 8 rows are in registers)
 
-template <Form kForm, int NT, bool kSelected>
-struct Desk4 : QueryDesk<wide(kForm) ? 8 : 4, NT>,
-               TeamDesk<NT, Shape4<kForm, NT, kSelected>::kTeam == 2>,
-               ListDesk<kSelected> {
-    float c[8 * NT];                      // log2(e) scale of the query rows' scores
-    int ends[8 * NT];                     // their bounds
-    uint64_t full[Shape4<kForm, NT, kSelected>::kStages];       // pages: copies that landed
-    uint32_t listed[Shape4<kForm, NT, kSelected>::kStages][2];  // which of a unit's keys are listed
+template <Form kForm, int kRows, bool kSelected>
+struct Desk4 : QueryDesk<wide(kForm) ? 8 : 4, kRows> {
+    uint64_t full[Shape4<kForm, kRows>::kStages];        // pages: copies that landed
+    uint64_t listed[Shape4<kForm, kRows>::kStages];      // which of a unit's keys there are
+    int64_t rows[kSelected ? kUnit : 1];                 // where listed tokens' codes are
+    int ends[8];                                         // tiles of 8 rows: their bounds
     int abort;
 };
 
-template <Form kForm, int NT, bool kSelected>
-struct Worker4 {
-    using S4 = Shape4<kForm, NT, kSelected>;
-    using Desk = Desk4<kForm, NT, kSelected>;
-    static constexpr int kTeam = S4::kTeam;
-    static constexpr int kBlocks = wide(kForm) ? 8 : 4;        // blocks of 16 columns in the scores' product
-    static constexpr int kSteps = kBlocks;                     // ... a step each
-    static constexpr int kMT = kUnit / 16 / kTeam;             // key tiles of 16 that the warp scores
-    static constexpr int kOT = kBlocks / kTeam;                // tiles of 16 value columns that it has
+// What the tiles of 8 rows and those of more share: the layout of a section, and
+// codes as operands.
+template <Form kForm, int kRows, bool kSelected>
+struct Base4 {
+    using Desk = Desk4<kForm, kRows, kSelected>;
+    static constexpr int kBlocks = wide(kForm) ? 8 : 4;        // blocks of 16 columns in registers
+    static constexpr int kSteps = kBlocks;                     // steps of the scores' product, a block's worth each
 
     const Att4Params& p;
     Desk& desk;
-    int lane, g, t, half;
-    uint2 q1[NT == 1 ? kSteps : 1];   // query operands of one column tile
-    float o[kOT][NT][4];
-    float m[NT][2], l[NT][2], c[NT][2];
+    int lane, g, t;
     Item4 item;
     int least;                        // the smallest bound of the item's rows
 
-    __device__ __forceinline__ Worker4(const Att4Params& params, Desk& d) : p(params), desk(d) {
+    __device__ __forceinline__ Base4(const Att4Params& params, Desk& d) : p(params), desk(d) {
         lane = threadIdx.x & 31;
         g = lane >> 2, t = lane & 3;
-        half = kTeam == 2 ? (threadIdx.x >> 5) & 1 : 0;
     }
 
     __device__ __forceinline__ int nblk() const { return kForm == kForm128 ? 8 : kForm == kForm64 ? 4 : p.dim / 16; }
     __device__ __forceinline__ int row_bytes() const { return 8 * nblk(); }
     __device__ __forceinline__ int scale_row() const { return wide(kForm) ? 8 : 4; }
-    __device__ __forceinline__ int codes_bytes() const { return kPage * row_bytes(); }
-    __device__ __forceinline__ int v_off() const { return codes_bytes(); }
-    __device__ __forceinline__ int s_off() const { return 2 * codes_bytes(); }
+    __device__ __forceinline__ int v_off() const { return kPage * row_bytes(); }
+    __device__ __forceinline__ int s_off() const { return 2 * kPage * row_bytes(); }
+    static constexpr bool kFull = kForm == kForm128 || kForm == kForm64;   // no block is missing
 
-    // The warps of the worker have all come here.
-    __device__ __forceinline__ void meet() const {
-        if constexpr (kTeam == 2)
-            asm volatile("bar.sync %0, 64;" ::"r"(static_cast<int>(threadIdx.x >> 6) + 1) : "memory");
-        else
-            __syncwarp();
-    }
-
-    // Which key of eight is operand row i: neighbours differ in parity, and so do those two apart
+    // Which key of eight is operand row (or column) i: neighbours differ in parity, and so do those two apart
     // (rows of keys and of values then meet in fewer banks).
     static __device__ __forceinline__ int key_of(int i) { return i ^ ((i >> 1) & 1); }
 
@@ -458,125 +428,240 @@ struct Worker4 {
     __device__ __forceinline__ int step_block(int s) const {
         return kForm == kForm128 ? 2 * t + (s >> 2) : t + (s & 4);
     }
-    // The thread's value columns, 2 kOT one behind the other, and their block.
-    __device__ __forceinline__ int columns() const { return half * 64 + g * 2 * kOT; }
-    __device__ __forceinline__ int block() const { return kOT == 8 ? g : half * 4 + (g >> 1); }
 
-    // Query operands, bounds and factors of an item.
-    __device__ __forceinline__ void begin(const Item4& x) {
-        item = x;
+    // A query row's columns for the thread's steps, times the power of two that puts the largest of the row next to
+    // 2^14; *c: what the row's scores are multiplied by then (log2(e) scale, the power taken back).
+    __device__ __forceinline__ void load_query(const uint16_t* src, bool on, float (&f)[kSteps][4], float* c) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int j0 = 0; j0 < NT; j0 += kTeam) {
-            const int j = j0 + half;
-            const int n = 8 * j + g;
-            const bool on = n < x.nq;
-            const int at = x.first + (on ? n : 0);
-            const int row = x.row0 + at / p.group, head = x.kvh * p.group + at % p.group;
-            const uint16_t* src = p.q + row * p.qrow + head * p.qhead;
-            float f[kSteps][4];
-            uint32_t top = 0;
-#pragma unroll
-            for (int b = 0; b < kBlocks / 4; ++b) {   // the thread's blocks: steps 4b .. 4b + 3
-                const int blk = step_block(4 * b);
-                uint4 w[2] = {};
-                if (on && blk < nblk()) {
-                    w[0] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk));
-                    w[1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk + 8));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 y = unpack2(p, (&w[i >> 2].x)[i & 3]);
-                    f[4 * b + i / 2][2 * (i & 1)] = y.x;
-                    f[4 * b + i / 2][2 * (i & 1) + 1] = y.y;
-                    top = max(top, max(__float_as_uint(y.x) & 0x7FFFFFFFu, __float_as_uint(y.y) & 0x7FFFFFFFu));
-                }
+        for (int b = 0; b < kBlocks / 4; ++b) {   // the thread's blocks: steps 4b .. 4b + 3
+            const int blk = step_block(4 * b);
+            uint4 w[2] = {};
+            if (on && blk < nblk()) {
+                w[0] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk));
+                w[1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * blk + 8));
             }
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // 2^(14 - power) for the exponent of the head's largest |q|
-            const int power = max(static_cast<int>(top >> 23) - 127, -112);
-            const float up = __int_as_float((127 + 14 - power) << 23);
-            const float down = power >= 14 ? __int_as_float((127 + power - 14) << 23) : 1.0f / up;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-            {
-                const uint2 b =
-                    make_uint2(Fp16::pack(f[s][0] * up, f[s][1] * up), Fp16::pack(f[s][2] * up, f[s][3] * up));
-                if constexpr (NT == 1) q1[s] = b;
-                else desk.q[s][j][lane] = b;
-            }
-            if (t == 0) {
-                desk.c[n] = fminf(fmaxf(p.c * down, 1e-37f), 3e38f);
-                desk.ends[n] = on ? min(max(p.row_ends[row], 0), p.max_keys) : 0x7FFFFFFF;
+            for (int i = 0; i < 8; ++i) {
+                const float2 y = unpack2(p, (&w[i >> 2].x)[i & 3]);
+                f[4 * b + i / 2][2 * (i & 1)] = y.x;
+                f[4 * b + i / 2][2 * (i & 1) + 1] = y.y;
+                top = max(top, max(__float_as_uint(y.x) & 0x7FFFFFFFu, __float_as_uint(y.y) & 0x7FFFFFFFu));
             }
         }
-        meet();
-        least = 0x7FFFFFFF;
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // 2^(14 - power) for the exponent of the row's largest |q|
+        const int power = max(static_cast<int>(top >> 23) - 127, -112);
+        const float up = __int_as_float((127 + 14 - power) << 23);
+        const float down = power >= 14 ? __int_as_float((127 + power - 14) << 23) : 1.0f / up;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = 8 * j + 2 * t + e;
-                c[j][e] = desk.c[n];
-                least = min(least, desk.ends[n]);
-                m[j][e] = -INFINITY;
-                l[j][e] = 0.0f;
-            }
-        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, 1));
-        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, 2));
-#pragma unroll
-        for (int i = 0; i < kOT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
+            for (int i = 0; i < 4; ++i) f[s][i] *= up;
+        *c = fminf(fmaxf(p.c * down, 1e-37f), 3e38f);
     }
 
-    // The scores of the warp's keys under the first N column tiles.
-    template <int N>
-    __device__ __forceinline__ void scores(const uint8_t* stage, float (&s)[kMT][N][4]) {
+    // The (row, head) pair n of the item's tile.
+    __device__ __forceinline__ void pair(int n, int* row, int* head) const {
+        const int at = item.first + n;
+        *row = item.row0 + at / p.group;
+        *head = item.kvh * p.group + at % p.group;
+    }
+
+    // Code words (8 columns each) of a key for the thread's steps, and its scales, each twice.
+    __device__ __forceinline__ void key_words(const uint8_t* stage, int key, uint32_t (&w)[kBlocks / 2],
+                                              uint32_t (&sc)[kBlocks / 4]) const {
+        const uint8_t* row = stage + key * row_bytes();
+        const uint8_t* scales = stage + s_off() + key * 2 * scale_row();
+        if constexpr (kForm == kForm128) {
+            const uint4 x = lds<uint4>(row + 16 * t);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            const uint32_t two = e4m3x2_f16(lds<uint16_t>(scales + 2 * t));
+            sc[0] = __byte_perm(two, 0, 0x1010);
+            sc[1] = __byte_perm(two, 0, 0x3232);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
-        uint32_t w[kMT][2][kBlocks / 2];   // words of 8 codes: rows g and g + 8
-        uint32_t sc[kMT][2][kBlocks / 4];  // a scale twice
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = 16 * (half * kMT + i) + 8 * h + key_of(g);
-                const uint8_t* row = stage + key * row_bytes();
-                const uint8_t* scales = stage + s_off() + key * 2 * scale_row();
-                if constexpr (kForm == kForm128) {
-                    const uint4 x = lds<uint4>(row + 16 * t);
-                    w[i][h][0] = x.x, w[i][h][1] = x.y, w[i][h][2] = x.z, w[i][h][3] = x.w;
-                    const uint32_t two = e4m3x2_f16(lds<uint16_t>(scales + 2 * t));
-                    sc[i][h][0] = __byte_perm(two, 0, 0x1010);
-                    sc[i][h][1] = __byte_perm(two, 0, 0x3232);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < kBlocks / 4; ++b) {
-                        const int blk = t + 4 * b;
-                        uint2 x = {0, 0};
-                        uint32_t one = 0;
-                        if (kForm == kForm64 || blk < nblk()) {
-                            x = lds<uint2>(row + 8 * blk);
-                            one = lds<uint8_t>(scales + blk);
-                        }
-                        w[i][h][2 * b] = x.x, w[i][h][2 * b + 1] = x.y;
-                        sc[i][h][b] = __byte_perm(e4m3x2_f16(one), 0, 0x1010);
-                    }
+            for (int b = 0; b < kBlocks / 4; ++b) {
+                const int blk = t + 4 * b;
+                uint2 x = {0, 0};
+                uint32_t one = 0;
+                if (kFull || blk < nblk()) {
+                    x = lds<uint2>(row + 8 * blk);
+                    one = lds<uint8_t>(scales + blk);
                 }
+                w[2 * b] = x.x, w[2 * b + 1] = x.y;
+                sc[b] = __byte_perm(e4m3x2_f16(one), 0, 0x1010);
             }
+        }
+    }
+
+    // Values of keys 2t, 2t + 1, 2t + 8, 2t + 9 (as operands count them) of key tile i, in the thread's columns (2
+    // kBlocks one behind the other from 2 kBlocks g): pairs of the first two keys and of the others, even columns and
+    // odd ones.  `use(x, z, ...)` gets columns 8x + 2z and 8x + 2z + 1.
+    template <typename Use>
+    __device__ __forceinline__ void value_words(const uint8_t* stage, int i, Use use) const {
+        const int blk = kBlocks == 8 ? g : g >> 1;
+        uint2 v[4];
+        uint32_t one[4];
 #pragma unroll
-        for (int x = 0; x < kSteps / 2; ++x) {   // a word: two steps
-            uint2 qs[2][N];
+        for (int z = 0; z < 4; ++z) {
+            const int key = 16 * i + 8 * (z >> 1) + key_of(2 * t + (z & 1));
+            const uint8_t* row = stage + v_off() + key * row_bytes() + g * kBlocks;
+            const uint8_t* scales = stage + s_off() + (key * 2 + 1) * scale_row();
+            v[z] = make_uint2(0, 0);
+            one[z] = 0;
+            if (kFull || blk < nblk()) {
+                if constexpr (kBlocks == 8) v[z] = lds<uint2>(row);
+                else v[z].x = lds<uint32_t>(row);
+                one[z] = lds<uint8_t>(scales + blk);
+            }
+        }
+        const uint32_t sa = e4m3x2_f16(one[0] | one[1] << 8), sb = e4m3x2_f16(one[2] | one[3] << 8);
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+        for (int x = 0; x < kBlocks / 4; ++x) {
+            const uint32_t k0 = x ? v[0].y : v[0].x, k1 = x ? v[1].y : v[1].x;
+            const uint32_t k2 = x ? v[2].y : v[2].x, k3 = x ? v[3].y : v[3].x;
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8((k0 & 0x0F0F0F0Fu) | (k1 << 4 & 0xF0F0F0F0u), a0);
+            e2m1x8((k0 >> 4 & 0x0F0F0F0Fu) | (k1 & 0xF0F0F0F0u), a1);
+            e2m1x8((k2 & 0x0F0F0F0Fu) | (k3 << 4 & 0xF0F0F0F0u), a2);
+            e2m1x8((k2 >> 4 & 0x0F0F0F0Fu) | (k3 & 0xF0F0F0F0u), a3);
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    if constexpr (NT == 1) qs[z][j] = q1[2 * x + z];
-                    else qs[z][j] = desk.q[2 * x + z][j][lane];
-                }
+            for (int z = 0; z < 4; ++z)
+                use(x, z, hmul2(a0[z], sa), hmul2(a1[z], sa), hmul2(a2[z], sb), hmul2(a3[z], sb));
+        }
+    }
+
+    // Whether a value scale is NaN (two keys a lane); the padding of a scale row holds anything.
+    __device__ __forceinline__ bool any_nan(const uint8_t* stage) const {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* at = stage + s_off() + ((lane + 32 * h) * 2 + 1) * scale_row();
+            bad |= nan4(lds<uint32_t>(at) & scale_bytes(0));
+            if (wide(kForm)) bad |= nan4(lds<uint32_t>(at + 4) & scale_bytes(4));
+        }
+        return __any_sync(0xFFFFFFFFu, bad != 0);
+    }
+    __device__ __forceinline__ uint32_t scale_bytes(int first) const {
+        return kFull || nblk() >= first + 4 ? ~0u : nblk() <= first ? 0u : (1u << 8 * (nblk() - first)) - 1;
+    }
+    __device__ __forceinline__ bool nan_at(const uint8_t* stage, int key, int blk) const {
+        return blk < nblk() && (lds<uint8_t>(stage + s_off() + (key * 2 + 1) * scale_row() + blk) & 0x7F) == 0x7F;
+    }
+    // Their bytes become zero (the columns they enter have become NaN for the rows that see the key, and for nobody
+    // else).
+    __device__ __forceinline__ void clear_nan(uint8_t* stage) const {
+        __syncwarp();
+#pragma unroll 1
+        for (int i = lane; i < kUnit * nblk(); i += 32) {
+            const int key = i / nblk(), blk = i - key * nblk();
+            if (nan_at(stage, key, blk)) stage[s_off() + (key * 2 + 1) * scale_row() + blk] = 0;
+        }
+        __syncwarp();
+        fence_proxy_async_smem();   // (the next copy into the stage is the asynchronous proxy's)
+    }
+
+    // Columns col .. col + n - 1 (n of 16 or 8) of pair n's output, or of a piece's.
+    template <int kCols>
+    __device__ __forceinline__ void write(int64_t slot, int n, int col, const float (&o)[kCols], float inv) const {
+        if (slot >= 0) {
+            float* dst = p.po + (slot * p.cap + n) * p.dim + col;
+#pragma unroll
+            for (int i = 0; i < kCols; i += 4)
+                *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else {
+            int row, head;
+            pair(n, &row, &head);
+            uint16_t* dst = p.out + row * p.orow + head * p.ohead + col;
+#pragma unroll
+            for (int i = 0; i < kCols; i += 8)
+                *reinterpret_cast<uint4*>(dst + i) =
+                    make_uint4(pack2(p, o[i] * inv, o[i + 1] * inv), pack2(p, o[i + 2] * inv, o[i + 3] * inv),
+                               pack2(p, o[i + 4] * inv, o[i + 5] * inv), pack2(p, o[i + 6] * inv, o[i + 7] * inv));
+        }
+    }
+    // Pair n's reference (times c) and sum of weights.
+    __device__ __forceinline__ void write_sum(int64_t slot, int n, float top, float sum) const {
+        if (slot >= 0) {
+            p.pml[slot * p.cap + n] = make_float2(sum == 0.0f ? -INFINITY : top, sum);
+        } else if (p.lse) {
+            int row, head;
+            pair(n, &row, &head);
+            p.lse[static_cast<int64_t>(row) * p.heads + head] =
+                sum == 0.0f ? -INFINITY : (top + log2f(sum) - kLift) * kLn2_4;
+        }
+    }
+};
+
+// Up to 8 query rows: keys (then value columns) are the 16 operand rows and query
+// rows the 8 columns, so that few rows waste nothing.  The scores' accumulators
+// become the values' second operand by a transposition in registers.
+template <Form kForm, bool kSelected>
+struct Few4 : Base4<kForm, 8, kSelected> {
+    using B = Base4<kForm, 8, kSelected>;
+    using B::p, B::desk, B::lane, B::g, B::t, B::item, B::least, B::nblk, B::key_of;
+    static constexpr int kBlocks = B::kBlocks, kSteps = B::kSteps;
+    static constexpr int kMT = kUnit / 16;
+
+    uint2 q[kSteps];                       // query operands
+    float o[kBlocks][4];                   // columns' tiles: rows g and g + 8 are columns 2i and 2i + 1
+    float ref[2], l[2], c[2], limit[2];    // query rows 2t, 2t + 1: reference, sum, factor, where the reference is raised
+
+    __device__ __forceinline__ Few4(const Att4Params& params, typename B::Desk& d) : B(params, d) {}
+
+    __device__ __forceinline__ void begin(const Item4& x) {
+        item = x;
+        const bool on = g < x.nq;
+        int row, head;
+        B::pair(on ? g : 0, &row, &head);
+        float f[kSteps][4], cj;
+        B::load_query(p.q + row * p.qrow + head * p.qhead, on, f, &cj);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[s] = make_uint2(Fp16::pack(f[s][0], f[s][1]), Fp16::pack(f[s][2], f[s][3]));
+        const int e = on ? min(max(p.row_ends[row], 0), p.max_keys) : 0x7FFFFFFF;
+        if (t == 0) desk.ends[g] = e;
+        least = e;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            c[i] = __shfl_sync(0xFFFFFFFFu, cj, (2 * t + i) * 4);
+            ref[i] = l[i] = 0.0f;
+            limit[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ bool sees(int e, int key, int key_base, uint64_t listed) const {
+        return kSelected ? (listed >> key & 1) : key_base + key < desk.ends[2 * t + e];
+    }
+
+    __device__ __forceinline__ void unit(uint8_t* stage, int key_base, uint64_t listed) {
+        if (B::any_nan(stage)) {
+#pragma unroll 1
+            for (int key = 0; key < kUnit; ++key)
+                if (B::nan_at(stage, key, kBlocks == 8 ? g : g >> 1))
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (sees(e, key, key_base, listed))
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i) o[i][e] = o[i][e + 2] = __int_as_float(0x7FC00000);
+            B::clear_nan(stage);
+        }
+        float s[kMT][4];
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+        uint32_t w[kMT][2][kBlocks / 2], sc[kMT][2][kBlocks / 4];   // keys g and g + 8 of a tile
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) B::key_words(stage, 16 * i + 8 * h + key_of(g), w[i][h], sc[i][h]);
+#pragma unroll
+        for (int x = 0; x < kSteps / 2; ++x)   // a word: two steps
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
                 uint32_t a[4], b[4];
@@ -589,287 +674,285 @@ struct Worker4 {
                 }
 #pragma unroll
                 for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        mma16816(s[i][j], a[2 * z], b[2 * z], a[2 * z + 1], b[2 * z + 1], qs[z][j].x, qs[z][j].y);
+                    mma16816(s[i], a[2 * z], b[2 * z], a[2 * z + 1], b[2 * z + 1], q[2 * x + z].x, q[2 * x + z].y);
             }
-        }
-    }
-
-    __device__ __forceinline__ bool sees(int j, int e, int key, int key_base, uint64_t listed) const {
-        return kSelected ? (listed >> key & 1) : key_base + key < desk.ends[8 * j + 2 * t + e];
-    }
-
-    // Scores of keys that a row does not see.
-    template <int N>
-    __device__ __forceinline__ void mask(int key_base, uint64_t listed, float (&s)[kMT][N][4]) {
-        if (kSelected ? listed == ~0ull : key_base + kUnit <= least) return;
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = 16 * (half * kMT + i) + 8 * (e >> 1) + key_of(g);
-                    if (!sees(j, e & 1, key, key_base, listed)) s[i][j][e] = -INFINITY;
-                }
-    }
-
-    // The largest score of each column among the warp's keys.
-    template <int N>
-    __device__ __forceinline__ void maxima(const float (&s)[kMT][N][4], float (&x)[N][2]) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                x[j][e] = fmaxf(s[0][j][e], s[0][j][e + 2]);
-#pragma unroll
-                for (int i = 1; i < kMT; ++i) x[j][e] = fmaxf(x[j][e], fmaxf(s[i][j][e], s[i][j][e + 2]));
-                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 4));
-                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 8));
-                x[j][e] = fmaxf(x[j][e], __shfl_xor_sync(0xFFFFFFFFu, x[j][e], 16));
-            }
-    }
-
-    // The weights of the warp's keys as operands, under the columns' maxima x of the unit; what there is so far is
-    // brought to the new maxima.
-    template <int N>
-    __device__ __forceinline__ void weights(const float (&s)[kMT][N][4], const float (&x)[N][2],
-                                            uint2 (&pb)[kMT][N]) {
-        bool raised = false;
-        float ref[N][2], keep[N][2];
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float top = fmaxf(x[j][e], m[j][e]);
-                raised |= top > m[j][e];
-                ref[j][e] = top == -INFINITY ? 0.0f : top;
-                keep[j][e] = ex2_4((m[j][e] - ref[j][e]) * c[j][e]);
-                m[j][e] = top;
-            }
-        if (__any_sync(0xFFFFFFFFu, raised)) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                l[j][0] *= keep[j][0], l[j][1] *= keep[j][1];
-#pragma unroll
-                for (int i = 0; i < kOT; ++i) {
-                    o[i][j][0] *= keep[j][0], o[i][j][2] *= keep[j][0];
-                    o[i][j][1] *= keep[j][1], o[i][j][3] *= keep[j][1];
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int i = 0; i < kMT; ++i) {
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // (the difference first: a large score times c would leave its rounding in the exponent)
-                    w[e] = ex2_4(__fmaf_rn(s[i][j][e] - ref[j][e & 1], c[j][e & 1], kLift));
-                    l[j][e & 1] += w[e];
-                }
-                pb[i][j] = make_uint2(transpose8x8(Fp16::pack(w[0], w[1])), transpose8x8(Fp16::pack(w[2], w[3])));
-            }
-    }
-
-    // The values of key tile i under its weights.
-    template <int N>
-    __device__ __forceinline__ void values(const uint8_t* stage, int i, const uint2 (&pb)[N]) {
-        uint2 v[4];          // codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 (operand rows), the thread's columns
-        uint32_t one[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            const int key = 16 * i + 8 * (z >> 1) + key_of(2 * t + (z & 1));
-            const uint8_t* row = stage + v_off() + key * row_bytes() + columns() / 2;
-            const uint8_t* scales = stage + s_off() + (key * 2 + 1) * scale_row();
-            v[z] = make_uint2(0, 0);
-            one[z] = 0;
-            if (kForm == kForm128 || kForm == kForm64 || block() < nblk()) {
-                if constexpr (kOT == 8) v[z] = lds<uint2>(row);
-                else v[z].x = lds<uint32_t>(row);
-                one[z] = lds<uint8_t>(scales + block());
-            }
-        }
-        const uint32_t sa = e4m3x2_f16(one[0] | one[1] << 8), sb = e4m3x2_f16(one[2] | one[3] << 8);
-#pragma unroll
-        for (int x = 0; x < kOT / 4; ++x) {   // a word: four column tiles
-            const uint32_t k0 = x ? v[0].y : v[0].x, k1 = x ? v[1].y : v[1].x;
-            const uint32_t k2 = x ? v[2].y : v[2].x, k3 = x ? v[3].y : v[3].x;
-            uint32_t a0[4], a1[4], a2[4], a3[4];   // even columns (operand rows 0-7), odd columns (8-15)
-            e2m1x8((k0 & 0x0F0F0F0Fu) | (k1 << 4 & 0xF0F0F0F0u), a0);
-            e2m1x8((k0 >> 4 & 0x0F0F0F0Fu) | (k1 & 0xF0F0F0F0u), a1);
-            e2m1x8((k2 & 0x0F0F0F0Fu) | (k3 << 4 & 0xF0F0F0F0u), a2);
-            e2m1x8((k2 >> 4 & 0x0F0F0F0Fu) | (k3 & 0xF0F0F0F0u), a3);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                a0[z] = hmul2(a0[z], sa), a1[z] = hmul2(a1[z], sa);
-                a2[z] = hmul2(a2[z], sb), a3[z] = hmul2(a3[z], sb);
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    mma16816(o[4 * x + z][j], a0[z], a1[z], a2[z], a3[z], pb[j].x, pb[j].y);
-            }
-        }
-    }
-
-    // Value scales that are NaN: the columns they enter become NaN for the rows that see the key, and the bytes zero,
-    // so that nobody else's do.
-    template <int N>
-    __device__ __forceinline__ void poison(uint8_t* stage, int key_base, uint64_t listed) {
-        const int blk = block();
-#pragma unroll 1
-        for (int key = 0; key < kUnit; ++key) {
-            uint8_t* const at = stage + s_off() + (key * 2 + 1) * scale_row() + blk;
-            const bool bad = blk < nblk() && (lds<uint8_t>(at) & 0x7F) == 0x7F;
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (bad && sees(j, e, key, key_base, listed))
-#pragma unroll
-                        for (int i = 0; i < kOT; ++i) o[i][j][e] = o[i][j][e + 2] = __int_as_float(0x7FC00000);
-            __syncwarp();
-            if (bad) *at = 0;
-        }
-        __syncwarp();
-        fence_proxy_async_smem();   // (the next copy into the stage is the asynchronous proxy's)
-    }
-
-    // Looks for value scales that are NaN among the warp's blocks, two keys a lane.
-    template <int N>
-    __device__ __forceinline__ void check(uint8_t* stage, int key_base, uint64_t listed) {
-        constexpr bool kBoth = wide(kForm) && kTeam == 1;   // two words of four blocks, or the warp's one
-        const int from = kTeam == 2 ? half * 4 : 0;
-        uint32_t bad = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint8_t* at = stage + s_off() + ((lane + 32 * h) * 2 + 1) * scale_row();
-            bad |= nan4(lds<uint32_t>(at + from) & scale_bytes(from));
-            if (kBoth) bad |= nan4(lds<uint32_t>(at + 4) & scale_bytes(4));
-        }
-        if (__any_sync(0xFFFFFFFFu, bad != 0)) poison<N>(stage, key_base, listed);
-    }
-    // The bytes of a scale row's word from `first` on that are scales (the row's padding holds anything).
-    __device__ __forceinline__ uint32_t scale_bytes(int first) const {
-        return kForm == kForm128 || kForm == kForm64 || nblk() >= first + 4 ? ~0u
-               : nblk() <= first                                             ? 0u
-                                                                             : (1u << 8 * (nblk() - first)) - 1;
-    }
-
-    // A unit that has landed in its stage (or not in time: true is returned).  `issue` orders the copies that the
-    // unit's progress makes room for.
-    template <int N, typename Issue>
-    __device__ __forceinline__ bool unit(uint8_t* stage, int key_base, uint64_t listed, bool any, Issue issue) {
-        float s[kMT][N][4], x[N][2];
-        uint2 pb[kMT][N];
-        if constexpr (kTeam == 1) {
-            __syncwarp();
-            if (!kSelected && *static_cast<volatile int*>(&desk.abort)) return true;
-            if (any) {
-                check<N>(stage, key_base, listed);
-                scores<N>(stage, s);
-                mask<N>(key_base, listed, s);
-                maxima<N>(s, x);
-                weights<N>(s, x, pb);
-#pragma unroll
-                for (int i = 0; i < kMT; ++i) values<N>(stage, i, pb[i]);
-            }
-            __syncwarp();
-            issue();
-            __syncwarp();
-        } else {
-            if (any) {
-                scores<N>(stage, s);
-                mask<N>(key_base, listed, s);
-                maxima<N>(s, x);
-                if (g == 0)
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        *reinterpret_cast<float2*>(&desk.top[half][8 * j + 2 * t]) = make_float2(x[j][0], x[j][1]);
-            }
-            meet();
-            // (seen alike by both warps: neither waits for the next unit before they have met again)
-            const bool gave_up = !kSelected && *static_cast<volatile int*>(&desk.abort) != 0;
-            if (!gave_up) issue();
-            if (gave_up || !any) {
-                meet();
-                return gave_up;
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float2 y = *reinterpret_cast<const float2*>(&desk.top[half ^ 1][8 * j + 2 * t]);
-                x[j][0] = fmaxf(x[j][0], y.x), x[j][1] = fmaxf(x[j][1], y.y);
-            }
-            check<N>(stage, key_base, listed);
-            weights<N>(s, x, pb);
+        if (kSelected ? listed != ~0ull : key_base + kUnit > least) {
 #pragma unroll
             for (int i = 0; i < kMT; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j) desk.p[half * kMT + i][j][lane] = pb[i][j];
-            meet();
+                for (int e = 0; e < 4; ++e)
+                    if (!sees(e & 1, 16 * i + 8 * (e >> 1) + key_of(g), key_base, listed)) s[i][e] = -INFINITY;
+        }
+        // The reference is raised when a score passes it by kSlack powers of two; until then O and l stay.
+        float top[2];
 #pragma unroll
-            for (int i = 0; i < 2 * kMT; ++i) {
-                uint2 w[N];
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(s[0][e], s[0][e + 2]);
 #pragma unroll
-                for (int j = 0; j < N; ++j) w[j] = desk.p[i][j][lane];
-                values<N>(stage, i, w);
+            for (int i = 1; i < kMT; ++i) top[e] = fmaxf(top[e], fmaxf(s[i][e], s[i][e + 2]));
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > limit[0] || top[1] > limit[1])) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], d));
+                if (top[e] > limit[e]) {
+                    const float keep = limit[e] == -INFINITY ? 0.0f : ex2_4((ref[e] - top[e]) * c[e]);
+                    ref[e] = top[e];
+                    limit[e] = top[e] + kSlack4 / c[e];
+                    l[e] *= keep;
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i) o[i][e] *= keep, o[i][e + 2] *= keep;
+                }
             }
         }
-        return false;
+        uint32_t pb[kMT][2];
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (the difference first: a large score times c would leave its rounding in the exponent)
+                y[e] = ex2_4(__fmaf_rn(s[i][e] - ref[e & 1], c[e & 1], kLift));
+                l[e & 1] += y[e];
+            }
+            pb[i][0] = transpose8x8(Fp16::pack(y[0], y[1]));
+            pb[i][1] = transpose8x8(Fp16::pack(y[2], y[3]));
+        }
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+            B::value_words(stage, i, [&](int x, int z, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                mma16816(o[4 * x + z], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+            });
     }
 
     // The item's result, or the partial one of a piece (slot >= 0).
     __device__ __forceinline__ void finish(int64_t slot) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 4);
-                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 8);
-                l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 16);
-                if constexpr (kTeam == 2)
-                    if (g == 0) desk.sum[half][8 * j + 2 * t + e] = l[j][e];
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const int n = 2 * t + e;
+            if (n >= item.nq) continue;
+            float y[2 * kBlocks];
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) y[2 * i] = o[i][e], y[2 * i + 1] = o[i][e + 2];
+            if (B::kFull || (kBlocks == 8 ? g : g >> 1) < nblk())
+                B::write(slot, n, g * 2 * kBlocks, y, sum == 0.0f ? 0.0f : p.v_scale / sum);
+            if (g == 0) B::write_sum(slot, n, ref[e] * c[e], sum);
+        }
+    }
+};
+
+// 16 or 32 query rows: they are the operand rows, keys (then value columns) the
+// columns, and the scores' accumulators are the values' first operand as they are.
+template <Form kForm, int kRows, bool kSelected>
+struct Many4 : Base4<kForm, kRows, kSelected> {
+    using B = Base4<kForm, kRows, kSelected>;
+    using B::p, B::desk, B::lane, B::g, B::t, B::item, B::least, B::nblk, B::key_of;
+    static constexpr int kBlocks = B::kBlocks, kSteps = B::kSteps;
+    static constexpr int kTiles = kRows / 16;
+    static constexpr int kOT = 2 * kBlocks;                  // tiles of 8 value columns: column n * kOT + i is n of tile i
+    static constexpr int kMT = kRows == 16 ? 4 : 2;          // tiles of 16 keys whose scores are in registers at once
+
+    float o[kOT][kTiles][4];
+    // query rows 16r + g and 16r + g + 8: reference, sum, factor, where the reference is raised, bound
+    float ref[kTiles][2], l[kTiles][2], c[kTiles][2], limit[kTiles][2];
+    int end[kTiles][2];
+
+    __device__ __forceinline__ Many4(const Att4Params& params, typename B::Desk& d) : B(params, d) {}
+
+    __device__ __forceinline__ void begin(const Item4& x) {
+        item = x;
+        least = 0x7FFFFFFF;
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r) {
+            uint2 a[2][kSteps];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 16 * r + 8 * h + g;
+                const bool on = n < x.nq;
+                int row, head;
+                B::pair(on ? n : 0, &row, &head);
+                float f[kSteps][4];
+                B::load_query(p.q + row * p.qrow + head * p.qhead, on, f, &c[r][h]);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    a[h][s] = make_uint2(Fp16::pack(f[s][0], f[s][1]), Fp16::pack(f[s][2], f[s][3]));
+                end[r][h] = on ? min(max(p.row_ends[row], 0), p.max_keys) : 0x7FFFFFFF;
+                least = min(least, end[r][h]);
+                ref[r][h] = l[r][h] = 0.0f;
+                limit[r][h] = -INFINITY;
             }
-        if constexpr (kTeam == 2) meet();
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+            for (int s = 0; s < kSteps; ++s) desk.q[s][r][lane] = make_uint4(a[0][s].x, a[1][s].x, a[0][s].y, a[1][s].y);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = 8 * j + 2 * t + e;
-                if (n >= item.nq) continue;
-                float sum = l[j][e];
-                if constexpr (kTeam == 2) sum = desk.sum[0][n] + desk.sum[1][n];
-                const bool cols = kForm == kForm128 || kForm == kForm64 || block() < nblk();
-                const bool first = g == 0 && half == 0;
-                const float top = m[j][e] * c[j][e];
-                if (slot >= 0) {
-                    float* dst = p.po + (slot * p.cap + n) * p.dim + columns();
-                    if (cols)
+            for (int i = 0; i < kOT; ++i) o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.0f;
+        }
 #pragma unroll
-                        for (int i = 0; i < kOT; i += 2)
-                            *reinterpret_cast<float4*>(dst + 2 * i) =
-                                make_float4(o[i][j][e], o[i][j][e + 2], o[i + 1][j][e], o[i + 1][j][e + 2]);
-                    if (first) p.pml[slot * p.cap + n] = make_float2(m[j][e] == -INFINITY ? -INFINITY : top, sum);
-                } else {
-                    const int row = item.row0 + (item.first + n) / p.group;
-                    const int head = item.kvh * p.group + (item.first + n) % p.group;
-                    const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
-                    uint16_t* dst = p.out + row * p.orow + head * p.ohead + columns();
-                    if (cols)
+        for (int d = 4; d < 32; d <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ bool sees(int r, int h, int key, int key_base, uint64_t listed) const {
+        return kSelected ? (listed >> key & 1) : key_base + key < end[r][h];
+    }
+
+    // The unit's keys under the first R tiles of 16 rows.
+    template <int R>
+    __device__ __forceinline__ void unit(uint8_t* stage, int key_base, uint64_t listed) {
+        if (B::any_nan(stage)) {
+#pragma unroll 1
+            for (int key = 0; key < kUnit; ++key)
 #pragma unroll
-                        for (int i = 0; i < kOT; i += 4)
-                            *reinterpret_cast<uint4*>(dst + 2 * i) =
-                                make_uint4(pack2(p, o[i][j][e] * inv, o[i][j][e + 2] * inv),
-                                           pack2(p, o[i + 1][j][e] * inv, o[i + 1][j][e + 2] * inv),
-                                           pack2(p, o[i + 2][j][e] * inv, o[i + 2][j][e + 2] * inv),
-                                           pack2(p, o[i + 3][j][e] * inv, o[i + 3][j][e + 2] * inv));
-                    if (first && p.lse)
-                        p.lse[static_cast<int64_t>(row) * p.heads + head] =
-                            sum == 0.0f ? -INFINITY : (top + log2f(sum) - kLift) * kLn2_4;
+                for (int e = 0; e < 2; ++e)
+                    if (B::nan_at(stage, key, kBlocks == 8 ? 2 * t + e : t))
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (sees(r, h, key, key_base, listed))
+#pragma unroll
+                                    for (int i = 0; i < kOT; ++i) o[i][r][2 * h + e] = __int_as_float(0x7FC00000);
+            B::clear_nan(stage);
+        }
+        const bool all_see = kSelected ? listed == ~0ull : key_base + kUnit <= least;
+#pragma unroll 1
+        for (int first = 0; first < kUnit / 16; first += kMT) {   // tiles of 16 keys, two of 8 each
+            float s[2 * kMT][R][4];
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i)
+#pragma unroll
+                for (int r = 0; r < R; ++r) s[i][r][0] = s[i][r][1] = s[i][r][2] = s[i][r][3] = 0.0f;
+            uint32_t w[2 * kMT][kBlocks / 2], sc[2 * kMT][kBlocks / 4];
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i) B::key_words(stage, 16 * first + 8 * i + key_of(g), w[i], sc[i]);
+#pragma unroll
+            for (int x = 0; x < kSteps / 2; ++x) {   // a word: two steps
+                uint4 q[2][R];
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) q[z][r] = desk.q[2 * x + z][r][lane];
+#pragma unroll
+                for (int i = 0; i < 2 * kMT; ++i) {
+                    uint32_t b[4];
+                    e2m1x8(w[i][x], b);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) b[z] = hmul2(b[z], sc[i][x / 2]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            mma16816(s[i][r], q[z][r].x, q[z][r].y, q[z][r].z, q[z][r].w, b[2 * z], b[2 * z + 1]);
                 }
             }
+            if (!all_see) {
+#pragma unroll
+                for (int i = 0; i < 2 * kMT; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!sees(r, e >> 1, 16 * first + 8 * i + key_of(2 * t + (e & 1)), key_base, listed))
+                                s[i][r][e] = -INFINITY;
+            }
+            // The reference is raised when a score passes it by kSlack powers of two; until then O and l stay.
+            float top[R][2];
+            bool raised = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[r][h] = fmaxf(s[0][r][2 * h], s[0][r][2 * h + 1]);
+#pragma unroll
+                    for (int i = 1; i < 2 * kMT; ++i)
+                        top[r][h] = fmaxf(top[r][h], fmaxf(s[i][r][2 * h], s[i][r][2 * h + 1]));
+                    raised |= top[r][h] > limit[r][h];
+                }
+            if (__any_sync(0xFFFFFFFFu, raised)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        top[r][h] = fmaxf(top[r][h], __shfl_xor_sync(0xFFFFFFFFu, top[r][h], 1));
+                        top[r][h] = fmaxf(top[r][h], __shfl_xor_sync(0xFFFFFFFFu, top[r][h], 2));
+                        if (top[r][h] > limit[r][h]) {
+                            const float keep =
+                                limit[r][h] == -INFINITY ? 0.0f : ex2_4((ref[r][h] - top[r][h]) * c[r][h]);
+                            ref[r][h] = top[r][h];
+                            limit[r][h] = top[r][h] + kSlack4 / c[r][h];
+                            l[r][h] *= keep;
+#pragma unroll
+                            for (int i = 0; i < kOT; ++i) o[i][r][2 * h] *= keep, o[i][r][2 * h + 1] *= keep;
+                        }
+                    }
+            }
+            uint32_t a[2 * kMT][R][2];
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float y[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // (the difference first: a large score times c would leave its rounding in the exponent)
+                            y[e] = ex2_4(__fmaf_rn(s[i][r][2 * h + e] - ref[r][h], c[r][h], kLift));
+                            l[r][h] += y[e];
+                        }
+                        a[i][r][h] = Fp16::pack(y[0], y[1]);
+                    }
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+                B::value_words(stage, first + i, [&](int x, int z, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        mma16816(o[8 * x + 2 * z][r], a[2 * i][r][0], a[2 * i][r][1], a[2 * i + 1][r][0],
+                                 a[2 * i + 1][r][1], a0, a2);
+                        mma16816(o[8 * x + 2 * z + 1][r], a[2 * i][r][0], a[2 * i][r][1], a[2 * i + 1][r][0],
+                                 a[2 * i + 1][r][1], a1, a3);
+                    }
+                });
+        }
     }
+    __device__ __forceinline__ void unit(uint8_t* stage, int key_base, uint64_t listed) {
+        if (kTiles == 2 && item.nq > 16) unit<kTiles>(stage, key_base, listed);
+        else unit<1>(stage, key_base, listed);
+    }
+
+    __device__ __forceinline__ void finish(int64_t slot) {
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sum = l[r][h];
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                const int n = 16 * r + 8 * h + g;
+                if (n >= item.nq) continue;
+                const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float y[kOT];
+#pragma unroll
+                    for (int i = 0; i < kOT; ++i) y[i] = o[i][r][2 * h + e];
+                    if (B::kFull || (kBlocks == 8 ? 2 * t + e : t) < nblk()) B::write(slot, n, (2 * t + e) * kOT, y, inv);
+                }
+                if (t == 0) B::write_sum(slot, n, ref[r][h] * c[r][h], sum);
+            }
+    }
+};
+
+template <Form kForm, int kRows, bool kSelected>
+struct Worker4 : Many4<kForm, kRows, kSelected> {
+    using Many4<kForm, kRows, kSelected>::Many4;
+};
+template <Form kForm, bool kSelected>
+struct Worker4<kForm, 8, kSelected> : Few4<kForm, kSelected> {
+    using Few4<kForm, kSelected>::Few4;
 };
 
 constexpr int kAxisBytes4 = (2 * (kCtaRequests + 1) + 66) * 8 + kCtaRequests * 4;
@@ -923,23 +1006,21 @@ __device__ __forceinline__ Unit4 listed_unit(const Att4Params& p, const int* sta
     return x;
 }
 
-// Shared memory: the workers' rings, their desks, then the axis.
-template <Form kForm, int NT, bool kSelected>
-__global__ void __launch_bounds__((Shape4<kForm, NT, kSelected>::kWarps * 32), 1)
-attend_fp4_kernel(const Att4Params p) {
-    using S4 = Shape4<kForm, NT, kSelected>;
-    using W4 = Worker4<kForm, NT, kSelected>;
-    using Desk = Desk4<kForm, NT, kSelected>;
-    constexpr int kTeam = S4::kTeam, kStages = S4::kStages, kLead = S4::kLead;
+// Shared memory: the warps' rings, their desks, then the axis.
+template <Form kForm, int kRows, bool kSelected>
+__global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend_fp4_kernel(const Att4Params p) {
+    using S4 = Shape4<kForm, kRows>;
+    using W4 = Worker4<kForm, kRows, kSelected>;
+    using Desk = Desk4<kForm, kRows, kSelected>;
+    constexpr int kStages = S4::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, worker = threadIdx.x / (32 * kTeam);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    uint8_t* const ring = smem + worker * kStages * p.stage;
-    Desk& desk = reinterpret_cast<Desk*>(smem + S4::kWorkers * kStages * p.stage)[worker];
+    uint8_t* const ring = smem + warp * kStages * p.stage;
+    Desk& desk = reinterpret_cast<Desk*>(smem + S4::kWarps * kStages * p.stage)[warp];
     W4 k(p, desk);
-    const bool leads = k.half == 0;      // the warp that looks units up and orders pages
-    if (leads && lane == 0) {
+    if (lane == 0) {
         if (!kSelected) {
             for (int i = 0; i < kStages; ++i) mbar_init(&desk.full[i], 1);
             mbar_fence_init();
@@ -948,7 +1029,7 @@ attend_fp4_kernel(const Att4Params p) {
     }
     Axis4 axis = p.axis;
     const int* starts = p.starts;
-    uint8_t* const table = smem + S4::kWorkers * (kStages * p.stage + sizeof(Desk));
+    uint8_t* const table = smem + S4::kWarps * (kStages * p.stage + sizeof(Desk));
     if (!kSelected && p.plan_in_cta) {
         axis.prefix = reinterpret_cast<int64_t*>(table);
         axis.units = axis.prefix + kCtaRequests + 1;
@@ -967,11 +1048,11 @@ attend_fp4_kernel(const Att4Params p) {
         if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
         __syncthreads();
     }
-    k.meet();
+    __syncwarp();
     const int64_t total = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles * p.list_units
                                     : axis.prefix[p.R];
     const int64_t W = sharers(p, total);
-    const int w = worker * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
+    const int w = warp * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
     if (w >= W) return;
     int64_t u0 = share4(w, total, W), u1 = share4(w + 1, total, W);
     if (!kSelected) u0 = unit_at(p, axis, u0), u1 = unit_at(p, axis, u1);
@@ -990,7 +1071,7 @@ attend_fp4_kernel(const Att4Params p) {
         if (i % 32 == 0) look_up(i);
         if (lane == i % 32) {
             uint64_t* const bar = &desk.full[i % kStages];
-            desk.listed[i % kStages][0] = mine.page >= 0;
+            desk.listed[i % kStages] = mine.page >= 0;
             if (mine.page >= 0) {
                 mbar_arrive_expect_tx(bar, p.section);
                 const uint8_t* src = p.cache + mine.page * p.page_stride + mine.kvh * p.head_stride;
@@ -1003,17 +1084,15 @@ attend_fp4_kernel(const Att4Params p) {
         }
     };
 
-    // Listed keys: two tokens a lane, or one where two warps share them.  While a unit is in work, the pages of the
-    // unit kLead on are looked up and the positions of the one behind it loaded.
-    constexpr int kTokens = 2 / kTeam;
-    int pos[kTokens], page[kTokens], ahead[kTokens];
+    // Listed keys, two tokens a lane: while a unit is in work, the pages of the unit kStages on are looked up and the
+    // positions of the one behind it loaded.
+    int pos[2], page[2], ahead[2];
     struct List {
         int req, kvh, bound;
     } next, later;                       // the units of pos / page, and of ahead
-    const int token0 = k.half * 32 + lane;
     auto load_positions = [&](int i) {   // into ahead / later
 #pragma unroll
-        for (int h = 0; h < kTokens; ++h) ahead[h] = -1;
+        for (int h = 0; h < 2; ++h) ahead[h] = -1;
         if (i >= count) return;
         if (i % 32 == 0) look_up(i);
         const int at = __shfl_sync(0xFFFFFFFFu, mine.at, i % 32), row = __shfl_sync(0xFFFFFFFFu, mine.row, i % 32);
@@ -1025,8 +1104,8 @@ attend_fp4_kernel(const Att4Params p) {
             p.packed ? p.list + static_cast<int64_t>(row) * p.list_units * kUnit : p.topk + row * p.topk_stride;
         const int most = p.packed ? p.list_units * kUnit : p.k;
 #pragma unroll
-        for (int h = 0; h < kTokens; ++h) {
-            const int e = at * kUnit + token0 + 32 * h;
+        for (int h = 0; h < 2; ++h) {
+            const int e = at * kUnit + lane + 32 * h;
             if (e < most) ahead[h] = list[e];
         }
     };
@@ -1034,7 +1113,7 @@ attend_fp4_kernel(const Att4Params p) {
         next = later;
         bool bad = false;
 #pragma unroll
-        for (int h = 0; h < kTokens; ++h) {
+        for (int h = 0; h < 2; ++h) {
             pos[h] = ahead[h];
             page[h] = -1;
             if (p.packed) {   // a slot
@@ -1055,31 +1134,30 @@ attend_fp4_kernel(const Att4Params p) {
     auto gather = [&](int i) {           // the unit of pos / page into its stage
         if (i < count) {
             uint8_t* const stage = ring + (i % kStages) * p.stage;
-            uint32_t any = 0;
+            uint32_t there[2];
 #pragma unroll
-            for (int h = 0; h < kTokens; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 const bool on = page[h] >= 0 && page[h] < p.num_pages;
                 if (pos[h] >= 0 && !on && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
                 // (tokens that are not there: any codes, and scales of zero)
                 const int token = pos[h] % kPage, sr = 2 * k.scale_row();
                 const int64_t section = on ? page[h] * p.page_stride + next.kvh * p.head_stride : 0;
-                desk.rows[token0 + 32 * h] = section + (on ? token * k.row_bytes() : 0);
+                desk.rows[lane + 32 * h] = section + (on ? token * k.row_bytes() : 0);
                 const uint8_t* src = p.cache + section + k.s_off() + (on ? token * sr : 0);
-                const uint32_t to = smem_u32(stage + k.s_off() + (token0 + 32 * h) * sr);
+                const uint32_t to = smem_u32(stage + k.s_off() + (lane + 32 * h) * sr);
                 if (p.num_pages > 0) {
                     if (sr == 16) cp_async16s(to, src, on ? 16 : 0);
                     else cp_async8(to, src, on ? 8 : 0);
                 }
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on);
-                any |= mask;
-                if (lane == 0) desk.listed[i % kStages][k.half + h] = mask;
+                there[h] = __ballot_sync(0xFFFFFFFFu, on);
             }
+            if (lane == 0) desk.listed[i % kStages] = static_cast<uint64_t>(there[1]) << 32 | there[0];
             __syncwarp();
             const int part = lane % kLanes;
-            if (any && part * kPiece < k.row_bytes()) {
+            if ((there[0] | there[1]) && part * kPiece < k.row_bytes()) {
 #pragma unroll
-                for (int c = 0; c < kTokens * kLanes; ++c) {
-                    const int token = k.half * 32 + c * (32 / kLanes) + lane / kLanes;
+                for (int c = 0; c < 2 * kLanes; ++c) {
+                    const int token = c * (32 / kLanes) + lane / kLanes;
                     const uint8_t* src = p.cache + desk.rows[token] + part * kPiece;
                     const uint32_t to = smem_u32(stage + token * k.row_bytes() + part * kPiece);
                     if (kPiece == 16) {
@@ -1096,14 +1174,14 @@ attend_fp4_kernel(const Att4Params p) {
     };
 
     if constexpr (kSelected) {
-        for (int i = 0; i < kLead; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             load_positions(i);
             load_pages();
             gather(i);
         }
-        load_positions(kLead);
-    } else if (leads) {
-        for (int i = 0; i < kLead; ++i) copy_page(i);
+        load_positions(kStages);
+    } else {
+        for (int i = 0; i < kStages; ++i) copy_page(i);
     }
     int i = 0;
     bool gave_up = false;
@@ -1117,43 +1195,32 @@ attend_fp4_kernel(const Att4Params p) {
         for (int at = x.at; at < until; ++at, ++i) {
             uint8_t* const stage = ring + (i % kStages) * p.stage;
             if constexpr (kSelected) {
-                load_pages();                     // of unit i + kLead
-                load_positions(i + kLead + 1);
-                cp_async_wait<kLead - 1>();
+                load_pages();                     // of unit i + kStages
+                load_positions(i + kStages + 1);
+                cp_async_wait<kStages - 1>();
                 __syncwarp();
             } else {
-                mbar_wait(&desk.full[i % kStages], (i / kStages) & 1, &desk.abort, p.status);
+                const bool landed = mbar_wait(&desk.full[i % kStages], (i / kStages) & 1, &desk.abort, p.status);
+                if (!__all_sync(0xFFFFFFFFu, landed)) {
+                    gave_up = true;
+                    break;
+                }
             }
-            // (written where the unit's copies were ordered, and the worker has met since)
-            uint64_t listed = 0;
-            bool any;
-            if constexpr (kSelected) {
-                listed = static_cast<uint64_t>(desk.listed[i % kStages][1]) << 32 | desk.listed[i % kStages][0];
-                any = kTeam == 2 || listed != 0;
-            } else {
-                any = desk.listed[i % kStages][0] != 0;
-            }
-            auto issue = [&]() {
-                if constexpr (kSelected) gather(i + kLead);
-                else if (leads) copy_page(i + kLead);
-            };
-            if constexpr (NT == 4) {
-                gave_up = x.nq <= 16 ? k.template unit<2>(stage, at * kUnit, listed, any, issue)
-                                     : k.template unit<4>(stage, at * kUnit, listed, any, issue);
-            } else {
-                gave_up = k.template unit<NT>(stage, at * kUnit, listed, any, issue);
-            }
-            if (gave_up) break;
+            const uint64_t listed = desk.listed[i % kStages];
+            if (listed != 0) k.unit(stage, at * kUnit, listed);
+            __syncwarp();
+            if constexpr (kSelected) gather(i + kStages);
+            else copy_page(i + kStages);
+            __syncwarp();
         }
         // slot 2w + 1: the item's first piece; 2w: a later one (a share has at most one of each)
         if (!gave_up) k.finish(x.at == 0 && until == x.n ? -1 : 2 * static_cast<int64_t>(w) + (x.at == 0 ? 1 : 0));
-        k.meet();
     }
     if constexpr (kSelected) {
         cp_async_wait<0>();
-    } else if (gave_up && leads) {   // the copies in flight land before the CTA ends
+    } else if (gave_up) {   // the copies in flight land before the CTA ends
         const unsigned long long deadline = globaltimer() + kWaitLimitNs;
-        for (int j = i; j < min(i + kLead + 1, count); ++j)
+        for (int j = i; j < min(i + kStages, count); ++j)
             mbar_drain(&desk.full[j % kStages], (j / kStages) & 1, deadline, p.status);
     }
 }
@@ -1264,7 +1331,6 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
     int64_t each = k > 0 ? 1 : max_query_len < rows ? max_query_len : rows;   // rows that share keys
     if (each < 1) each = 1;
     L.cap = static_cast<int>(group * each < 32 ? group * each : 32);
-    L.nt = L.cap <= 8 ? 1 : L.cap <= 16 ? 2 : 4;
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;
@@ -1277,7 +1343,7 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
     L.list = take(k > 0 ? rows * ((k + kUnit - 1) / kUnit * kUnit) * 4 : 0);
     L.pages = take(k > 0 ? 0 : num_requests * 4);
     L.rows = take(k > 0 ? 0 : rows * static_cast<int64_t>(sizeof(Row4)));
-    const int64_t slots = 2 * kMaxCtas4 * kMaxWorkers4;
+    const int64_t slots = 2 * kMaxCtas4 * kMaxWarps4;
     L.po = take(slots * L.cap * dim * 4);
     L.pml = take(slots * L.cap * 8);
     L.total = at;
@@ -1315,12 +1381,12 @@ static int check_attend4(const dsa_kv_cache_fp4* cache, int32_t dtype, const voi
     return DSA_OK;
 }
 
-template <Form kForm, int NT, bool kSelected>
+template <Form kForm, int kRows, bool kSelected>
 static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
-    static_assert(Shape4<kForm, NT, kSelected>::kWorkers <= kMaxWorkers4, "workspaces are sized for it");
-    using S4 = Shape4<kForm, NT, kSelected>;
-    auto* kernel = attend_fp4_kernel<kForm, NT, kSelected>;
-    const int smem = S4::kWorkers * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, NT, kSelected>))) +
+    static_assert(Shape4<kForm, kRows>::kWarps <= kMaxWarps4, "workspaces are sized for it");
+    using S4 = Shape4<kForm, kRows>;
+    auto* kernel = attend_fp4_kernel<kForm, kRows, kSelected>;
+    const int smem = S4::kWarps * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, kRows, kSelected>))) +
                      (kSelected ? (kCtaRequests + 1) * 4 : p.plan_in_cta ? kAxisBytes4 : 0);
     static bool attr_set[64] = {false};
     int dev = 0;
@@ -1330,17 +1396,17 @@ static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
             return DSA_ERR_CUDA;
         attr_set[dev] = true;
     }
-    p.workers = ctas * S4::kWorkers;
+    p.warps = ctas * S4::kWarps;
     return launch_pdl(kernel, dim3(ctas), dim3(S4::kWarps * 32), smem, stream, p) == cudaSuccess ? DSA_OK
                                                                                                : DSA_ERR_CUDA;
 }
 
-template <bool kSelected, int NT>
+template <bool kSelected, int kRows>
 static int launch_form4(Att4Params& p, int ctas, cudaStream_t stream) {
-    return p.dim == 128  ? launch_attend4<kForm128, NT, kSelected>(p, ctas, stream)
-           : p.dim == 64 ? launch_attend4<kForm64, NT, kSelected>(p, ctas, stream)
-           : p.dim > 64  ? launch_attend4<kFormAny128, NT, kSelected>(p, ctas, stream)
-                         : launch_attend4<kFormAny64, NT, kSelected>(p, ctas, stream);
+    return p.dim == 128  ? launch_attend4<kForm128, kRows, kSelected>(p, ctas, stream)
+           : p.dim == 64 ? launch_attend4<kForm64, kRows, kSelected>(p, ctas, stream)
+           : p.dim > 64  ? launch_attend4<kFormAny128, kRows, kSelected>(p, ctas, stream)
+                         : launch_attend4<kFormAny64, kRows, kSelected>(p, ctas, stream);
 }
 
 template <bool kSelected>
@@ -1364,9 +1430,9 @@ static int launch_all4(Att4Params& p, cudaStream_t stream) {
     if (!kSelected && !p.plan_in_cta &&
         launch_pdl(attend_fp4_plan_kernel, dim3(1), dim3(kPlan4Threads), 0, stream, p) != cudaSuccess)
         return DSA_ERR_CUDA;
-    const int rc = p.nt == 1   ? launch_form4<kSelected, 1>(p, ctas, stream)
-                   : p.nt == 2 ? launch_form4<kSelected, 2>(p, ctas, stream)
-                               : launch_form4<kSelected, 4>(p, ctas, stream);
+    const int rc = p.cap <= 8    ? launch_form4<kSelected, 8>(p, ctas, stream)
+                   : p.cap <= 16 ? launch_form4<kSelected, 16>(p, ctas, stream)
+                                 : launch_form4<kSelected, 32>(p, ctas, stream);
     if (rc != DSA_OK) return rc;
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
     // Few rows and heads have many pieces each, which the warps of a CTA share.
@@ -1395,7 +1461,7 @@ static Att4Params params4(const dsa_kv_cache_fp4* c, const Att4Layout& L, uint8_
     p.row_info = reinterpret_cast<Row4*>(ws + L.rows);
     p.po = reinterpret_cast<float*>(ws + L.po);
     p.pml = reinterpret_cast<float2*>(ws + L.pml);
-    p.nt = L.nt, p.cap = L.cap;
+    p.cap = L.cap;
     p.c = scale * c->k_scale * kLog2e4, p.v_scale = c->v_scale;
     return p;
 }
@@ -1437,7 +1503,7 @@ extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype
     p.group = p.heads / p.kv_heads;
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
     p.plan_in_cta = p.R <= kCtaRequests && p.rows <= 4096;
-    if (p.nt == 4) p.light = 2, p.heavy = 3;
+    if (p.cap > 16) p.light = 2, p.heavy = 3;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return launch_all4<false>(p, stream);
 }
