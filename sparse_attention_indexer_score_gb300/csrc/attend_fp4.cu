@@ -31,6 +31,7 @@ constexpr int kMaxCtas4 = 160;          // workspaces are sized for at most this
 constexpr int kMaxWarps4 = 12;        // ... of this many warps
 constexpr int kCtaRequests = 256;       // up to this many requests every CTA lays out the axis itself
 constexpr int kPlan4Threads = 512;
+constexpr int kFewUnits = 8;            // units a warp under which the axis counts units alone
 constexpr int kList4Threads = 256;
 constexpr int kBitmapKeys = 1 << 20;    // positions that a list is put in order by
 constexpr int64_t kPackBytes = 64 << 20;   // listed sections' bytes from which lists are put in order first
@@ -46,11 +47,13 @@ constexpr float kSlack4 = 8.0f;
 struct Row4 {
     int64_t first;          // where the row's request starts on the axis
     int pages, tiles;       // units an item, row tiles a head
-    int place, weight;      // the row's place in its request, what a unit of it takes of the axis
+    int place;              // the row's place in its request
+    int weight, start;      // what a unit, and an item's start, take of the axis
+    int pad;
 };
 
 struct Att4Layout {
-    size_t info;            // int64: the axis' length
+    size_t info;            // int64[2]: the axis' length, whether it counts units alone
     size_t prefix, units, pages;   // the axis in global memory: int64[R + 1] twice, int[R]
     size_t list;            // int[rows][kpad]: slots of the listed keys
     size_t rows;            // Row4[rows]
@@ -64,6 +67,7 @@ struct Axis4 {
     int64_t* prefix;
     int64_t* units;
     int* pages;
+    int light, heavy, start;   // what units of up to 16 query rows, and of more, and an item's start take of the axis
 };
 
 struct Att4Params {
@@ -90,7 +94,6 @@ struct Att4Params {
     int R, rows, heads, group, kv_heads, dim, max_keys, num_pages;
     int k, list_units, list_tiles;   // listed keys: units an item, row tiles a head
     int packed;                      // ... and slots in `list`, in order, instead of positions in `topk`
-    int light, heavy;                // what units of up to 16 query rows, and of more, take of the axis
     int cap, warps;                  // query rows of a tile; warps of the whole grid
     int bf16;                        // type of q and out (else FP16)
     int section, stage;              // bytes of a section, and of a ring stage
@@ -119,9 +122,13 @@ __device__ __forceinline__ int worker_at(int64_t u, int64_t T, int64_t W) {
     return static_cast<int>(((u + 1) * W - 1) / T);
 }
 
-// How many workers share an axis of length T: no more than leave a unit's start to every share.
-__device__ __forceinline__ int64_t sharers(const Att4Params& p, int64_t T) {
-    return max(min(static_cast<int64_t>(p.warps), T / p.heavy), static_cast<int64_t>(T > 0));
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {   // (a 64-bit division takes five times as long)
+    return (a | b) < (int64_t(1) << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// How many warps share an axis of length T on which units are at most `most` apart: every share has one.
+__device__ __forceinline__ int64_t sharers(const Att4Params& p, int64_t T, int most) {
+    return max(min(static_cast<int64_t>(p.warps), div64(T, most)), static_cast<int64_t>(T > 0));
 }
 
 // The last request that starts at or before v.
@@ -142,30 +149,41 @@ __device__ __forceinline__ int pairs_of(const Att4Params& p, int j, int* row0) {
     return (min(max(p.starts[j + 1], *row0), p.rows) - *row0) * p.group;
 }
 
-// Units before the first that starts at or behind place c of the axis.
+// An item of n units takes start + n weight of the axis: its first unit is at its
+// beginning, unit k behind that at start + k weight.
+__device__ __forceinline__ int64_t item_length(int n, int weight, int start) {
+    return n > 0 ? start + static_cast<int64_t>(n) * weight : 0;
+}
+
+// Units before the first that is at or behind place c of the axis.
 __device__ __forceinline__ int64_t unit_at(const Att4Params& p, const Axis4& x, int64_t c) {
     if (c >= x.prefix[p.R]) return x.units[p.R];
     const int j = last_at_most(x.prefix, p.R, c);
     int row0;
-    const int weight = pairs_of(p, j, &row0) <= 16 ? p.light : p.heavy;
-    const int64_t in = c - x.prefix[j] + weight - 1;
-    return x.units[j] + (weight == 1                 ? in
-                         : in < (int64_t(1) << 32) ? static_cast<uint32_t>(in) / static_cast<uint32_t>(weight)
-                                                   : in / weight);
+    const int weight = pairs_of(p, j, &row0) <= 16 ? x.light : x.heavy, n = x.pages[j];
+    const int64_t length = item_length(n, weight, x.start), in = c - x.prefix[j];
+    const int64_t item = div64(in, length), rest = in - item * length;
+    const int64_t k = rest == 0 ? 0 : rest <= x.start ? 1 : max(div64(rest - x.start + weight - 1, weight), int64_t(1));
+    return x.units[j] + item * n + k;
+}
+
+// The axis of few units counts them alone: a share is a unit or a few then.
+__device__ __forceinline__ void count_units(Axis4& x) {
+    x.prefix = x.units;
+    x.light = x.heavy = 1, x.start = 0;
 }
 
 // Lays out the requests (whole block).  `tmp`: 66 int64 of shared scratch.
 // `write`: also what the join reads.
-__device__ void lay_out4(const Att4Params& p, const Axis4& x, int64_t* tmp, bool write) {
+__device__ void lay_out4(const Att4Params& p, Axis4& x, int64_t* tmp, bool write) {
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
     // (on their way while the starts are read)
     for (int r = threadIdx.x * 32; r < p.rows; r += nt * 32)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_ends + r));
     if (write)
-        for (int r = threadIdx.x; r < p.rows; r += nt) p.row_info[r] = Row4{0, 0, 1, 0, 1};
+        for (int r = threadIdx.x; r < p.rows; r += nt) p.row_info[r] = Row4{0, 0, 1, 0, 1, 0, 0};
     int64_t carry = 0, carry_units = 0;
-    if (write) __syncthreads();
     for (int base = 0; base < p.R; base += nt) {
         const int j = base + threadIdx.x;
         int s0 = 0, s1 = 0, most = 0;
@@ -182,8 +200,9 @@ __device__ void lay_out4(const Att4Params& p, const Axis4& x, int64_t* tmp, bool
         }
         const int n = (most + kUnit - 1) / kUnit;
         const int64_t all = static_cast<int64_t>(s1 - s0) * p.group;
-        const int tiles = static_cast<int>((all + p.cap - 1) / p.cap), weight = all <= 16 ? p.light : p.heavy;
-        const int64_t units = static_cast<int64_t>(n) * tiles * p.kv_heads, cost = units * weight;
+        const int tiles = static_cast<int>((all + p.cap - 1) / p.cap), weight = all <= 16 ? x.light : x.heavy;
+        const int64_t items = static_cast<int64_t>(tiles) * p.kv_heads;
+        const int64_t units = n * items, cost = item_length(n, weight, x.start) * items;
         int64_t v = cost, y = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -209,17 +228,27 @@ __device__ void lay_out4(const Att4Params& p, const Axis4& x, int64_t* tmp, bool
             x.prefix[j] = before;
             x.units[j] = carry_units + y - units + (warp > 0 ? tmp[33 + warp - 1] : 0);
             x.pages[j] = n;
-            if (write)
-                for (int r = s0; r < s1; ++r) p.row_info[r] = Row4{before, n, max(tiles, 1), r - s0, weight};
         }
         carry += tmp[32];
         carry_units += tmp[65];
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        x.prefix[p.R] = carry;
-        x.units[p.R] = carry_units;
-        if (write) p.info[0] = carry;
+    if (threadIdx.x == 0) x.prefix[p.R] = carry, x.units[p.R] = carry_units;
+    const bool few = carry_units < kFewUnits * static_cast<int64_t>(p.warps);
+    __syncthreads();
+    if (few) count_units(x);
+    if (write) {
+        if (threadIdx.x == 0) p.info[0] = x.prefix[p.R], p.info[1] = few;
+        for (int j = threadIdx.x; j < p.R; j += nt) {
+            int row0;
+            const int all = pairs_of(p, j, &row0);
+            const Row4 info = {x.prefix[j], x.pages[j], max((all + p.cap - 1) / p.cap, 1), 0,
+                               all <= 16 ? x.light : x.heavy, x.start, 0};
+            for (int r = 0; r < all / p.group; ++r) {
+                p.row_info[row0 + r] = info;
+                p.row_info[row0 + r].place = r;
+            }
+        }
     }
     if (write && bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
     __syncthreads();
@@ -229,7 +258,8 @@ __global__ void __launch_bounds__(kPlan4Threads) attend_fp4_plan_kernel(const At
     pdl_wait();
     pdl_launch_dependents();
     __shared__ int64_t tmp[66];
-    lay_out4(p, p.axis, tmp, true);
+    Axis4 axis = p.axis;
+    lay_out4(p, axis, tmp, true);
 }
 
 // Listed keys as slots (page * 64 + token), in the order of their positions, so that
@@ -329,7 +359,7 @@ constexpr bool wide(Form f) { return f == kForm128 || f == kFormAny128; }
 // Tiles of 8, 16 or 32 query rows; warps of a CTA and stages of a warp's ring.
 template <Form kForm, int kRows>
 struct Shape4 {
-    static constexpr int kWarps = kRows == 8 ? 12 : kRows == 16 ? (wide(kForm) ? 10 : 12) : 8;
+    static constexpr int kWarps = kRows == 8 ? 12 : kRows == 16 ? (wide(kForm) ? 8 : 12) : 8;
     static constexpr int kStages = 2;
 };
 
@@ -754,7 +784,7 @@ struct Many4 : Base4<kForm, kRows, kSelected> {
     static constexpr int kBlocks = B::kBlocks, kSteps = B::kSteps;
     static constexpr int kTiles = kRows / 16;
     static constexpr int kOT = 2 * kBlocks;                  // tiles of 8 value columns: column n * kOT + i is n of tile i
-    static constexpr int kMT = kRows == 16 ? 4 : 2;          // tiles of 16 keys whose scores are in registers at once
+    static constexpr int kMT = kRows == 16 ? 4 : 1;          // tiles of 16 keys whose scores are in registers at once
 
     float o[kOT][kTiles][4];
     // query rows 16r + g and 16r + g + 8: reference, sum, factor, where the reference is raised, bound
@@ -1035,6 +1065,8 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
         axis.units = axis.prefix + kCtaRequests + 1;
         axis.pages = reinterpret_cast<int*>(axis.units + kCtaRequests + 1 + 66);
         lay_out4(p, axis, axis.units + kCtaRequests + 1, blockIdx.x == 0);
+    } else if (!kSelected && p.info[1]) {
+        count_units(axis);
     }
     if (kSelected && !p.packed) {
         bool bad = false;
@@ -1051,7 +1083,7 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
     __syncwarp();
     const int64_t total = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles * p.list_units
                                     : axis.prefix[p.R];
-    const int64_t W = sharers(p, total);
+    const int64_t W = sharers(p, total, kSelected ? 1 : axis.heavy + axis.start);
     const int w = warp * gridDim.x + blockIdx.x;   // (neighbouring shares on different SMs)
     if (w >= W) return;
     int64_t u0 = share4(w, total, W), u1 = share4(w + 1, total, W);
@@ -1243,7 +1275,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
     if (kSelected) {
         const int64_t per_row = static_cast<int64_t>(p.kv_heads) * p.list_tiles * p.list_units;
         total = p.rows * per_row;
-        ri = Row4{row * per_row, p.list_units, p.list_tiles, 0, 1};
+        ri = Row4{row * per_row, p.list_units, p.list_tiles, 0, 1, 0, 0};
     } else {
         ri = p.row_info[row];
         total = p.info[0];
@@ -1254,10 +1286,10 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
         const int n = ri.place * p.group + in_group;
         const int tile = n / p.cap;
         cap_row = n - tile * p.cap;
-        const int64_t W = sharers(p, total);
-        const int64_t a =
-            min(ri.first + (static_cast<int64_t>(kvh) * ri.tiles + tile) * ri.pages * ri.weight, total - 1);
-        const int64_t last = min(a + static_cast<int64_t>(ri.pages - 1) * ri.weight, total - 1);
+        const int64_t W = sharers(p, total, kSelected || p.info[1] ? 1 : p.axis.heavy + p.axis.start);
+        const int64_t length = item_length(ri.pages, ri.weight, ri.start);
+        const int64_t a = min(ri.first + (static_cast<int64_t>(kvh) * ri.tiles + tile) * length, total - 1);
+        const int64_t last = min(ri.pages > 1 ? a + length - ri.weight : a, total - 1);
         const int wa = worker_at(a, total, W), wb = worker_at(last, total, W);
         pieces = wb - wa + 1;
         if (pieces == 1) return;   // written by the attention kernel
@@ -1337,7 +1369,7 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
         at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
         return here;
     };
-    L.info = take(8);
+    L.info = take(16);
     L.prefix = take(k > 0 ? 0 : (num_requests + 1) * 8);
     L.units = take(k > 0 ? 0 : (num_requests + 1) * 8);
     L.list = take(k > 0 ? rows * ((k + kUnit - 1) / kUnit * kUnit) * 4 : 0);
@@ -1396,7 +1428,6 @@ static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
             return DSA_ERR_CUDA;
         attr_set[dev] = true;
     }
-    p.warps = ctas * S4::kWarps;
     return launch_pdl(kernel, dim3(ctas), dim3(S4::kWarps * 32), smem, stream, p) == cudaSuccess ? DSA_OK
                                                                                                : DSA_ERR_CUDA;
 }
@@ -1413,6 +1444,10 @@ template <bool kSelected>
 static int launch_all4(Att4Params& p, cudaStream_t stream) {
     int ctas = device_sm_count();
     if (ctas > kMaxCtas4) ctas = kMaxCtas4;
+    const bool wide_head = p.dim > 64;
+    p.warps = ctas * (p.cap <= 8    ? Shape4<kForm128, 8>::kWarps
+                      : p.cap <= 16 ? (wide_head ? Shape4<kForm128, 16>::kWarps : Shape4<kForm64, 16>::kWarps)
+                                    : Shape4<kForm128, 32>::kWarps);
     if (kSelected && p.packed) {
         const int bitmap = p.max_keys <= kBitmapKeys ? (p.max_keys + 31) / 32 * 4 : 0;
         static bool attr_set[64] = {false};
@@ -1455,9 +1490,8 @@ static Att4Params params4(const dsa_kv_cache_fp4* c, const Att4Layout& L, uint8_
     p.stage = (p.section + 127) / 128 * 128;
     p.info = reinterpret_cast<int64_t*>(ws + L.info);
     p.axis = Axis4{reinterpret_cast<int64_t*>(ws + L.prefix), reinterpret_cast<int64_t*>(ws + L.units),
-                   reinterpret_cast<int*>(ws + L.pages)};
+                   reinterpret_cast<int*>(ws + L.pages), 1, 1, 0};
     p.list = reinterpret_cast<int*>(ws + L.list);
-    p.light = p.heavy = 1;
     p.row_info = reinterpret_cast<Row4*>(ws + L.rows);
     p.po = reinterpret_cast<float*>(ws + L.po);
     p.pml = reinterpret_cast<float2*>(ws + L.pml);
@@ -1503,7 +1537,7 @@ extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype
     p.group = p.heads / p.kv_heads;
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
     p.plan_in_cta = p.R <= kCtaRequests && p.rows <= 4096;
-    if (p.cap > 16) p.light = 2, p.heavy = 3;
+    p.axis.light = 5, p.axis.heavy = p.cap > 16 ? 7 : 5, p.axis.start = 4;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return launch_all4<false>(p, stream);
 }
