@@ -18,6 +18,7 @@
 // Neither product cares in what order the summed index is taken, which leaves the
 // layouts free: a thread's bytes of a key are those of its own operand rows.
 // Codes times scales are exact in FP16 (6 bits).
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "elem16.cuh"
@@ -492,6 +493,50 @@ struct Base4 {
         *c = fminf(fmaxf(p.c * down, 1e-37f), 3e38f);
     }
 
+    // The rows of 64 listed tokens (two a lane: their place in page[h], that a position chose, -1 for none) into a
+    // stage, asynchronously.
+    __device__ __forceinline__ void gather(uint8_t* stage, int index, const int (&pos)[2], const int (&page)[2],
+                                           int kvh) const {
+        // rows of codes are cut into pieces of 16 bytes (8 where rows are not multiples of 16)
+        constexpr int kPiece = kFull ? 16 : 8;
+        constexpr int kLanes = kForm == kForm128 ? 4 : kForm == kForm64 ? 2 : wide(kForm) ? 8 : 4;   // of a row
+        uint32_t there[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool on = page[h] >= 0 && page[h] < p.num_pages;
+            if (pos[h] >= 0 && !on && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
+            // (tokens that are not there: any codes, and scales of zero)
+            const int token = pos[h] % kPage, sr = 2 * scale_row();
+            const int64_t section = on ? page[h] * p.page_stride + kvh * p.head_stride : 0;
+            desk.rows[lane + 32 * h] = section + (on ? token * row_bytes() : 0);
+            const uint8_t* src = p.cache + section + s_off() + (on ? token * sr : 0);
+            const uint32_t to = smem_u32(stage + s_off() + (lane + 32 * h) * sr);
+            if (p.num_pages > 0) {
+                if (sr == 16) cp_async16s(to, src, on ? 16 : 0);
+                else cp_async8(to, src, on ? 8 : 0);
+            }
+            there[h] = __ballot_sync(0xFFFFFFFFu, on);
+        }
+        if (lane == 0) desk.listed[index] = static_cast<uint64_t>(there[1]) << 32 | there[0];
+        __syncwarp();
+        const int part = lane % kLanes;
+        if ((there[0] | there[1]) && part * kPiece < row_bytes()) {
+#pragma unroll
+            for (int c = 0; c < 2 * kLanes; ++c) {
+                const int token = c * (32 / kLanes) + lane / kLanes;
+                const uint8_t* src = p.cache + desk.rows[token] + part * kPiece;
+                const uint32_t to = smem_u32(stage + token * row_bytes() + part * kPiece);
+                if (kPiece == 16) {
+                    cp_async16s(to, src, 16);
+                    cp_async16s(to + v_off(), src + v_off(), 16);
+                } else {
+                    cp_async8(to, src, 8);
+                    cp_async8(to + v_off(), src + v_off(), 8);
+                }
+            }
+        }
+    }
+
     // The (row, head) pair n of the item's tile.
     __device__ __forceinline__ void pair(int n, int* row, int* head) const {
         const int at = item.first + n;
@@ -593,11 +638,11 @@ struct Base4 {
         fence_proxy_async_smem();   // (the next copy into the stage is the asynchronous proxy's)
     }
 
-    // Columns col .. col + n - 1 (n of 16 or 8) of pair n's output, or of a piece's.
+    // kCols columns from col on of pair n's output, or of a piece's (po).
     template <int kCols>
-    __device__ __forceinline__ void write(int64_t slot, int n, int col, const float (&o)[kCols], float inv) const {
-        if (slot >= 0) {
-            float* dst = p.po + (slot * p.cap + n) * p.dim + col;
+    __device__ __forceinline__ void write(float* po, int n, int col, const float (&o)[kCols], float inv) const {
+        if (po) {
+            float* dst = po + n * p.dim + col;
 #pragma unroll
             for (int i = 0; i < kCols; i += 4)
                 *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -613,9 +658,9 @@ struct Base4 {
         }
     }
     // Pair n's reference (times c) and sum of weights.
-    __device__ __forceinline__ void write_sum(int64_t slot, int n, float top, float sum) const {
-        if (slot >= 0) {
-            p.pml[slot * p.cap + n] = make_float2(sum == 0.0f ? -INFINITY : top, sum);
+    __device__ __forceinline__ void write_sum(float2* pml, int n, float top, float sum) const {
+        if (pml) {
+            pml[n] = make_float2(sum == 0.0f ? -INFINITY : top, sum);
         } else if (p.lse) {
             int row, head;
             pair(n, &row, &head);
@@ -756,8 +801,8 @@ struct Few4 : Base4<kForm, 8, kSelected> {
             });
     }
 
-    // The item's result, or the partial one of a piece (slot >= 0).
-    __device__ __forceinline__ void finish(int64_t slot) {
+    // The item's result, or a piece's: sums [row][column] to po, references and sums of weights to pml.
+    __device__ __forceinline__ void finish(float* po, float2* pml) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float sum = l[e];
@@ -769,8 +814,8 @@ struct Few4 : Base4<kForm, 8, kSelected> {
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) y[2 * i] = o[i][e], y[2 * i + 1] = o[i][e + 2];
             if (B::kFull || (kBlocks == 8 ? g : g >> 1) < nblk())
-                B::write(slot, n, g * 2 * kBlocks, y, sum == 0.0f ? 0.0f : p.v_scale / sum);
-            if (g == 0) B::write_sum(slot, n, ref[e] * c[e], sum);
+                B::write(po, n, g * 2 * kBlocks, y, sum == 0.0f ? 0.0f : p.v_scale / sum);
+            if (g == 0) B::write_sum(pml, n, ref[e] * c[e], sum);
         }
     }
 };
@@ -953,7 +998,7 @@ struct Many4 : Base4<kForm, kRows, kSelected> {
         else unit<1>(stage, key_base, listed);
     }
 
-    __device__ __forceinline__ void finish(int64_t slot) {
+    __device__ __forceinline__ void finish(float* po, float2* pml) {
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
 #pragma unroll
@@ -969,9 +1014,9 @@ struct Many4 : Base4<kForm, kRows, kSelected> {
                     float y[kOT];
 #pragma unroll
                     for (int i = 0; i < kOT; ++i) y[i] = o[i][r][2 * h + e];
-                    if (B::kFull || (kBlocks == 8 ? 2 * t + e : t) < nblk()) B::write(slot, n, (2 * t + e) * kOT, y, inv);
+                    if (B::kFull || (kBlocks == 8 ? 2 * t + e : t) < nblk()) B::write(po, n, (2 * t + e) * kOT, y, inv);
                 }
-                if (t == 0) B::write_sum(slot, n, ref[r][h] * c[r][h], sum);
+                if (t == 0) B::write_sum(pml, n, ref[r][h] * c[r][h], sum);
             }
     }
 };
@@ -1160,48 +1205,8 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
         }
         if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
     };
-    // Rows of codes are cut into pieces of 16 bytes (8 where rows are not multiples of 16).
-    constexpr int kPiece = kForm == kForm128 || kForm == kForm64 ? 16 : 8;
-    constexpr int kLanes = kForm == kForm128 ? 4 : kForm == kForm64 ? 2 : wide(kForm) ? 8 : 4;   // of a row
     auto gather = [&](int i) {           // the unit of pos / page into its stage
-        if (i < count) {
-            uint8_t* const stage = ring + (i % kStages) * p.stage;
-            uint32_t there[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool on = page[h] >= 0 && page[h] < p.num_pages;
-                if (pos[h] >= 0 && !on && p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
-                // (tokens that are not there: any codes, and scales of zero)
-                const int token = pos[h] % kPage, sr = 2 * k.scale_row();
-                const int64_t section = on ? page[h] * p.page_stride + next.kvh * p.head_stride : 0;
-                desk.rows[lane + 32 * h] = section + (on ? token * k.row_bytes() : 0);
-                const uint8_t* src = p.cache + section + k.s_off() + (on ? token * sr : 0);
-                const uint32_t to = smem_u32(stage + k.s_off() + (lane + 32 * h) * sr);
-                if (p.num_pages > 0) {
-                    if (sr == 16) cp_async16s(to, src, on ? 16 : 0);
-                    else cp_async8(to, src, on ? 8 : 0);
-                }
-                there[h] = __ballot_sync(0xFFFFFFFFu, on);
-            }
-            if (lane == 0) desk.listed[i % kStages] = static_cast<uint64_t>(there[1]) << 32 | there[0];
-            __syncwarp();
-            const int part = lane % kLanes;
-            if ((there[0] | there[1]) && part * kPiece < k.row_bytes()) {
-#pragma unroll
-                for (int c = 0; c < 2 * kLanes; ++c) {
-                    const int token = c * (32 / kLanes) + lane / kLanes;
-                    const uint8_t* src = p.cache + desk.rows[token] + part * kPiece;
-                    const uint32_t to = smem_u32(stage + token * k.row_bytes() + part * kPiece);
-                    if (kPiece == 16) {
-                        cp_async16s(to, src, 16);
-                        cp_async16s(to + k.v_off(), src + k.v_off(), 16);
-                    } else {
-                        cp_async8(to, src, 8);
-                        cp_async8(to + k.v_off(), src + k.v_off(), 8);
-                    }
-                }
-            }
-        }
+        if (i < count) k.gather(ring + (i % kStages) * p.stage, i % kStages, pos, page, next.kvh);
         cp_async_commit();
     };
 
@@ -1246,7 +1251,9 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
             __syncwarp();
         }
         // slot 2w + 1: the item's first piece; 2w: a later one (a share has at most one of each)
-        if (!gave_up) k.finish(x.at == 0 && until == x.n ? -1 : 2 * static_cast<int64_t>(w) + (x.at == 0 ? 1 : 0));
+        const int64_t slot = 2 * static_cast<int64_t>(w) + (x.at == 0 ? 1 : 0);
+        const bool whole = x.at == 0 && until == x.n;
+        if (!gave_up) k.finish(whole ? nullptr : p.po + slot * p.cap * p.dim, whole ? nullptr : p.pml + slot * p.cap);
     }
     if constexpr (kSelected) {
         cp_async_wait<0>();
@@ -1254,6 +1261,235 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
         const unsigned long long deadline = globaltimer() + kWaitLimitNs;
         for (int j = i; j < min(i + kStages, count); ++j)
             mbar_drain(&desk.full[j % kStages], (j / kStages) & 1, deadline, p.status);
+    }
+}
+
+// Few items with few units: eight CTAs, a cluster, have an item, and its units go round
+// their warps.  What the warps have is joined through the cluster's shared memory, so
+// one launch does it all, and the first page is on its way before the item's length
+// is known.
+constexpr int kCluster = 8;
+constexpr int kClusterUnits = 4;   // units of a warp at most
+
+template <Form kForm, int kRows, bool kSelected>
+__global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1)
+attend_fp4_cluster_kernel(const Att4Params p) {
+    using S4 = Shape4<kForm, kRows>;
+    using W4 = Worker4<kForm, kRows, kSelected>;
+    using Desk = Desk4<kForm, kRows, kSelected>;
+    constexpr int kStages = S4::kStages, kWarps = S4::kWarps, kSharers = kWarps * kCluster;
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 ml[kWarps][kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = cluster.block_rank(), item = blockIdx.x / kCluster;
+    pdl_wait();
+    pdl_launch_dependents();
+    uint8_t* const ring = smem + warp * kStages * p.stage;
+    Desk& desk = reinterpret_cast<Desk*>(smem + kWarps * kStages * p.stage)[warp];
+    W4 k(p, desk);
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&desk.full[i], 1);
+        mbar_fence_init();
+        desk.abort = 0;
+    }
+    __syncwarp();
+    const int sharer = warp * kCluster + rank;   // (an item's first units are on different SMs)
+
+    // The item, and its units: those of this warp are sharer, sharer + kSharers, ...
+    int row0 = 0, all = 0, kvh, units = 0, req = -1, bound = 0;
+    bool bad = false;
+    int first_page = -1, first_pos[2] = {-1, -1};   // the first unit's page, its positions
+    if (kSelected) {
+        const int per_row = p.kv_heads * p.list_tiles;
+        row0 = item / per_row;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = sharer * kUnit + lane + 32 * h;
+            if (e < p.k) first_pos[h] = p.topk[row0 * p.topk_stride + e];
+        }
+        kvh = (item - row0 * per_row) / p.list_tiles;
+        units = p.list_units;
+        const int j = p.R > 0 ? last_at_most(p.starts, p.R, row0) : -1;
+        if (j >= 0 && p.starts[j] <= row0 && row0 < p.starts[j + 1]) req = j;
+        const int e = p.row_ends[row0];
+        bound = min(max(e, 0), p.max_keys);
+        bad = req >= 0 && e != bound;
+        if (req < 0) units = 0;
+    } else {
+        req = item / p.kv_heads;
+        kvh = item - req * p.kv_heads;
+        if (lane == 0 && sharer * kPage < p.max_keys) {
+            // (a copy that the item turns out not to need is waited for like any other)
+            const int page = p.bt[req * p.bt_stride + sharer];
+            first_page = page >= 0 && page < p.num_pages ? page : -1;
+            if (first_page >= 0) {
+                mbar_arrive_expect_tx(&desk.full[0], p.section);
+                bulk_load(ring, p.cache + first_page * p.page_stride + kvh * p.head_stride, p.section, &desk.full[0]);
+            }
+        }
+        all = pairs_of(p, req, &row0);
+        int most = 0;
+        for (int r = row0 + lane; r < row0 + all / p.group; r += 32) {
+            const int given = p.row_ends[r], e = min(max(given, 0), p.max_keys);
+            bad |= e != given;
+            most = max(most, e);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        units = (most + kUnit - 1) / kUnit;
+    }
+    // what the geometry says wrong, and rows outside every request
+    if (blockIdx.x == 0) {
+        for (int j = threadIdx.x; j <= p.R; j += blockDim.x) {
+            const int a = p.starts[j];
+            bad |= a < 0 || (j > 0 && a < p.starts[j - 1]) || a > p.rows;
+        }
+        if (!kSelected)
+            for (int r = warp; r < p.rows; r += kWarps) {
+                bool mine = false;
+                for (int j = lane; j < p.R; j += 32) mine |= p.starts[j] <= r && r < p.starts[j + 1];
+                if (__any_sync(0xFFFFFFFFu, mine)) continue;
+                for (int i = lane; i < p.heads * (p.dim / 8); i += 32) {
+                    const int head = i / (p.dim / 8), col = i - head * (p.dim / 8);
+                    *reinterpret_cast<uint4*>(p.out + r * p.orow + head * p.ohead + col * 8) = make_uint4(0, 0, 0, 0);
+                    if (col == 0 && p.lse) p.lse[static_cast<int64_t>(r) * p.heads + head] = -INFINITY;
+                }
+            }
+    }
+    if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+
+    const int count = sharer < units ? (units - sharer + kSharers - 1) / kSharers : 0;
+    const int tiles = kSelected ? 1 : (all + p.cap - 1) / p.cap;
+    int pos[2], page[2];
+    auto copy = [&](int tile, int i) {   // unit i of the warp into its stage
+        uint8_t* const stage = ring + (i % kStages) * p.stage;
+        if constexpr (kSelected) {
+            if (i < count) {
+                const int32_t* list = p.topk + row0 * p.topk_stride;
+                const int from = (sharer + i * kSharers) * kUnit + lane;
+                bool past = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pos[h] = i == 0 ? first_pos[h] : from + 32 * h < p.k ? list[from + 32 * h] : -1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (pos[h] >= bound) past |= pos[h] >= 0, pos[h] = -1;
+                    page[h] = pos[h] >= 0 ? p.bt[req * p.bt_stride + pos[h] / kPage] : -1;
+                }
+                if (past && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
+                k.gather(stage, i % kStages, pos, page, kvh);
+            }
+            cp_async_commit();
+        } else if (lane == 0 && i < count && !(tile == 0 && i == 0 && first_page >= 0)) {
+            const int at = p.bt[req * p.bt_stride + sharer + i * kSharers];
+            const bool ok = at >= 0 && at < p.num_pages;
+            desk.listed[i % kStages] = ok;
+            if (ok) {
+                mbar_arrive_expect_tx(&desk.full[i % kStages], p.section);
+                bulk_load(stage, p.cache + at * p.page_stride + kvh * p.head_stride, p.section,
+                          &desk.full[i % kStages]);
+            } else {
+                mbar_arrive(&desk.full[i % kStages]);
+                if (p.status) atomicOr(p.status, DSA_STATUS_BAD_PAGE);
+            }
+        } else if (lane == 0 && tile == 0 && i == 0 && first_page >= 0) {
+            desk.listed[0] = 1;
+        }
+    };
+    // Parities of the stages' barriers: a copy that was not needed took one of stage 0 too.
+    int turns[kStages] = {};
+    for (int tile = 0; tile < max(tiles, 1); ++tile) {
+        Item4 x;
+        if (kSelected) {
+            const int first = (item % p.list_tiles) * p.cap;
+            x = Item4{row0, first, min(p.cap, p.group - first), kvh, 0, 0};
+        } else {
+            x = Item4{row0, tile * p.cap, min(p.cap, all - tile * p.cap), kvh, 0, 0};
+        }
+        for (int i = 0; i < kStages; ++i) copy(tile, i);
+        __syncwarp();
+        if (x.nq > 0 && count > 0) k.begin(x);
+        for (int i = 0; i < count && x.nq > 0; ++i) {
+            uint8_t* const stage = ring + (i % kStages) * p.stage;
+            if constexpr (kSelected) {
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+            } else {
+                int parity = 0;
+#pragma unroll
+                for (int s = 0; s < kStages; ++s)
+                    if (i % kStages == s) parity = turns[s]++ & 1;
+                const bool ok = mbar_wait(&desk.full[i % kStages], parity, &desk.abort, p.status);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {   // the copies in flight land before their place is used again
+                    const unsigned long long deadline = globaltimer() + kWaitLimitNs;
+                    for (int j = i; j < min(i + kStages, count); ++j) {
+#pragma unroll
+                        for (int s = 0; s < kStages; ++s)
+                            if (j % kStages == s) parity = (turns[s] - (j == i)) & 1;
+                        mbar_drain(&desk.full[j % kStages], parity, deadline, p.status);
+                    }
+                    break;
+                }
+            }
+            const uint64_t listed = desk.listed[i % kStages];
+            if (listed != 0) k.unit(stage, (sharer + i * kSharers) * kUnit, listed);
+            __syncwarp();
+            copy(tile, i + kStages);
+            __syncwarp();
+        }
+        if (kSelected) cp_async_wait<0>();
+        if (!kSelected && tile == 0 && count == 0 && lane == 0 && first_page >= 0)   // the copy that was not needed
+            mbar_drain(&desk.full[0], 0, globaltimer() + kWaitLimitNs, p.status);
+        __syncwarp();
+        // The warp's results take the place of its ring.
+        if (x.nq > 0 && count > 0) k.finish(reinterpret_cast<float*>(ring), ml[warp]);
+        cluster.sync();
+        const int pieces = min(units, kSharers);
+        for (int i = rank * blockDim.x + threadIdx.x; i < x.nq * (p.dim / 4); i += kCluster * blockDim.x) {
+            const int n = i / (p.dim / 4), col = (i - n * (p.dim / 4)) * 4;
+            float top = -INFINITY, l = 0.0f;
+            float4 o = {0, 0, 0, 0};
+            constexpr int kAhead = 8;
+            for (int base = 0; base < pieces; base += kAhead) {
+                float2 e[kAhead];
+                float4 v[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int w = base + j;   // sharer w: warp w / kCluster of CTA w % kCluster
+                    e[j] = make_float2(-INFINITY, 0.0f);
+                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (w < pieces) {
+                        const float* src = reinterpret_cast<const float*>(smem + (w / kCluster) * kStages * p.stage);
+                        e[j] = *cluster.map_shared_rank(&ml[w / kCluster][n], w % kCluster);
+                        v[j] = *reinterpret_cast<const float4*>(
+                            cluster.map_shared_rank(src + n * p.dim + col, w % kCluster));
+                    }
+                }
+                float m = top;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) m = fmaxf(m, e[j].x);
+                const float keep = top == -INFINITY ? 0.0f : ex2_4(top - m);
+                top = m;
+                l *= keep;
+                o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const float f = e[j].x == -INFINITY ? 0.0f : ex2_4(e[j].x - m);
+                    l += e[j].y * f;
+                    o.x += v[j].x * f, o.y += v[j].y * f, o.z += v[j].z * f, o.w += v[j].w * f;
+                }
+            }
+            const float inv = l == 0.0f ? 0.0f : p.v_scale / l;
+            const int row = x.row0 + (x.first + n) / p.group, head = kvh * p.group + (x.first + n) % p.group;
+            *reinterpret_cast<uint2*>(p.out + row * p.orow + head * p.ohead + col) =
+                make_uint2(pack2(p, o.x * inv, o.y * inv), pack2(p, o.z * inv, o.w * inv));
+            if (col == 0 && p.lse)
+                p.lse[static_cast<int64_t>(row) * p.heads + head] =
+                    l == 0.0f ? -INFINITY : (top + log2f(l) - kLift) * kLn2_4;
+        }
+        cluster.sync();   // (what the others read of this CTA stays until they are done)
     }
 }
 
@@ -1432,6 +1668,43 @@ static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
                                                                                                : DSA_ERR_CUDA;
 }
 
+template <Form kForm, int kRows, bool kSelected>
+static int launch_cluster4(Att4Params& p, int items, cudaStream_t stream) {
+    using S4 = Shape4<kForm, kRows>;
+    auto* kernel = attend_fp4_cluster_kernel<kForm, kRows, kSelected>;
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost4 - 4096) != cudaSuccess)
+            return DSA_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(items * kCluster);
+    cfg.blockDim = dim3(S4::kWarps * 32);
+    cfg.dynamicSmemBytes =
+        S4::kWarps * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, kRows, kSelected>)));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+template <bool kSelected, int kRows>
+static int launch_cluster_form4(Att4Params& p, int items, cudaStream_t stream) {
+    return p.dim == 128  ? launch_cluster4<kForm128, kRows, kSelected>(p, items, stream)
+           : p.dim == 64 ? launch_cluster4<kForm64, kRows, kSelected>(p, items, stream)
+           : p.dim > 64  ? launch_cluster4<kFormAny128, kRows, kSelected>(p, items, stream)
+                         : launch_cluster4<kFormAny64, kRows, kSelected>(p, items, stream);
+}
+
 template <bool kSelected, int kRows>
 static int launch_form4(Att4Params& p, int ctas, cudaStream_t stream) {
     return p.dim == 128  ? launch_attend4<kForm128, kRows, kSelected>(p, ctas, stream)
@@ -1444,6 +1717,17 @@ template <bool kSelected>
 static int launch_all4(Att4Params& p, cudaStream_t stream) {
     int ctas = device_sm_count();
     if (ctas > kMaxCtas4) ctas = kMaxCtas4;
+    // A cluster an item, where there are few and their units few.
+    const int64_t items_all = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles
+                                        : static_cast<int64_t>(p.R) * p.kv_heads;
+    const int most_units = kSelected ? p.list_units : p.max_keys / kUnit;
+    if (items_all > 0 && items_all * kCluster <= ctas && most_units <= 8 * kCluster * kClusterUnits &&
+        (kSelected || static_cast<int64_t>(p.rows) * p.group <= 2 * p.cap)) {
+        const int n = static_cast<int>(items_all);
+        return p.cap <= 8    ? launch_cluster_form4<kSelected, 8>(p, n, stream)
+               : p.cap <= 16 ? launch_cluster_form4<kSelected, 16>(p, n, stream)
+                             : launch_cluster_form4<kSelected, 32>(p, n, stream);
+    }
     const bool wide_head = p.dim > 64;
     p.warps = ctas * (p.cap <= 8    ? Shape4<kForm128, 8>::kWarps
                       : p.cap <= 16 ? (wide_head ? Shape4<kForm128, 16>::kWarps : Shape4<kForm64, 16>::kWarps)

@@ -283,3 +283,61 @@ def test_captured_and_on_another_stream(cuda_lib):
     torch.cuda.synchronize()
     c.check(got[:2])
     c.check(got[2:], topk)
+
+
+@pytest.mark.parametrize("lens,qlens,hq,hkv,dim", [
+    ([1000], [1], 32, 8, 128), ([64 * 90], [4], 16, 4, 128), ([64 * 100 + 1], [2], 8, 2, 64), ([0, 5, 130], [1, 2, 1], 8, 2, 96),
+    ([20000], [1], 4, 1, 128), ([24576], [2], 30, 1, 80), ([700, 0], [3, 0], 24, 2, 128), ([300, 300], [1, 1], 128, 2, 48)])
+def test_few_items(cuda_lib, lens, qlens, hq, hkv, dim):
+    """Batches small enough for a cluster an item (and, by a hint that is too small, their row tiles in turn)."""
+    c = Case(lens, qlens, hq=hq, hkv=hkv, dim=dim, pad_rows=2)
+    for hint in (c.qlen, 1):
+        c.check(c.paged(cuda_lib, max_query_len=hint))
+    for k in (3, 2048):
+        topk = choose(c, k, seed=k)
+        c.check(c.selected(cuda_lib, topk), topk)
+
+
+def test_few_items_and_many_agree(cuda_lib):
+    """The same request alone and among others: the parts of its keys are joined in another order."""
+    one = Case([1500], [2], hq=8, hkv=2, dim=128, seed=3)
+    alone = one.paged(cuda_lib)
+    one.check(alone)
+    table = one.block_table.repeat(40, 1)
+    q = one.q.repeat(40, 1, 1)
+    starts = torch.arange(0, 82, 2, dtype=torch.int32, device="cuda")
+    out, lse = cuda_lib.attend_paged_fp4(q, one.cache, table, starts, one.row_ends.repeat(40), 2, want_lse=True)
+    for j in (0, 17, 39):
+        one.check((out[2 * j: 2 * j + 2], lse[2 * j: 2 * j + 2]))
+
+
+def test_lists_in_order_of_their_positions(cuda_lib):
+    """A batch large enough that lists are put in order first: random orders, holes, positions listed twice, past the
+    bound, and pages outside the pool."""
+    lens = [200 + 37 * j for j in range(130)]
+    c = Case(lens, [1] * 130, hq=8, hkv=8, dim=128)
+    topk = choose(c, 700)
+    assert 130 * 8 * 11 * F.section_bytes(128) >= 64 << 20
+    got = c.selected(cuda_lib, topk)
+    c.check(got, topk, rows=range(0, 130, 9))
+    shuffled = topk.clone()
+    for r in (3, 77):
+        shuffled[r] = topk[r][torch.randperm(700, device="cuda")]
+    again = c.selected(cuda_lib, shuffled)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    twice = topk.clone()
+    twice[5, :60], twice[5, 60:] = torch.arange(60), -1
+    twice[5, 60:120] = torch.arange(60)
+    twice[6, 5] = 10 ** 6
+    out, lse = c.selected(cuda_lib, twice, status=status)
+    assert int(status) == 4
+    c.check((out, lse - np.log(2.0)), topk=twice[:, :60].contiguous(), rows=[5])
+    assert torch.equal(out[7:], got[0][7:])
+    c.block_table[9, 1] = 10 ** 7
+    status.zero_()
+    out, lse = c.selected(cuda_lib, topk, status=status)
+    assert int(status) == 2 and torch.equal(out[10:], got[0][10:])
+    keep = topk.clone()                                   # (the same keys, in units of their own)
+    keep[9] = torch.where((topk[9] >= 64) & (topk[9] < 128), -1, topk[9])
+    c.check((out, lse), keep, rows=[9])
