@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libdsa.so")
 BINDING = os.path.join(HERE, "_dsa_binding.so")
 BUILT_WITH = os.path.join(BUILD_DIR, "built_with.txt")
 SOURCES = ["quant.cu", "layout.cu", "score.cu", "topk.cu", "norm.cu", "probe.cu", "kvcache.cu", "attend.cu",
-           "kvfp4.cu", "attend_fp4.cu"]
+           "kvfp4.cu", "attend_fp4_paged.cu", "attend_fp4_selected.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -18,6 +18,8 @@
 // Neither product cares in what order the summed index is taken, which leaves the
 // layouts free: a thread's bytes of a key are those of its own operand rows.
 // Codes times scales are exact in FP16 (6 bits).
+#pragma once
+
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -255,6 +257,7 @@ __device__ void lay_out4(const Att4Params& p, Axis4& x, int64_t* tmp, bool write
     __syncthreads();
 }
 
+template <bool kSelected>
 __global__ void __launch_bounds__(kPlan4Threads) attend_fp4_plan_kernel(const Att4Params p) {
     pdl_wait();
     pdl_launch_dependents();
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(kPlan4Threads) attend_fp4_plan_kernel(const At
 // comes from a bitmap of the row's positions; where a position is listed twice (it
 // counts twice), or where there are more positions than the bitmap holds, the slots
 // stay in the list's order.
+template <bool kSelected>
 __global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const Att4Params p) {
     pdl_wait();
     pdl_launch_dependents();
@@ -1732,23 +1736,26 @@ static int launch_all4(Att4Params& p, cudaStream_t stream) {
     p.warps = ctas * (p.cap <= 8    ? Shape4<kForm128, 8>::kWarps
                       : p.cap <= 16 ? (wide_head ? Shape4<kForm128, 16>::kWarps : Shape4<kForm64, 16>::kWarps)
                                     : Shape4<kForm128, 32>::kWarps);
-    if (kSelected && p.packed) {
-        const int bitmap = p.max_keys <= kBitmapKeys ? (p.max_keys + 31) / 32 * 4 : 0;
-        static bool attr_set[64] = {false};
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
-        if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(attend_fp4_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kBitmapKeys / 8) != cudaSuccess)
+    if constexpr (kSelected) {
+        if (p.packed) {
+            const int bitmap = p.max_keys <= kBitmapKeys ? (p.max_keys + 31) / 32 * 4 : 0;
+            auto* kernel = attend_fp4_list_kernel<kSelected>;
+            static bool attr_set[64] = {false};
+            int dev = 0;
+            if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
+            if (!attr_set[dev]) {
+                if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBitmapKeys / 8) !=
+                    cudaSuccess)
+                    return DSA_ERR_CUDA;
+                attr_set[dev] = true;
+            }
+            if (launch_pdl(kernel, dim3(p.rows), dim3(kList4Threads), bitmap, stream, p) != cudaSuccess)
                 return DSA_ERR_CUDA;
-            attr_set[dev] = true;
         }
-        if (launch_pdl(attend_fp4_list_kernel, dim3(p.rows), dim3(kList4Threads), bitmap, stream, p) != cudaSuccess)
-            return DSA_ERR_CUDA;
-    }
-    if (!kSelected && !p.plan_in_cta &&
-        launch_pdl(attend_fp4_plan_kernel, dim3(1), dim3(kPlan4Threads), 0, stream, p) != cudaSuccess)
+    } else if (!p.plan_in_cta && launch_pdl(attend_fp4_plan_kernel<kSelected>, dim3(1), dim3(kPlan4Threads), 0, stream,
+                                            p) != cudaSuccess) {
         return DSA_ERR_CUDA;
+    }
     const int rc = p.cap <= 8    ? launch_form4<kSelected, 8>(p, ctas, stream)
                    : p.cap <= 16 ? launch_form4<kSelected, 16>(p, ctas, stream)
                                  : launch_form4<kSelected, 32>(p, ctas, stream);
@@ -1785,79 +1792,3 @@ static Att4Params params4(const dsa_kv_cache_fp4* c, const Att4Layout& L, uint8_
 }
 
 }  // namespace dsa
-
-using namespace dsa;
-
-extern "C" size_t dsa_attend_workspace_size_fp4(int64_t rows, int64_t num_requests, int64_t heads, int64_t kv_heads,
-                                                int64_t dim, int64_t max_query_len, int64_t k) {
-    if (rows < 0 || num_requests < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || max_query_len < 0 || k < 0 ||
-        k > (1 << 24) || !sizes4_ok(rows, num_requests, heads, kv_heads, dim))
-        return 0;
-    return attend4_layout(rows, num_requests, heads, kv_heads, dim, max_query_len, k).total;
-}
-
-extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* q, int64_t q_row_stride,
-                                    int64_t q_head_stride, int64_t heads, const int32_t* block_table,
-                                    int64_t bt_stride, int64_t max_pages, const int32_t* starts,
-                                    const int32_t* row_ends, int64_t num_requests, int64_t rows, int64_t max_query_len,
-                                    float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
-                                    float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
-                                    void* stream_) {
-    const int rc = check_attend4(cache, dtype, q, q_row_stride, q_head_stride, heads, block_table, bt_stride,
-                                 max_pages, starts, row_ends, num_requests, rows, scale, out, out_row_stride,
-                                 out_head_stride, workspace);
-    if (rc != DSA_OK) return rc;
-    if (max_query_len < 0) return DSA_ERR_INVALID;
-    if (rows == 0) return DSA_OK;
-    const Att4Layout L = attend4_layout(rows, num_requests, heads, cache->heads, cache->dim, max_query_len, 0);
-    if (workspace_bytes < L.total) return DSA_ERR_INVALID;
-    Att4Params p = params4(cache, L, static_cast<uint8_t*>(workspace), scale);
-    p.bf16 = dtype == DSA_BF16;
-    p.q = static_cast<const uint16_t*>(q), p.qrow = q_row_stride, p.qhead = q_head_stride;
-    p.out = static_cast<uint16_t*>(out), p.orow = out_row_stride, p.ohead = out_head_stride;
-    p.lse = lse, p.status = status;
-    p.bt = block_table, p.bt_stride = bt_stride, p.starts = starts, p.row_ends = row_ends;
-    p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
-    p.group = p.heads / p.kv_heads;
-    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
-    p.plan_in_cta = p.R <= kCtaRequests && p.rows <= 4096;
-    p.axis.light = 5, p.axis.heavy = p.cap > 16 ? 7 : 5, p.axis.start = 4;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return launch_all4<false>(p, stream);
-}
-
-extern "C" int dsa_attend_selected_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* q,
-                                       int64_t q_row_stride, int64_t q_head_stride, int64_t heads,
-                                       const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
-                                       const int32_t* starts, const int32_t* row_ends, int64_t num_requests,
-                                       int64_t rows, const int32_t* topk, int64_t topk_stride, int64_t k, float scale,
-                                       void* out, int64_t out_row_stride, int64_t out_head_stride, float* lse,
-                                       void* workspace, size_t workspace_bytes, int32_t* status, void* stream_) {
-    const int rc = check_attend4(cache, dtype, q, q_row_stride, q_head_stride, heads, block_table, bt_stride,
-                                 max_pages, starts, row_ends, num_requests, rows, scale, out, out_row_stride,
-                                 out_head_stride, workspace);
-    if (rc != DSA_OK) return rc;
-    if (k < 0 || (k > 0 && rows > 0 && (!topk || topk_stride < k))) return DSA_ERR_INVALID;
-    if (k > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
-    if (rows == 0) return DSA_OK;
-    // (an empty list is one key long in the workspace: the rows still need their zeros)
-    const Att4Layout L = attend4_layout(rows, num_requests, heads, cache->heads, cache->dim, 1, k > 0 ? k : 1);
-    if (workspace_bytes < L.total) return DSA_ERR_INVALID;
-    Att4Params p = params4(cache, L, static_cast<uint8_t*>(workspace), scale);
-    p.bf16 = dtype == DSA_BF16;
-    p.q = static_cast<const uint16_t*>(q), p.qrow = q_row_stride, p.qhead = q_head_stride;
-    p.out = static_cast<uint16_t*>(out), p.orow = out_row_stride, p.ohead = out_head_stride;
-    p.lse = lse, p.status = status;
-    p.bt = block_table, p.bt_stride = bt_stride, p.starts = starts, p.row_ends = row_ends;
-    p.topk = topk, p.topk_stride = topk_stride, p.k = static_cast<int>(k);
-    p.R = static_cast<int>(num_requests), p.rows = static_cast<int>(rows), p.heads = static_cast<int>(heads);
-    p.group = p.heads / p.kv_heads;
-    p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
-    p.list_units = static_cast<int>((k + kUnit - 1) / kUnit);
-    p.list_tiles = (p.group + p.cap - 1) / p.cap;
-    const int64_t per_row = static_cast<int64_t>(p.kv_heads) * p.list_tiles * p.list_units;
-    if (per_row > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
-    p.packed = cache->num_pages <= (1 << 25) && per_row * rows * p.section >= kPackBytes;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return launch_all4<true>(p, stream);
-}

@@ -404,7 +404,6 @@ PyObject* kv_read_fp4(PyObject* const* a) {
     const int64_t n = s.size(0);
     const at::Tensor& slots = list_of(a[0], cache.device, at::kLong, n, "slots must be contiguous int64 [n]");
     int32_t* const status = status_word(a[8], cache.device);
-    const OnDevice on(cache.device);
     at::Tensor out[2];
     for (int i = 0; i < 2; ++i) {
         constexpr const char* what = "k_out and v_out must be [n, heads, dim] of dtype with contiguous columns";
@@ -415,6 +414,7 @@ PyObject* kv_read_fp4(PyObject* const* a) {
             out[i] = at::empty({n, cache.c.heads, cache.c.dim}, at::TensorOptions().dtype(type).device(cache.device));
         }
     }
+    const OnDevice on(cache.device);
     check(dsa_kv_read_fp4(&cache.c, dtype_of(type), static_cast<const int64_t*>(pointer(slots)), n, pointer(out[0]),
                           stride(out[0], 0), stride(out[0], 1), pointer(out[1]), stride(out[1], 0), stride(out[1], 1),
                           status, on.stream),
@@ -491,8 +491,8 @@ PyObject* attend_paged_fp4(PyObject* const* a) {
     const Attention4 x(a, a[6], a[7], a[8], a[9], a[10]);
     const int64_t max_query_len = whole(a[5]);
     int32_t* const status = status_word(a[12], x.cache.device);
-    const OnDevice on(x.cache.device);
     const at::Tensor ws = x.workspace(a[11], max_query_len, 0);
+    const OnDevice on(x.cache.device);
     check(dsa_attend_paged_fp4(&x.cache.c, dtype_of(x.q.scalar_type()), pointer(x.q), stride(x.q, 0), stride(x.q, 1),
                                x.heads, x.table, x.bt_stride, x.pages, x.starts, x.ends, x.requests, x.rows,
                                max_query_len, x.scale, pointer(x.out), stride(x.out, 0), stride(x.out, 1), x.lse_ptr,
@@ -509,8 +509,8 @@ PyObject* attend_selected_fp4(PyObject* const* a) {
     need(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == x.rows && dense(t, 1), what);
     const int64_t k = t.size(1);
     int32_t* const status = status_word(a[12], x.cache.device);
-    const OnDevice on(x.cache.device);
     const at::Tensor ws = x.workspace(a[11], 1, k > 0 ? k : 1);
+    const OnDevice on(x.cache.device);
     check(dsa_attend_selected_fp4(&x.cache.c, dtype_of(x.q.scalar_type()), pointer(x.q), stride(x.q, 0),
                                   stride(x.q, 1), x.heads, x.table, x.bt_stride, x.pages, x.starts, x.ends, x.requests,
                                   x.rows, static_cast<const int32_t*>(pointer(t)), stride(t, 0, k), k, x.scale,
