@@ -178,7 +178,7 @@ __device__ __forceinline__ void count_units(Axis4& x) {
 
 // Lays out the requests (whole block).  `tmp`: 66 int64 of shared scratch.
 // `write`: also what the join reads.
-__device__ void lay_out4(const Att4Params& p, Axis4& x, int64_t* tmp, bool write) {
+static __device__ void lay_out4(const Att4Params& p, Axis4& x, int64_t* tmp, bool write) {
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
     // (on their way while the starts are read)
