@@ -37,7 +37,7 @@ constexpr int kPlan4Threads = 512;
 constexpr int kFewUnits = 8;            // units a warp under which the axis counts units alone
 constexpr int kList4Threads = 256;
 constexpr int kBitmapKeys = 1 << 20;    // positions that a list is put in order by
-constexpr int64_t kPackBytes = 64 << 20;   // listed sections' bytes from which lists are put in order first
+constexpr int64_t kPackBytes = 32 << 20;   // listed sections' bytes from which lists are put in order first
 constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr float kLn2_4 = 0.6931471805599453f;
 // Weights are kept times 2^6: FP16 then holds them from 2^-30 of the largest on.
@@ -282,6 +282,14 @@ __global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const At
     const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t* src = p.topk + row * p.topk_stride;
     int* const dst = p.list + static_cast<int64_t>(row) * p.list_units * kUnit;
+    // (the first entries are on their way while the row's request is looked up)
+    constexpr int kFirst = 8;
+    int first[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int at = threadIdx.x + i * kList4Threads;
+        first[i] = at < p.k ? src[at] : -1;
+    }
     const int e = p.row_ends[row], bound = min(max(e, 0), p.max_keys);
     const bool ordered = p.max_keys <= kBitmapKeys;
     const int words = ordered ? (bound + 31) / 32 : 0;
@@ -294,11 +302,15 @@ __global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const At
         if (a < 0 || b < a || b > p.rows) bad = true;
         if (a <= row && row < b) atomicMax(&s_req, j);
     }
-    if (ordered)
-        for (int i = threadIdx.x; i < p.k; i += kList4Threads) {
-            const int t = src[i];
-            if (t >= 0 && t < bound && (atomicOr(&bitmap[t >> 5], 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
-        }
+    bool past = false;
+    auto mark = [&](int t) {
+        past |= t >= bound;
+        if (ordered && t >= 0 && t < bound && (atomicOr(&bitmap[t >> 5], 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+        if (first[i] >= 0) mark(first[i]);
+    for (int i = threadIdx.x + kFirst * kList4Threads; i < p.k; i += kList4Threads) mark(src[i]);
     __syncthreads();
     const int req = s_req;
     const int32_t* const table = p.bt + (req >= 0 ? req : 0) * p.bt_stride;
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const At
     };
     int count = 0;
     if (req >= 0) {
-        if (e != bound) bad = true;
+        if (e != bound || past) bad = true;
         const bool by_map = ordered && !s_twice;
         // positions: a run of the bitmap's words a thread; entries: one a thread and round
         const int each = (words + kList4Threads - 1) / kList4Threads;
@@ -347,7 +359,6 @@ __global__ void __launch_bounds__(kList4Threads) attend_fp4_list_kernel(const At
             count = all;
             __syncthreads();
         }
-        for (int i = threadIdx.x; i < p.k; i += kList4Threads) bad |= src[i] >= bound;
     }
     for (int i = count + threadIdx.x; i < p.list_units * kUnit; i += kList4Threads) dst[i] = -1;
     if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
@@ -1536,7 +1547,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
         slot = 2 * static_cast<int64_t>(wa + 1);
     }
     const bool on = lane * 4 < p.dim;
-    constexpr int kAhead = 4;
+    constexpr int kAhead = kWarps > 1 ? 8 : 4;   // pieces a warp has in flight
     float top = -INFINITY, l = 0.0f;
     float4 o = {0, 0, 0, 0};
     for (int base = kWarps == 1 ? 0 : warp; base < pieces; base += kAhead * kWarps) {

@@ -36,7 +36,7 @@ extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype
     p.group = p.heads / p.kv_heads;
     p.max_keys = cache->num_pages > 0 ? static_cast<int>(max_pages * kPage) : 0;
     p.plan_in_cta = p.R <= kCtaRequests && p.rows <= 4096;
-    p.axis.light = 5, p.axis.heavy = p.cap > 16 ? 7 : 5, p.axis.start = 4;
+    p.axis.light = 5, p.axis.heavy = p.cap > 16 ? 7 : 5, p.axis.start = p.cap > 16 ? 7 : 4;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return launch_all4<false>(p, stream);
 }

@@ -69,17 +69,22 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
     a = x;
 }
 
-// The largest magnitude as bits: their order is that of the values, and NaN is above all.
-__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
-    uint32_t m = 0;
+// The larger of two magnitudes, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+    float m = fabsf(x[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
     return m;
 }
 
 // A block's scale byte from its largest magnitude, 6 g given.
-__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float six) {
-    const float s = __fdiv_rn(__uint_as_float(amax_bits), six);
+__device__ __forceinline__ uint32_t block_scale(float amax, float six) {
+    const float s = __fdiv_rn(amax, six);
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(s));
     return two & 0xFFu;
@@ -87,8 +92,9 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float six) {
 
 // Eight codes of x / (s g).  The quotient is correctly rounded without a division
 // an element: q0 = x inv(d) with the correctly rounded reciprocal, its remainder
-// exactly by a fused multiply-add, one correction (Markstein).  |x| is first cut to
-// 8 d, past the largest code, so that nothing overflows.
+// (negated, so that the quotient of -0 stays -0) exactly by a fused multiply-add, one
+// correction (Markstein).  Under the largest scale |x| is first cut to 8 d, past the
+// largest code, so that nothing overflows; under the others |x| is not above 7 d.
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale_byte, float g) {
     const float d = __fmul_rn(half2_float2(e4m3x2_f16(scale_byte)).x, g);
     uint32_t w = 0;
@@ -97,15 +103,22 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale_b
         for (int i = 0; i < 8; ++i) w |= (__float_as_uint(x[i]) >> 31) << (4 * i + 3);
         return w;
     }
-    const float inv = __frcp_rn(d), most = 8.0f * d;
+    const float inv = __frcp_rn(d);
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = x[i];
+    if (scale_byte >= 0x7E) {
+        const float most = 8.0f * d;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = fminf(fmaxf(a[i], -most), most);
+    }
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         float y[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float a = fminf(fmaxf(x[i + j], -most), most);
-            const float q0 = __fmul_rn(a, inv);
-            y[j] = copysignf(__fmaf_rn(__fmaf_rn(-q0, d, a), inv, q0), a);   // (-0 would lose its sign)
+            const float q0 = __fmul_rn(a[i + j], inv);
+            y[j] = __fmaf_rn(-__fmaf_rn(q0, d, -a[i + j]), inv, q0);
         }
         uint32_t two;
         asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
@@ -247,14 +260,14 @@ __device__ __forceinline__ void append_keys_values(const Append4Args& a, int64_t
         unpack8<T>(kw, f);
         unpack8<T>(ky, g);
         if (x.turns) turn_row<kInterleaved>(f, g, c, s);
-        uint32_t m0 = amax8(f), m1 = amax8(g);
+        float m0 = amax8(f), m1 = amax8(g);
         if (!kInterleaved && a.rot_units > 0) {
-            const uint32_t a0 = __shfl_sync(0xFFFFFFFFu, m0, mate0), a1 = __shfl_sync(0xFFFFFFFFu, m1, mate0);
-            const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, m0, mate1), b1 = __shfl_sync(0xFFFFFFFFu, m1, mate1);
-            m0 = max(m0, second0 ? a1 : a0);
-            m1 = max(m1, second1 ? b1 : b0);
+            const float a0 = __shfl_sync(0xFFFFFFFFu, m0, mate0), a1 = __shfl_sync(0xFFFFFFFFu, m1, mate0);
+            const float b0 = __shfl_sync(0xFFFFFFFFu, m0, mate1), b1 = __shfl_sync(0xFFFFFFFFu, m1, mate1);
+            m0 = max_nan(m0, second0 ? a1 : a0);
+            m1 = max_nan(m1, second1 ? b1 : b0);
         } else {
-            m0 = m1 = max(m0, m1);
+            m0 = m1 = max_nan(m0, m1);
         }
         if (!on) continue;
         {
@@ -273,7 +286,7 @@ __device__ __forceinline__ void append_keys_values(const Append4Args& a, int64_t
         }
         unpack8<T>(vw, f);
         unpack8<T>(vy, g);
-        const uint32_t s0 = block_scale(max(amax8(f), amax8(g)), a.v_six);
+        const uint32_t s0 = block_scale(max_nan(amax8(f), amax8(g)), a.v_six);
         const uint32_t w0 = codes8(f, s0, a.v_scale), w1 = codes8(g, s0, a.v_scale);
         *reinterpret_cast<uint2*>(at + fp4_v_row(a.dim, off) + x.unit * 8) = make_uint2(w0, w1);
         scales[sr + x.unit] = static_cast<uint8_t>(s0);
@@ -329,7 +342,8 @@ __global__ void __launch_bounds__(kRead4Threads) kv_read_fp4_kernel(const Read4A
     pdl_launch_dependents();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kRead4Threads + threadIdx.x;
     const int per_token = a.heads * a.units;
-    const int64_t tok = i / per_token;
+    const int64_t tok = i < (int64_t(1) << 32) ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per_token)
+                                               : i / per_token;
     if (tok >= a.n) return;
     const int in = static_cast<int>(i - tok * per_token);
     const int head = in / a.units, unit = in - head * a.units;
@@ -437,10 +451,13 @@ extern "C" int dsa_kv_append_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, c
     a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
     a.k_six = 6.0f * a.k_scale, a.v_six = 6.0f * a.v_scale;
     a.status = status;
-    // Long appends: 64 threads a token, so that a thread turns several heads with
-    // the angles it holds; short ones: a CTA a token (the split of dsa_kv_append).
-    const bool streams = n >= 4 * device_sm_count();
-    const int want = streams ? 64 : kAppend4Threads;
+    // The longer the append, the fewer threads a token, so that a thread turns more
+    // heads with the angles it holds: short ones a CTA a token of each kind (latency),
+    // 16384 tokens of 32 + 2 x 8 heads 131, 91, 84 to 87 and 84 us with 128, 64, 32 and
+    // 16 threads (the call and the reading back of what it wrote).
+    const int64_t sms = device_sm_count();
+    const bool streams = n >= 4 * sms;
+    const int want = n >= 32 * sms ? 16 : streams ? 64 : kAppend4Threads;
     a.row_lanes = 1;
     while (a.row_lanes < a.units) a.row_lanes *= 2;
     a.head_lanes = want / a.row_lanes;
