@@ -1237,13 +1237,27 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
     }
     int i = 0;
     bool gave_up = false;
+    Item4 x, behind;
+    auto item_of = [&](int at, Item4* y) {
+        if (kSelected) listed_unit(p, starts, u0 + at, y);
+        else paged_unit(p, axis, u0 + at, y);
+    };
+    if (count > 0) item_of(0, &behind);
     while (i < count && !gave_up) {
         // The part of an item that is in the share: units at .. until - 1 of its n.
-        Item4 x;
-        if (kSelected) listed_unit(p, starts, u0 + i, &x);
-        else paged_unit(p, axis, u0 + i, &x);
+        x = behind;
         k.begin(x);
         const int until = min(x.n, x.at + count - i);
+        // The next item's queries are on their way to L2 meanwhile.
+        if (i + until - x.at < count) {
+            item_of(i + until - x.at, &behind);
+            if (lane < behind.nq) {
+                const int n = behind.first + lane;
+                const uint16_t* src =
+                    p.q + (behind.row0 + n / p.group) * p.qrow + (behind.kvh * p.group + n % p.group) * p.qhead;
+                for (int c = 0; c < p.dim; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+            }
+        }
         for (int at = x.at; at < until; ++at, ++i) {
             uint8_t* const stage = ring + (i % kStages) * p.stage;
             if constexpr (kSelected) {
