@@ -646,7 +646,8 @@ size_t dsa_kv_section_bytes_fp4(int64_t dim);
  *   s = E4M3(max |x| / (6 g)), codes E2M1(x / (s g)), g = k_scale or v_scale,
  * products and quotients correctly rounded in FP32, conversions to nearest (ties to
  * even) and to the largest magnitude where a value is past it; s = 0 makes every
- * code a zero.  A block with a NaN gets the scale NaN (it reads as NaN) and codes of
+ * code a zero.  Where equal slots race, codes of one token may be left under scales of
+ * another.  A block with a NaN gets the scale NaN (it reads as NaN) and codes of
  * the largest magnitude; an infinite value becomes the largest magnitude of its block, 2688 g.
  */
 int dsa_kv_append_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* k, int64_t k_token_stride,

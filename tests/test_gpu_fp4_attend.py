@@ -65,6 +65,14 @@ def test_many_rows(cuda_lib):
     c.check(c.paged(cuda_lib), rows=range(0, 4800, 401))
 
 
+@pytest.mark.parametrize("qlen", [33, 64, 257, 700])
+@pytest.mark.parametrize("hq,hkv,dim", [(24, 2, 128), (5, 1, 64)])
+def test_rows_of_a_prompt(cuda_lib, hq, hkv, dim, qlen):
+    """Even and odd numbers of row tiles, whose bounds rise from the first key to the last, beside short requests."""
+    c = Case([qlen, 90, 0, qlen + 300], [qlen, 1, 2, 40], hq=hq, hkv=hkv, dim=dim, pad_rows=3)
+    c.check(c.paged(cuda_lib), rows=sorted({*range(0, c.q.shape[0], 29), 0, qlen - 1, qlen, c.q.shape[0] - 1}))
+
+
 @pytest.mark.parametrize("hq,hkv,lens", [(16, 1, [20000] * 2), (32, 8, [9001]), (64, 8, [5000, 10, 7000]),
                                          (12, 4, [30001])])
 def test_long(cuda_lib, hq, hkv, lens):
