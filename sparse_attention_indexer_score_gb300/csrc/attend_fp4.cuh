@@ -1102,7 +1102,7 @@ constexpr int kAxisBytes4 = (2 * (kCtaRequests + 1) + 66) * 8 + kCtaRequests * 4
 // A head's row tiles lie on the axis from both ends of the request in turn: where rows
 // see ever more keys (a prompt's), units past the bounds of a tile's rows are not
 // multiplied, and two neighbours together have as many as any others (4096 rows of 4096
-// keys, 32 heads over 8: 1051 us in order).
+// keys, 32 heads over 8: 732 us, 1051 with the tiles in order).
 __device__ __forceinline__ int tile_at(int i, int tiles) { return i & 1 ? tiles - 1 - i / 2 : i / 2; }
 __device__ __forceinline__ int place_of(int tile, int tiles) {
     return 2 * tile < tiles ? 2 * tile : 2 * (tiles - 1 - tile) + 1;

@@ -320,25 +320,40 @@ struct Read4Args {
     int32_t* status;
 };
 
-template <typename T>
+// 16 columns, first to leave L2: in one store where they are a sector (32-byte
+// alignment).  A sector that is written in two halves may leave L2 between them, and
+// what is missing is then read.
+template <bool kSectors>
+__device__ __forceinline__ void st_block(uint16_t* dst, const uint32_t (&w)[8]) {
+    if constexpr (kSectors) {
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4*>(dst + 8), make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+template <typename T, bool kSectors>
 __device__ __forceinline__ void write_block(uint16_t* dst, uint2 codes, uint32_t scale, float g) {
     const float s = half2_float2(e4m3x2_f16(scale)).x;
+    uint32_t out[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint32_t h[4];
         e2m1x8(i ? codes.y : codes.x, h);
-        uint32_t out[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = half2_float2(h[j]);
-            out[j] = T::pack(__fmul_rn(__fmul_rn(f.x, s), g), __fmul_rn(__fmul_rn(f.y, s), g));
+            out[4 * i + j] = T::pack(__fmul_rn(__fmul_rn(f.x, s), g), __fmul_rn(__fmul_rn(f.y, s), g));
         }
-        __stcs(reinterpret_cast<uint4*>(dst + 8 * i), make_uint4(out[0], out[1], out[2], out[3]));
     }
+    st_block<kSectors>(dst, out);
 }
 
 // A thread reads the block of 16 columns of a token's head out of keys and values.
-template <typename T>
+template <typename T, bool kSectors>
 __global__ void __launch_bounds__(kRead4Threads) kv_read_fp4_kernel(const Read4Args a) {
     pdl_wait();
     pdl_launch_dependents();
@@ -363,8 +378,8 @@ __global__ void __launch_bounds__(kRead4Threads) kv_read_fp4_kernel(const Read4A
         ks = scales[0];
         vs = scales[fp4_scale_row(a.dim)];
     }
-    write_block<T>(a.k + tok * a.kt + head * a.kh + unit * 16, kc, ks, a.k_scale);
-    write_block<T>(a.v + tok * a.vt + head * a.vh + unit * 16, vc, vs, a.v_scale);
+    write_block<T, kSectors>(a.k + tok * a.kt + head * a.kh + unit * 16, kc, ks, a.k_scale);
+    write_block<T, kSectors>(a.v + tok * a.vt + head * a.vh + unit * 16, vc, vs, a.v_scale);
 }
 
 template <typename T>
@@ -506,8 +521,10 @@ extern "C" int dsa_kv_read_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, con
     if (blocks > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const dim3 grid(static_cast<unsigned>(blocks));
-    const cudaError_t err =
-        dtype == DSA_BF16 ? launch_pdl(kv_read_fp4_kernel<Bf16>, grid, dim3(kRead4Threads), 0, stream, a)
-                          : launch_pdl(kv_read_fp4_kernel<Fp16>, grid, dim3(kRead4Threads), 0, stream, a);
+    const bool sectors = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0 &&
+                         ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 15) == 0;
+    auto* kernel = dtype == DSA_BF16 ? (sectors ? kv_read_fp4_kernel<Bf16, true> : kv_read_fp4_kernel<Bf16, false>)
+                                     : (sectors ? kv_read_fp4_kernel<Fp16, true> : kv_read_fp4_kernel<Fp16, false>);
+    const cudaError_t err = launch_pdl(kernel, grid, dim3(kRead4Threads), 0, stream, a);
     return err == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -146,6 +146,18 @@ def test_read_into_views_and_past_the_pool(cuda_lib):
     assert cuda_lib.kv_read_fp4(slots[:0], cache, 96)[0].shape == (0, 3, 96)
 
 
+@pytest.mark.parametrize("at,width", [(0, 96), (0, 104), (8, 112), (16, 112), (8, 104)])
+def test_read_into_any_alignment(cuda_lib, at, width):
+    """Rows that begin on 32 bytes, and on 16 only."""
+    q, k, v, slots, cache, pos, cs = case(67, 1, 3, 80, 80, "fp16")
+    cuda_lib.kv_append_fp4(k, v, slots, cache, pos, cs)
+    want = cuda_lib.kv_read_fp4(slots, cache, 80, torch.float16)
+    room = torch.full((2, 67, 3, width), 7.0, dtype=torch.float16, device="cuda")
+    got = cuda_lib.kv_read_fp4(slots, cache, 80, torch.float16, k_out=room[0][..., at:at + 80], v_out=room[1][..., at:at + 80])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((room[..., :at] == 7).all()) and bool((room[..., at + 80:] == 7).all())
+
+
 def test_far_pages(cuda_lib):
     """Sections past 2^32 bytes of the pool."""
     pages, heads, dim = 60000, 8, 128                     # 4.4 GB
