@@ -24,7 +24,7 @@
 // unit to 435 cycles, 32 to 670.  Measured: 413, 653 and 712 cycles.  So up to 8 rows
 // the memory bounds (64 requests of 4096 to 8192 keys, 32 heads over 8: 82 us, 82 % of
 // the copy rate with 5 us until the first unit), past them the pipes (128 requests of 4
-// rows, 64 heads over 8, 64 to 8192 keys: 236 us and 13 for the join).
+// rows, 64 heads over 8, 64 to 8192 keys: 243 us, 11 of them the join).
 //
 // tcgen05 was built for 9 to 32 rows and taken back: operands made by some warps and put
 // into tensor memory, products issued by another, the softmax in four more.  It was right
@@ -1590,14 +1590,15 @@ attend_fp4_cluster_kernel(const Att4Params p) {
 // ----------------------------------------------------------------- join
 // Joins the pieces of a (row, head), and writes the rows that no unit reached:
 // kWarps warps take every kWarps-th piece, four columns a lane.  Bound by the pieces'
-// way through L2 and by its launch: 5 us behind 64 rows of 32 heads, 13 behind 512 of 64.
-template <int kWarps, bool kSelected>
+// way through L2 and by its launch: 5 us behind 64 rows of 32 heads, 11 behind 512 of 64.
+// A warp by itself takes kHeads neighbouring heads of a row, which lie in one tile.
+template <int kWarps, int kHeads, bool kSelected>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_join_kernel(const Att4Params p) {
     constexpr int kItems = kWarps == 1 ? 4 : 1;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t item = blockIdx.x * kItems + (kWarps == 1 ? warp : 0), heads = p.heads;
+    const uint32_t item = (blockIdx.x * kItems + (kWarps == 1 ? warp : 0)) * kHeads, heads = p.heads;
     if (item >= static_cast<uint32_t>(p.rows) * heads) return;
     const int row = item / heads, head = item - row * heads;
     const int kvh = static_cast<uint32_t>(head) / static_cast<uint32_t>(p.group), in_group = head - kvh * p.group;
@@ -1629,61 +1630,74 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_jo
         slot = 2 * static_cast<int64_t>(wa + 1);
     }
     const bool on = lane * 4 < p.dim;
-    constexpr int kAhead = kWarps > 1 ? 8 : 4;   // pieces a warp has in flight
-    float top = -INFINITY, l = 0.0f;
-    float4 o = {0, 0, 0, 0};
+    constexpr int kAhead = kWarps > 1 ? 8 : kHeads > 1 ? 2 : 4;   // pieces a warp has in flight
+    float top[kHeads], l[kHeads];
+    float4 o[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) top[h] = -INFINITY, l[h] = 0.0f, o[h] = {0, 0, 0, 0};
     for (int base = kWarps == 1 ? 0 : warp; base < pieces; base += kAhead * kWarps) {
-        float2 e[kAhead];
-        float4 v[kAhead];
+        float2 e[kHeads][kAhead];
+        float4 v[kHeads][kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = base + j * kWarps;
-            e[j] = make_float2(-INFINITY, 0.0f);
-            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < pieces) {
-                const int64_t at = (i == 0 ? slot - 1 : slot + 2 * (i - 1)) * p.cap + cap_row;
-                e[j] = p.pml[at];
-                if (on) v[j] = *reinterpret_cast<const float4*>(p.po + at * p.dim + lane * 4);
+            const int64_t at = (i == 0 ? slot - 1 : slot + 2 * (i - 1)) * p.cap + cap_row;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                e[h][j] = make_float2(-INFINITY, 0.0f);
+                v[h][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < pieces) {
+                    e[h][j] = p.pml[at + h];
+                    if (on) v[h][j] = *reinterpret_cast<const float4*>(p.po + (at + h) * p.dim + lane * 4);
+                }
             }
         }
-        float m = top;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) m = fmaxf(m, e[j].x);
-        const float keep = top == -INFINITY ? 0.0f : ex2_4(top - m);
-        top = m;
-        l *= keep;
-        o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+        for (int h = 0; h < kHeads; ++h) {
+            float m = top[h];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const float f = e[j].x == -INFINITY ? 0.0f : ex2_4(e[j].x - m);
-            l += e[j].y * f;
-            o.x += v[j].x * f, o.y += v[j].y * f, o.z += v[j].z * f, o.w += v[j].w * f;
+            for (int j = 0; j < kAhead; ++j) m = fmaxf(m, e[h][j].x);
+            const float keep = top[h] == -INFINITY ? 0.0f : ex2_4(top[h] - m);
+            top[h] = m;
+            l[h] *= keep;
+            o[h].x *= keep, o[h].y *= keep, o[h].z *= keep, o[h].w *= keep;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float f = e[h][j].x == -INFINITY ? 0.0f : ex2_4(e[h][j].x - m);
+                l[h] += e[h][j].y * f;
+                o[h].x += v[h][j].x * f, o[h].y += v[h][j].y * f, o[h].z += v[h][j].z * f, o[h].w += v[h][j].w * f;
+            }
         }
     }
     if (kWarps > 1) {
+        static_assert(kWarps == 1 || kHeads == 1, "several warps join one head");
         __shared__ float2 sl[kWarps];
         __shared__ float4 so[kWarps][32];
-        if (lane == 0) sl[warp] = make_float2(top, l);
-        so[warp][lane] = o;
+        if (lane == 0) sl[warp] = make_float2(top[0], l[0]);
+        so[warp][lane] = o[0];
         __syncthreads();
         if (warp > 0) return;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sl[i].x);
-        l = 0.0f;
-        o = {0, 0, 0, 0};
+        for (int i = 0; i < kWarps; ++i) top[0] = fmaxf(top[0], sl[i].x);
+        l[0] = 0.0f;
+        o[0] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             const float4 v = so[i][lane];
-            const float f = sl[i].x == -INFINITY ? 0.0f : ex2_4(sl[i].x - top);
-            l += sl[i].y * f;
-            o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+            const float f = sl[i].x == -INFINITY ? 0.0f : ex2_4(sl[i].x - top[0]);
+            l[0] += sl[i].y * f;
+            o[0].x += v.x * f, o[0].y += v.y * f, o[0].z += v.z * f, o[0].w += v.w * f;
         }
     }
-    const float inv = l == 0.0f ? 0.0f : p.v_scale / l;
-    if (on)
-        *reinterpret_cast<uint2*>(p.out + row * p.orow + head * p.ohead + lane * 4) =
-            make_uint2(pack2(p, o.x * inv, o.y * inv), pack2(p, o.z * inv, o.w * inv));
-    if (lane == 0 && p.lse) p.lse[item] = l == 0.0f ? -INFINITY : (top + log2f(l) - kLift) * kLn2_4;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+        const float inv = l[h] == 0.0f ? 0.0f : p.v_scale / l[h];
+        if (on)
+            *reinterpret_cast<uint2*>(p.out + row * p.orow + (head + h) * p.ohead + lane * 4) =
+                make_uint2(pack2(p, o[h].x * inv, o[h].y * inv), pack2(p, o[h].z * inv, o[h].w * inv));
+        if (lane == 0 && p.lse)
+            p.lse[item + h] = l[h] == 0.0f ? -INFINITY : (top[h] + log2f(l[h]) - kLift) * kLn2_4;
+    }
 }
 
 // ----------------------------------------------------------------- host
@@ -1854,12 +1868,17 @@ static int launch_all4(Att4Params& p, cudaStream_t stream) {
                                  : launch_form4<kSelected, 32>(p, ctas, stream);
     if (rc != DSA_OK) return rc;
     const int64_t items = static_cast<int64_t>(p.rows) * p.heads;
-    // Few rows and heads have many pieces each, which the warps of a CTA share.
+    // Few rows and heads have many pieces each, which the warps of a CTA share; many leave a warp several heads, for
+    // which it looks up the pieces once (the whole call, 4 heads a warp and one: 400 rows of 64 heads 81 and 85 us, 64
+    // rows of 32 heads 88.0 and 87.3).
     const cudaError_t e =
         items <= 4 * ctas
-            ? launch_pdl(attend_fp4_join_kernel<8, kSelected>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
+            ? launch_pdl(attend_fp4_join_kernel<8, 1, kSelected>, dim3(static_cast<unsigned>(items)), dim3(256), 0,
                          stream, p)
-            : launch_pdl(attend_fp4_join_kernel<1, kSelected>, dim3(static_cast<unsigned>((items + 3) / 4)),
+        : items >= 32 * ctas && p.group % 4 == 0
+            ? launch_pdl(attend_fp4_join_kernel<1, 4, kSelected>, dim3(static_cast<unsigned>((items + 15) / 16)),
+                         dim3(128), 0, stream, p)
+            : launch_pdl(attend_fp4_join_kernel<1, 1, kSelected>, dim3(static_cast<unsigned>((items + 3) / 4)),
                          dim3(128), 0, stream, p);
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -70,7 +70,10 @@ def test_many_rows(cuda_lib):
 def test_rows_of_a_prompt(cuda_lib, hq, hkv, dim, qlen):
     """Even and odd numbers of row tiles, whose bounds rise from the first key to the last, beside short requests."""
     c = Case([qlen, 90, 0, qlen + 300], [qlen, 1, 2, 40], hq=hq, hkv=hkv, dim=dim, pad_rows=3)
-    c.check(c.paged(cuda_lib), rows=sorted({*range(0, c.q.shape[0], 29), 0, qlen - 1, qlen, c.q.shape[0] - 1}))
+    rows = sorted({*range(0, c.q.shape[0], 29), 0, qlen - 1, qlen, c.q.shape[0] - 1})
+    c.check(c.paged(cuda_lib), rows=rows)
+    topk = choose(c, 100)
+    c.check(c.selected(cuda_lib, topk), topk, rows=rows)
 
 
 @pytest.mark.parametrize("hq,hkv,lens", [(16, 1, [20000] * 2), (32, 8, [9001]), (64, 8, [5000, 10, 7000]),
