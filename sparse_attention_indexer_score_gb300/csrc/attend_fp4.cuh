@@ -1539,6 +1539,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         __syncwarp();
         // The warp's results take the place of its ring.
         if (x.nq > 0 && count > 0) k.finish(reinterpret_cast<float*>(ring), ml[warp]);
+        fence_proxy_async_smem();   // (the next tile's copies take the results' place)
         cluster.sync();
         const int pieces = min(units, kSharers);
         for (int i = rank * blockDim.x + threadIdx.x; i < x.nq * (p.dim / 4); i += kCluster * blockDim.x) {

@@ -352,3 +352,52 @@ def test_lists_in_order_of_their_positions(cuda_lib):
     keep = topk.clone()                                   # (the same keys, in units of their own)
     keep[9] = torch.where((topk[9] >= 64) & (topk[9] < 128), -1, topk[9])
     c.check((out, lse), keep, rows=[9])
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls of both kinds side by side, each stream with a workspace of its own, give what they give alone."""
+    cases = [Case([900 + 61 * j for j in range(24)], [4] * 24, hq=64, hkv=8, dim=128, seed=5),
+             Case([1300], [2], hq=16, hkv=2, dim=128, dtype="fp16", seed=6)]
+    lists = [choose(c, 300, seed=9) for c in cases]
+    spaces = [torch.empty(max(cuda_lib.attend_workspace_size_fp4(c.q.shape[0], c.starts.numel() - 1, c.q.shape[1], c.hkv,
+                                                                 c.dim, c.qlen, k) for k in (0, 300)),
+                          dtype=torch.uint8, device="cuda") for c in cases]
+
+    def run(i):
+        c = cases[i]
+        args = (c.q, c.cache, c.block_table, c.starts, c.row_ends)
+        return (cuda_lib.attend_paged_fp4(*args, c.qlen, workspace=spaces[i])[0],
+                cuda_lib.attend_selected_fp4(*args, lists[i], workspace=spaces[i])[0])
+
+    alone = [run(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(4):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got.append((i, run(i)))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone[i]))
+
+
+@pytest.mark.parametrize("requests", [1, 90])
+def test_rows_before_the_first_request(cuda_lib, requests):
+    c = Case([150 + j for j in range(requests)], [2] * requests, hq=8, hkv=2, dim=96)
+    topk = choose(c, 70)
+    q = torch.cat([c.q[:1].expand(3, -1, -1), c.q])
+    ends = torch.cat([torch.full((3,), 40, dtype=torch.int32, device="cuda"), c.row_ends])
+    args = (q, c.cache, c.block_table, c.starts + 3, ends)
+    for got, lists in ((cuda_lib.attend_paged_fp4(*args, 2, want_lse=True), None),
+                       (cuda_lib.attend_selected_fp4(*args, torch.cat([topk[:1].expand(3, -1), topk]), want_lse=True), topk)):
+        assert not got[0][:3].any() and bool(torch.isneginf(got[1][:3]).all())
+        c.check(tuple(t[3:] for t in got), lists, rows=range(0, 2 * requests, 7))
+
+
+def test_output_in_the_place_of_the_queries(cuda_lib):
+    c = Case([500 + 9 * j for j in range(40)], [3] * 40, hq=24, hkv=2, dim=64)
+    want = c.paged(cuda_lib)[0]
+    q = c.q.clone()
+    out, _ = cuda_lib.attend_paged_fp4(q, c.cache, c.block_table, c.starts, c.row_ends, c.qlen, out=q)
+    assert out is q and torch.equal(q, want)
