@@ -1374,7 +1374,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 ml[kWarps][kRows];
+    __shared__ float2 ml[kWarps][kRows], joined[kRows];   // references and sums of the warps, of the CTA
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster.block_rank(), item = blockIdx.x / kCluster;
     pdl_wait();
@@ -1433,21 +1433,24 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         for (int d = 1; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
         units = (most + kUnit - 1) / kUnit;
     }
-    // what the geometry says wrong, and rows outside every request
-    if (blockIdx.x == 0) {
-        for (int j = threadIdx.x; j <= p.R; j += blockDim.x) {
+    // what the geometry says wrong, and rows outside every request (a warp that has units last, or none)
+    if (blockIdx.x == 0 && warp == kWarps - 1) {
+        for (int j = lane; j <= p.R; j += 32) {
             const int a = p.starts[j];
             bad |= a < 0 || (j > 0 && a < p.starts[j - 1]) || a > p.rows;
         }
         if (!kSelected)
-            for (int r = warp; r < p.rows; r += kWarps) {
-                bool mine = false;
-                for (int j = lane; j < p.R; j += 32) mine |= p.starts[j] <= r && r < p.starts[j + 1];
-                if (__any_sync(0xFFFFFFFFu, mine)) continue;
-                for (int i = lane; i < p.heads * (p.dim / 8); i += 32) {
-                    const int head = i / (p.dim / 8), col = i - head * (p.dim / 8);
-                    *reinterpret_cast<uint4*>(p.out + r * p.orow + head * p.ohead + col * 8) = make_uint4(0, 0, 0, 0);
-                    if (col == 0 && p.lse) p.lse[static_cast<int64_t>(r) * p.heads + head] = -INFINITY;
+            for (int base = 0; base < p.rows; base += 32) {
+                bool mine = base + lane >= p.rows;
+                for (int j = 0; j < p.R; ++j) mine |= p.starts[j] <= base + lane && base + lane < p.starts[j + 1];
+                for (uint32_t others = ~__ballot_sync(0xFFFFFFFFu, mine); others; others &= others - 1) {
+                    const int r = base + __ffs(others) - 1;
+                    for (int i = lane; i < p.heads * (p.dim / 8); i += 32) {
+                        const int head = i / (p.dim / 8), col = i - head * (p.dim / 8);
+                        *reinterpret_cast<uint4*>(p.out + r * p.orow + head * p.ohead + col * 8) =
+                            make_uint4(0, 0, 0, 0);
+                        if (col == 0 && p.lse) p.lse[static_cast<int64_t>(r) * p.heads + head] = -INFINITY;
+                    }
                 }
             }
     }
@@ -1537,44 +1540,55 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         if (!kSelected && tile == 0 && count == 0 && lane == 0 && first_page >= 0)   // the copy that was not needed
             mbar_drain(&desk.full[0], 0, globaltimer() + kWaitLimitNs, p.status);
         __syncwarp();
-        // The warp's results take the place of its ring.
+        // The warp's results take the place of its ring; the CTA's are joined in its first warp's, the cluster's from
+        // there.
         if (x.nq > 0 && count > 0) k.finish(reinterpret_cast<float*>(ring), ml[warp]);
         fence_proxy_async_smem();   // (the next tile's copies take the results' place)
-        cluster.sync();
-        const int pieces = min(units, kSharers);
-        for (int i = rank * blockDim.x + threadIdx.x; i < x.nq * (p.dim / 4); i += kCluster * blockDim.x) {
-            const int n = i / (p.dim / 4), col = (i - n * (p.dim / 4)) * 4;
+        __syncthreads();
+        const int pieces = min(units, kSharers), vectors = x.nq * (p.dim / 4);
+        const int held = pieces > rank ? (pieces - rank + kCluster - 1) / kCluster : 0;   // warps with results
+        for (int i = threadIdx.x; i < vectors; i += blockDim.x) {
+            const int n = i / (p.dim / 4);
             float top = -INFINITY, l = 0.0f;
             float4 o = {0, 0, 0, 0};
-            constexpr int kAhead = 8;
-            for (int base = 0; base < pieces; base += kAhead) {
-                float2 e[kAhead];
-                float4 v[kAhead];
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int w = base + j;   // sharer w: warp w / kCluster of CTA w % kCluster
-                    e[j] = make_float2(-INFINITY, 0.0f);
-                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (w < pieces) {
-                        const float* src = reinterpret_cast<const float*>(smem + (w / kCluster) * kStages * p.stage);
-                        e[j] = *cluster.map_shared_rank(&ml[w / kCluster][n], w % kCluster);
-                        v[j] = *reinterpret_cast<const float4*>(
-                            cluster.map_shared_rank(src + n * p.dim + col, w % kCluster));
-                    }
+            for (int w = 0; w < kWarps; ++w)
+                if (w < held) top = fmaxf(top, ml[w][n].x);
+#pragma unroll 4
+            for (int w = 0; w < held; ++w) {
+                const float2 e = ml[w][n];
+                const float4 v = reinterpret_cast<const float4*>(smem + w * kStages * p.stage)[i];
+                const float f = e.x == -INFINITY ? 0.0f : ex2_4(e.x - top);
+                l += e.y * f;
+                o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+            }
+            reinterpret_cast<float4*>(smem)[i] = o;
+            if (i == n * (p.dim / 4)) joined[n] = make_float2(top, l);
+        }
+        fence_proxy_async_smem();
+        cluster.sync();
+        for (int i = (warp * kCluster + rank) * 32 + lane; i < vectors; i += kCluster * blockDim.x) {
+            const int n = i / (p.dim / 4), col = (i - n * (p.dim / 4)) * 4;
+            float2 e[kCluster];
+            float4 v[kCluster];
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c) {
+                e[c] = make_float2(-INFINITY, 0.0f);
+                v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < pieces) {
+                    e[c] = *cluster.map_shared_rank(&joined[n], c);
+                    v[c] = *cluster.map_shared_rank(reinterpret_cast<const float4*>(smem) + i, c);
                 }
-                float m = top;
+            }
+            float top = e[0].x, l = 0.0f;
+            float4 o = {0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) m = fmaxf(m, e[j].x);
-                const float keep = top == -INFINITY ? 0.0f : ex2_4(top - m);
-                top = m;
-                l *= keep;
-                o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+            for (int c = 1; c < kCluster; ++c) top = fmaxf(top, e[c].x);
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const float f = e[j].x == -INFINITY ? 0.0f : ex2_4(e[j].x - m);
-                    l += e[j].y * f;
-                    o.x += v[j].x * f, o.y += v[j].y * f, o.z += v[j].z * f, o.w += v[j].w * f;
-                }
+            for (int c = 0; c < kCluster; ++c) {
+                const float f = e[c].x == -INFINITY ? 0.0f : ex2_4(e[c].x - top);
+                l += e[c].y * f;
+                o.x += v[c].x * f, o.y += v[c].y * f, o.z += v[c].z * f, o.w += v[c].w * f;
             }
             const float inv = l == 0.0f ? 0.0f : p.v_scale / l;
             const int row = x.row0 + (x.first + n) / p.group, head = kvh * p.group + (x.first + n) % p.group;
