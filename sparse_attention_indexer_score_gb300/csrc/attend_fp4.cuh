@@ -1354,14 +1354,16 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
     }
 }
 
-// Few items with few units: eight CTAs, a cluster, have an item, and its units go round
-// their warps.  What the warps have is joined through the cluster's shared memory, so
-// one launch does it all, and the first page is on its way before the item's length
-// is known.  Bound by latency: one request of 1000 keys, 32 heads over 8, 7.7 us (12.1 by
-// the axis and a join), one row's list of 2048 8.9 (11.2).  Taken where every item gets a
-// cluster at once and a warp at most kClusterUnits units: with more, the axis shares
-// them better and the join is small beside them.
-constexpr int kCluster = 8;
+// Few items with few units: eight CTAs, a cluster, have an item (four where the items
+// are too many for eight), and its units go round their warps.  What the warps have is
+// joined through the cluster's shared memory, so one launch does it all, and the first
+// page is on its way before the item's length is known.  Bound by latency: one request of
+// 1000 keys, 32 heads over 8, 6.9 us as a graph (10.7 by the axis and a join), of 6000 8.6
+// (12.3), one row's list of 2048 7.5 (9.3).  Taken where all clusters run at once, as
+// far as the GPU has room for them (15 of eight CTAs; a second turn took 14.4 us), and a
+// warp has at most kClusterUnits units: with more, the axis shares them better and the
+// join is small beside them.
+constexpr int kCluster = 8;        // CTAs of a cluster at most
 constexpr int kClusterUnits = 4;   // units of a warp at most
 
 template <Form kForm, int kRows, bool kSelected>
@@ -1370,13 +1372,14 @@ attend_fp4_cluster_kernel(const Att4Params p) {
     using S4 = Shape4<kForm, kRows>;
     using W4 = Worker4<kForm, kRows, kSelected>;
     using Desk = Desk4<kForm, kRows, kSelected>;
-    constexpr int kStages = S4::kStages, kWarps = S4::kWarps, kSharers = kWarps * kCluster;
+    constexpr int kStages = S4::kStages, kWarps = S4::kWarps;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 ml[kWarps][kRows], joined[kRows];   // references and sums of the warps, of the CTA
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = cluster.block_rank(), item = blockIdx.x / kCluster;
+    const int rank = cluster.block_rank(), ctas = cluster.num_blocks(), item = blockIdx.x / ctas;
+    const int sharers = kWarps * ctas;
     pdl_wait();
     pdl_launch_dependents();
     uint8_t* const ring = smem + warp * kStages * p.stage;
@@ -1388,9 +1391,9 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         desk.abort = 0;
     }
     __syncwarp();
-    const int sharer = warp * kCluster + rank;   // (an item's first units are on different SMs)
+    const int sharer = warp * ctas + rank;   // (an item's first units are on different SMs)
 
-    // The item, and its units: those of this warp are sharer, sharer + kSharers, ...
+    // The item, and its units: those of this warp are sharer, sharer + sharers, ...
     int row0 = 0, all = 0, kvh, units = 0, req = -1, bound = 0;
     bool bad = false;
     int first_page = -1, first_pos[2] = {-1, -1};   // the first unit's page, its positions
@@ -1456,7 +1459,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
     }
     if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
 
-    const int count = sharer < units ? (units - sharer + kSharers - 1) / kSharers : 0;
+    const int count = sharer < units ? (units - sharer + sharers - 1) / sharers : 0;
     const int tiles = kSelected ? 1 : (all + p.cap - 1) / p.cap;
     int pos[2], page[2];
     auto copy = [&](int tile, int i) {   // unit i of the warp into its stage
@@ -1464,7 +1467,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         if constexpr (kSelected) {
             if (i < count) {
                 const int32_t* list = p.topk + row0 * p.topk_stride;
-                const int from = (sharer + i * kSharers) * kUnit + lane;
+                const int from = (sharer + i * sharers) * kUnit + lane;
                 bool past = false;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -1479,7 +1482,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
             }
             cp_async_commit();
         } else if (lane == 0 && i < count && !(tile == 0 && i == 0 && first_page >= 0)) {
-            const int at = p.bt[req * p.bt_stride + sharer + i * kSharers];
+            const int at = p.bt[req * p.bt_stride + sharer + i * sharers];
             const bool ok = at >= 0 && at < p.num_pages;
             desk.listed[i % kStages] = ok;
             if (ok) {
@@ -1530,7 +1533,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
                 }
             }
             const uint64_t listed = desk.listed[i % kStages];
-            const int first = (sharer + i * kSharers) * kUnit;
+            const int first = (sharer + i * sharers) * kUnit;
             if (listed != 0 && (kSelected || first < k.most)) k.unit(stage, first, listed);
             __syncwarp();
             copy(tile, i + kStages);
@@ -1545,8 +1548,8 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         if (x.nq > 0 && count > 0) k.finish(reinterpret_cast<float*>(ring), ml[warp]);
         fence_proxy_async_smem();   // (the next tile's copies take the results' place)
         __syncthreads();
-        const int pieces = min(units, kSharers), vectors = x.nq * (p.dim / 4);
-        const int held = pieces > rank ? (pieces - rank + kCluster - 1) / kCluster : 0;   // warps with results
+        const int pieces = min(units, sharers), vectors = x.nq * (p.dim / 4);
+        const int held = pieces > rank ? (pieces - rank + ctas - 1) / ctas : 0;   // warps with results
         for (int i = threadIdx.x; i < vectors; i += blockDim.x) {
             const int n = i / (p.dim / 4);
             float top = -INFINITY, l = 0.0f;
@@ -1567,7 +1570,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         }
         fence_proxy_async_smem();
         cluster.sync();
-        for (int i = (warp * kCluster + rank) * 32 + lane; i < vectors; i += kCluster * blockDim.x) {
+        for (int i = (warp * ctas + rank) * 32 + lane; i < vectors; i += ctas * blockDim.x) {
             const int n = i / (p.dim / 4), col = (i - n * (p.dim / 4)) * 4;
             float2 e[kCluster];
             float4 v[kCluster];
@@ -1575,7 +1578,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
             for (int c = 0; c < kCluster; ++c) {
                 e[c] = make_float2(-INFINITY, 0.0f);
                 v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (c < pieces) {
+                if (c < min(pieces, ctas)) {
                     e[c] = *cluster.map_shared_rank(&joined[n], c);
                     v[c] = *cluster.map_shared_rank(reinterpret_cast<const float4*>(smem) + i, c);
                 }
@@ -1794,11 +1797,13 @@ static int launch_attend4(Att4Params& p, int ctas, cudaStream_t stream) {
                                                                                                : DSA_ERR_CUDA;
 }
 
+// Returns DSA_ERR_UNSUPPORTED, with nothing launched, where the GPU has no room for `items` clusters at once.
 template <Form kForm, int kRows, bool kSelected>
-static int launch_cluster4(Att4Params& p, int items, cudaStream_t stream) {
+static int launch_cluster4(Att4Params& p, int items, int sms, int most_units, cudaStream_t stream) {
     using S4 = Shape4<kForm, kRows>;
     auto* kernel = attend_fp4_cluster_kernel<kForm, kRows, kSelected>;
     static bool attr_set[64] = {false};
+    static int room[64][2] = {};   // clusters of 8 and of 4 CTAs that run at once, and one
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
     if (!attr_set[dev]) {
@@ -1807,28 +1812,40 @@ static int launch_cluster4(Att4Params& p, int items, cudaStream_t stream) {
         attr_set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(items * kCluster);
     cfg.blockDim = dim3(S4::kWarps * 32);
     cfg.dynamicSmemBytes =
         S4::kWarps * (S4::kStages * p.stage + static_cast<int>(sizeof(Desk4<kForm, kRows, kSelected>)));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kCluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    for (int i = 0; i < 2; ++i) {
+        const int ctas = kCluster >> i;
+        if (items * ctas > sms || most_units > S4::kWarps * ctas * kClusterUnits) continue;
+        cfg.gridDim = dim3(items * ctas);
+        attr[0].val.clusterDim.x = ctas;
+        if (room[dev][i] == 0) {
+            int n = 0;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return DSA_ERR_CUDA;
+            room[dev][i] = n + 1;
+        }
+        if (items >= room[dev][i]) continue;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    }
+    return DSA_ERR_UNSUPPORTED;
 }
 
 template <bool kSelected, int kRows>
-static int launch_cluster_form4(Att4Params& p, int items, cudaStream_t stream) {
-    return p.dim == 128  ? launch_cluster4<kForm128, kRows, kSelected>(p, items, stream)
-           : p.dim == 64 ? launch_cluster4<kForm64, kRows, kSelected>(p, items, stream)
-           : p.dim > 64  ? launch_cluster4<kFormAny128, kRows, kSelected>(p, items, stream)
-                         : launch_cluster4<kFormAny64, kRows, kSelected>(p, items, stream);
+static int launch_cluster_form4(Att4Params& p, int items, int sms, int most_units, cudaStream_t stream) {
+    return p.dim == 128  ? launch_cluster4<kForm128, kRows, kSelected>(p, items, sms, most_units, stream)
+           : p.dim == 64 ? launch_cluster4<kForm64, kRows, kSelected>(p, items, sms, most_units, stream)
+           : p.dim > 64  ? launch_cluster4<kFormAny128, kRows, kSelected>(p, items, sms, most_units, stream)
+                         : launch_cluster4<kFormAny64, kRows, kSelected>(p, items, sms, most_units, stream);
 }
 
 template <bool kSelected, int kRows>
@@ -1843,16 +1860,17 @@ template <bool kSelected>
 static int launch_all4(Att4Params& p, cudaStream_t stream) {
     int ctas = device_sm_count();
     if (ctas > kMaxCtas4) ctas = kMaxCtas4;
-    // A cluster an item, where there are few and their units few.
+    // A cluster an item, where there are few and their units few, and a request has a row tile or hardly more.
     const int64_t items_all = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles
                                         : static_cast<int64_t>(p.R) * p.kv_heads;
     const int most_units = kSelected ? p.list_units : p.max_keys / kUnit;
-    if (items_all > 0 && items_all * kCluster <= ctas && most_units <= 8 * kCluster * kClusterUnits &&
-        (kSelected || static_cast<int64_t>(p.rows) * p.group <= 2 * p.cap)) {
+    if (items_all > 0 && items_all * (kCluster / 2) <= ctas &&
+        (kSelected || static_cast<int64_t>(p.rows) * p.group <= static_cast<int64_t>(p.R + 1) * p.cap)) {
         const int n = static_cast<int>(items_all);
-        return p.cap <= 8    ? launch_cluster_form4<kSelected, 8>(p, n, stream)
-               : p.cap <= 16 ? launch_cluster_form4<kSelected, 16>(p, n, stream)
-                             : launch_cluster_form4<kSelected, 32>(p, n, stream);
+        const int rc = p.cap <= 8    ? launch_cluster_form4<kSelected, 8>(p, n, ctas, most_units, stream)
+                       : p.cap <= 16 ? launch_cluster_form4<kSelected, 16>(p, n, ctas, most_units, stream)
+                                     : launch_cluster_form4<kSelected, 32>(p, n, ctas, most_units, stream);
+        if (rc != DSA_ERR_UNSUPPORTED) return rc;
     }
     const bool wide_head = p.dim > 64;
     p.warps = ctas * (p.cap <= 8    ? Shape4<kForm128, 8>::kWarps
