@@ -1354,15 +1354,16 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
     }
 }
 
-// Few items with few units: eight CTAs, a cluster, have an item (four where the items
-// are too many for eight), and its units go round their warps.  What the warps have is
-// joined through the cluster's shared memory, so one launch does it all, and the first
-// page is on its way before the item's length is known.  Bound by latency: one request of
-// 1000 keys, 32 heads over 8, 6.9 us as a graph (10.7 by the axis and a join), of 6000 8.6
-// (12.3), one row's list of 2048 7.5 (9.3).  Taken where all clusters run at once, as
-// far as the GPU has room for them (15 of eight CTAs; a second turn took 14.4 us), and a
-// warp has at most kClusterUnits units: with more, the axis shares them better and the
-// join is small beside them.
+// Few items with few units: eight CTAs, a cluster, have an item (four, two or one where
+// the items are too many for more), and its units go round their warps.  What the warps
+// have is joined through the cluster's shared memory, so one launch does it all, and the
+// first page is on its way before the item's length is known.  Bound by latency (as
+// graphs, and by the axis and a join; 32 heads over 8): one request of 1000 keys 7.0 and
+// 10.9 us, of 6000 8.7 and 12.6, 9 of 1000 7.8 and 12.5, 19 of 3000 16.8 and 23.5, lists of
+// 2048 for one row 7.5 and 10.5, for 19 rows 16.8 and 24.4.  Taken where all clusters run
+// at once, as far as the GPU has room for them (15 of eight CTAs; a second turn took 14.4
+// us for 8.5 with four), and a warp has at most kClusterUnits units: there the two meet (10
+// requests of 6000 keys 24.8 and 24.6, 4 of 12000 16.9 and 20.1), past it the axis shares them better.
 constexpr int kCluster = 8;        // CTAs of a cluster at most
 constexpr int kClusterUnits = 4;   // units of a warp at most
 
@@ -1803,7 +1804,7 @@ static int launch_cluster4(Att4Params& p, int items, int sms, int most_units, cu
     using S4 = Shape4<kForm, kRows>;
     auto* kernel = attend_fp4_cluster_kernel<kForm, kRows, kSelected>;
     static bool attr_set[64] = {false};
-    static int room[64][2] = {};   // clusters of 8 and of 4 CTAs that run at once, and one
+    static int room[64][4] = {};   // clusters of 8, 4, 2 CTAs and CTAs that run at once, and one
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
     if (!attr_set[dev]) {
@@ -1822,7 +1823,7 @@ static int launch_cluster4(Att4Params& p, int items, int sms, int most_units, cu
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const int ctas = kCluster >> i;
         if (items * ctas > sms || most_units > S4::kWarps * ctas * kClusterUnits) continue;
         cfg.gridDim = dim3(items * ctas);
@@ -1864,7 +1865,7 @@ static int launch_all4(Att4Params& p, cudaStream_t stream) {
     const int64_t items_all = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles
                                         : static_cast<int64_t>(p.R) * p.kv_heads;
     const int most_units = kSelected ? p.list_units : p.max_keys / kUnit;
-    if (items_all > 0 && items_all * (kCluster / 2) <= ctas &&
+    if (items_all > 0 && items_all <= ctas &&
         (kSelected || static_cast<int64_t>(p.rows) * p.group <= static_cast<int64_t>(p.R + 1) * p.cap)) {
         const int n = static_cast<int>(items_all);
         const int rc = p.cap <= 8    ? launch_cluster_form4<kSelected, 8>(p, n, ctas, most_units, stream)
