@@ -125,7 +125,7 @@ def _link_binding(obj: str) -> None:
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libdsa.so", f"-L{torch_lib}", "-ltorch_python",
-          "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of the binding")
+          "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of the binding")
     os.replace(tmp, BINDING)
 
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -138,8 +139,14 @@ const at::Tensor& list_of(PyObject* o, const at::Device& device, at::ScalarType 
 }
 
 // The caller's output tensor, or a new one like q.
+// A new contiguous tensor, past the dispatcher where it is a GPU's (the short calls' time is the host's).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Device& device) {
+    if (device.is_cuda()) return at::detail::empty_cuda(sizes, type, device, std::nullopt);
+    return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+}
+
 at::Tensor output(PyObject* o, const at::Tensor& q, const char* what) {
-    if (!given(o)) return at::empty(q.sizes(), q.options());
+    if (!given(o)) return fresh(q.sizes(), q.scalar_type(), q.device());
     const at::Tensor& t = tensor(o, q.device(), what);
     need(t.scalar_type() == q.scalar_type() && t.sizes() == q.sizes() && t.stride(2) == 1, what);
     return t;
@@ -411,7 +418,7 @@ PyObject* kv_read_fp4(PyObject* const* a) {
             out[i] = half_rows(a[6 + i], cache, type, what);
             need(out[i].size(0) == n && out[i].size(1) == cache.c.heads, what);
         } else {
-            out[i] = at::empty({n, cache.c.heads, cache.c.dim}, at::TensorOptions().dtype(type).device(cache.device));
+            out[i] = fresh({n, cache.c.heads, cache.c.dim}, type, cache.device);
         }
     }
     const OnDevice on(cache.device);
@@ -459,7 +466,7 @@ struct Attention4 {
                                : static_cast<float>(1.0 / std::sqrt(static_cast<double>(cache.c.dim)));
         out = output(out_o, q, "out must match q");
         if (truth(want_lse)) {
-            lse = at::empty({rows, heads}, q.options().dtype(at::kFloat));
+            lse = fresh({rows, heads}, at::kFloat, cache.device);
             lse_ptr = static_cast<float*>(pointer(lse));
         }
     }
