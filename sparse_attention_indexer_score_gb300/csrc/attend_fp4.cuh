@@ -23,8 +23,8 @@
 // a cycle on one SM); the matrix products of 8 rows hide behind that, 16 rows bring a
 // unit to 435 cycles, 32 to 670.  Measured: 413, 653 and 712 cycles.  So up to 8 rows
 // the memory bounds (64 requests of 4096 to 8192 keys, 32 heads over 8: 82 us, 82 % of
-// the copy rate with 5 us until the first unit), past them the pipes (128 requests of 4
-// rows, 64 heads over 8, 64 to 8192 keys: 243 us, 11 of them the join).
+// the copy rate with 5 us until the first unit), past them the pipes (128 requests of 1
+// to 4 rows, 64 heads over 8, 64 to 8192 keys: 243 us, 11 of them the join).
 //
 // tcgen05 was built for 9 to 32 rows and taken back: operands made by some warps and put
 // into tensor memory, products issued by another, the softmax in four more.  It was right
@@ -1609,7 +1609,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
 // ----------------------------------------------------------------- join
 // Joins the pieces of a (row, head), and writes the rows that no unit reached:
 // kWarps warps take every kWarps-th piece, four columns a lane.  Bound by the pieces'
-// way through L2 and by its launch: 5 us behind 64 rows of 32 heads, 11 behind 512 of 64.
+// way through L2 and by its launch: 5 us behind 64 rows of 32 heads, 11 behind 320 of 64.
 // A warp by itself takes kHeads neighbouring heads of a row, which lie in one tile.
 template <int kWarps, int kHeads, bool kSelected>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) attend_fp4_join_kernel(const Att4Params p) {
