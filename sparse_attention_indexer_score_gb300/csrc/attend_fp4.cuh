@@ -1438,16 +1438,18 @@ attend_fp4_cluster_kernel(const Att4Params p) {
         units = (most + kUnit - 1) / kUnit;
     }
     // what the geometry says wrong, and rows outside every request (a warp that has units last, or none)
-    if (blockIdx.x == 0 && warp == kWarps - 1) {
-        for (int j = lane; j <= p.R; j += 32) {
-            const int a = p.starts[j];
-            bad |= a < 0 || (j > 0 && a < p.starts[j - 1]) || a > p.rows;
-        }
+    if (warp == kWarps - 1) {
+        if (blockIdx.x == 0)
+            for (int j = lane; j <= p.R; j += 32) {
+                const int a = p.starts[j];
+                bad |= a < 0 || (j > 0 && a < p.starts[j - 1]) || a > p.rows;
+            }
         if (!kSelected)
-            for (int base = 0; base < p.rows; base += 32) {
-                bool mine = base + lane >= p.rows;
-                for (int j = 0; j < p.R; ++j) mine |= p.starts[j] <= base + lane && base + lane < p.starts[j + 1];
-                for (uint32_t others = ~__ballot_sync(0xFFFFFFFFu, mine); others; others &= others - 1) {
+            for (int base = blockIdx.x * 32; base < p.rows; base += gridDim.x * 32) {
+                const int j = last_at_most(p.starts, p.R, base + lane);
+                const bool mine = p.starts[j] <= base + lane && base + lane < p.starts[j + 1];
+                for (uint32_t others = __ballot_sync(0xFFFFFFFFu, !mine && base + lane < p.rows); others;
+                     others &= others - 1) {
                     const int r = base + __ffs(others) - 1;
                     for (int i = lane; i < p.heads * (p.dim / 8); i += 32) {
                         const int head = i / (p.dim / 8), col = i - head * (p.dim / 8);

@@ -300,15 +300,17 @@ def test_captured_and_on_another_stream(cuda_lib):
     ([1000], [1], 32, 8, 128), ([64 * 90], [4], 16, 4, 128), ([64 * 100 + 1], [2], 8, 2, 64), ([0, 5, 130], [1, 2, 1], 8, 2, 96),
     ([20000], [1], 4, 1, 128), ([24576], [2], 30, 1, 80), ([700, 0], [3, 0], 24, 2, 128), ([300, 300], [1, 1], 128, 2, 48),
     ([100 + 170 * j for j in range(5)], [1, 4, 2, 1, 3], 24, 6, 128), ([130 + 40 * j for j in range(9)], [1] * 9, 32, 8, 128),
-    ([64 * (j % 9) for j in range(19)], [1 + j % 2 for j in range(19)], 16, 8, 64), ([777] * 37, [2] * 37, 16, 1, 112)])
+    ([64 * (j % 9) for j in range(19)], [1 + j % 2 for j in range(19)], 16, 8, 64), ([777] * 37, [2] * 37, 16, 1, 112),
+    ([40 + j % 7 for j in range(120)], [31] * 120, 1, 1, 16)])
 def test_few_items(cuda_lib, lens, qlens, hq, hkv, dim):
     """Batches small enough for a cluster an item (and, by a hint that is too small, their row tiles in turn)."""
     c = Case(lens, qlens, hq=hq, hkv=hkv, dim=dim, pad_rows=2)
+    rows = range(0, c.q.shape[0], 1 + c.q.shape[0] // 400)
     for hint in (c.qlen, 1):
-        c.check(c.paged(cuda_lib, max_query_len=hint))
+        c.check(c.paged(cuda_lib, max_query_len=hint), rows=rows)
     for k in (3, 2048):
         topk = choose(c, k, seed=k)
-        c.check(c.selected(cuda_lib, topk), topk)
+        c.check(c.selected(cuda_lib, topk), topk, rows=rows)
 
 
 def test_few_items_and_many_agree(cuda_lib):
