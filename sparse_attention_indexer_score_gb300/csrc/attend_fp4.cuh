@@ -599,6 +599,7 @@ struct Base4 {
                 }
             }
         }
+        __syncwarp();   // (all have read the places before the next unit's are written over them)
     }
 
     // The (row, head) pair n of the item's tile.
