@@ -64,7 +64,9 @@ constexpr float kLn2_4 = 0.6931471805599453f;
 // Weights are kept times 2^6: FP16 then holds them from 2^-30 of the largest on.
 constexpr float kLift = 6.0f;
 // ... and a row's reference is raised when a score passes it by 2^8, which leaves
-// them below 2^14; until then what there is needs no rescaling.
+// them below 2^14 (the score's limit is rounded down: where a step of FP32 is several
+// powers of two, up would let a weight pass FP16); until then what there is needs no
+// rescaling.
 constexpr float kSlack4 = 8.0f;
 
 // Where the join finds a row's pieces.
@@ -840,7 +842,7 @@ struct Few4 : Base4<kForm, 8, kSelected> {
                 if (top[e] > limit[e]) {
                     const float keep = limit[e] == -INFINITY ? 0.0f : ex2_4((ref[e] - top[e]) * c[e]);
                     ref[e] = top[e];
-                    limit[e] = top[e] + kSlack4 / c[e];
+                    limit[e] = __fadd_rd(top[e], kSlack4 / c[e]);
                     l[e] *= keep;
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i) o[i][e] *= keep, o[i][e + 2] *= keep;
@@ -1025,7 +1027,7 @@ struct Many4 : Base4<kForm, kRows, kSelected> {
                             const float keep =
                                 limit[r][h] == -INFINITY ? 0.0f : ex2_4((ref[r][h] - top[r][h]) * c[r][h]);
                             ref[r][h] = top[r][h];
-                            limit[r][h] = top[r][h] + kSlack4 / c[r][h];
+                            limit[r][h] = __fadd_rd(top[r][h], kSlack4 / c[r][h]);
                             l[r][h] *= keep;
 #pragma unroll
                             for (int i = 0; i < kOT; ++i) o[i][r][2 * h] *= keep, o[i][r][2 * h + 1] *= keep;
