@@ -7,9 +7,12 @@
 // Argument errors raise ValueError here or RuntimeError with the C ABI's code.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -138,13 +141,17 @@ const at::Tensor& list_of(PyObject* o, const at::Device& device, at::ScalarType 
     return t;
 }
 
-// The caller's output tensor, or a new one like q.
-// A new contiguous tensor, past the dispatcher where it is a GPU's (the short calls' time is the host's).
+// A new contiguous tensor.  On a GPU past the dispatcher (the short calls' time is the host's),
+// unless something listens there (dispatch modes, tracers, function transforms, profilers) or new memory is to be
+// filled.
 at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Device& device) {
-    if (device.is_cuda()) return at::detail::empty_cuda(sizes, type, device, std::nullopt);
+    const c10::DispatchKeySet heard = c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set;
+    if (device.is_cuda() && heard.empty() && !at::hasCallbacks() && !at::globalContext().deterministicAlgorithms())
+        return at::detail::empty_cuda(sizes, type, device, std::nullopt);
     return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
 }
 
+// The caller's output tensor, or a new one like q.
 at::Tensor output(PyObject* o, const at::Tensor& q, const char* what) {
     if (!given(o)) return fresh(q.sizes(), q.scalar_type(), q.device());
     const at::Tensor& t = tensor(o, q.device(), what);
