@@ -86,6 +86,7 @@ struct Att4Layout {
     size_t po, pml;         // float[slots][cap][dim], float2[slots][cap]: partial results
     size_t total;
     int cap;                // query rows of a tile, and of a slot
+    int tiles;              // row tiles of the longest request, as far as max_query_len tells
 };
 
 // The requests on the axis: where each starts, units before it, and pages an item of it has.
@@ -1369,6 +1370,12 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
 // requests of 6000 keys 24.8 and 24.6, 4 of 12000 16.9 and 20.1), past it the axis shares them better.
 constexpr int kCluster = 8;        // CTAs of a cluster at most
 constexpr int kClusterUnits = 4;   // units of a warp at most
+// A request's row tiles take turns in its cluster, 11 to 25 us each, while the axis spreads
+// them: the longest request that max_query_len allows has this many at most (30 requests of
+// 1000 keys, 16 heads over 1, a row each 11.2 us and by the axis 17.5, one of them with two
+// tiles 26.2 and 19.0, with three 38.6 and 19.0; 63 of 4096 keys with a row each beside one of
+// 67 rows 990 and 50).
+constexpr int kClusterTiles = 2;
 
 template <Form kForm, int kRows, bool kSelected>
 __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1)
@@ -1734,6 +1741,7 @@ static Att4Layout attend4_layout(int64_t rows, int64_t num_requests, int64_t hea
     int64_t each = k > 0 ? 1 : max_query_len < rows ? max_query_len : rows;   // rows that share keys
     if (each < 1) each = 1;
     L.cap = static_cast<int>(group * each < 32 ? group * each : 32);
+    L.tiles = k > 0 ? 1 : static_cast<int>((group * each + L.cap - 1) / L.cap);
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;
@@ -1863,14 +1871,15 @@ static int launch_form4(Att4Params& p, int ctas, cudaStream_t stream) {
 }
 
 template <bool kSelected>
-static int launch_all4(Att4Params& p, cudaStream_t stream) {
+static int launch_all4(Att4Params& p, int most_tiles, cudaStream_t stream) {
     int ctas = device_sm_count();
     if (ctas > kMaxCtas4) ctas = kMaxCtas4;
-    // A cluster an item, where there are few and their units few, and a request has a row tile or hardly more.
+    // A cluster an item, where there are few and their units few, and a request has a row tile or hardly more, on
+    // average and at most.
     const int64_t items_all = kSelected ? static_cast<int64_t>(p.rows) * p.kv_heads * p.list_tiles
                                         : static_cast<int64_t>(p.R) * p.kv_heads;
     const int most_units = kSelected ? p.list_units : p.max_keys / kUnit;
-    if (items_all > 0 && items_all <= ctas &&
+    if (items_all > 0 && items_all <= ctas && most_tiles <= kClusterTiles &&
         (kSelected || static_cast<int64_t>(p.rows) * p.group <= static_cast<int64_t>(p.R + 1) * p.cap)) {
         const int n = static_cast<int>(items_all);
         const int rc = p.cap <= 8    ? launch_cluster_form4<kSelected, 8>(p, n, ctas, most_units, stream)

@@ -41,5 +41,5 @@ extern "C" int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype
     // rows 260 us against 247, 150 of 64 to 4096 under 16 rows 121 against 108, 200 under 8 rows 108 against 100.
     p.axis.light = 5, p.axis.heavy = p.cap > 16 ? 7 : 5, p.axis.start = p.cap > 16 ? 13 : 10;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return launch_all4<false>(p, stream);
+    return launch_all4<false>(p, L.tiles, stream);
 }

@@ -36,5 +36,5 @@ extern "C" int dsa_attend_selected_fp4(const dsa_kv_cache_fp4* cache, int32_t dt
     if (per_row > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
     p.packed = cache->num_pages <= (1 << 25) && per_row * rows * p.section >= kPackBytes;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return launch_all4<true>(p, stream);
+    return launch_all4<true>(p, L.tiles, stream);
 }
