@@ -36,6 +36,8 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "elem16.cuh"
 #include "fp4_cache.cuh"
 #include "host.h"
@@ -1817,7 +1819,9 @@ static int launch_cluster4(Att4Params& p, int items, int sms, int most_units, cu
     using S4 = Shape4<kForm, kRows>;
     auto* kernel = attend_fp4_cluster_kernel<kForm, kRows, kSelected>;
     static bool attr_set[64] = {false};
-    static int room[64][4] = {};   // clusters of 8, 4, 2 CTAs and CTAs that run at once, and one
+    // Clusters of 8, 4, 2 CTAs and CTAs that run at once, and one, for heads of 16, 32, ... columns (what they keep in
+    // shared memory differs); host threads may come at the same time and find the same.
+    static std::atomic<int> room[64][kFp4MaxDim / 16][4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
     if (!attr_set[dev]) {
@@ -1841,13 +1845,14 @@ static int launch_cluster4(Att4Params& p, int items, int sms, int most_units, cu
         if (items * ctas > sms || most_units > S4::kWarps * ctas * kClusterUnits) continue;
         cfg.gridDim = dim3(items * ctas);
         attr[0].val.clusterDim.x = ctas;
-        if (room[dev][i] == 0) {
-            int n = 0;
+        std::atomic<int>& known = room[dev][p.dim / 16 - 1][i];
+        int n = known.load(std::memory_order_relaxed) - 1;
+        if (n < 0) {
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return DSA_ERR_CUDA;
-            room[dev][i] = n + 1;
+            known.store(n + 1, std::memory_order_relaxed);
         }
-        if (items >= room[dev][i]) continue;
+        if (items > n) continue;
         cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
     }
