@@ -688,8 +688,16 @@ size_t dsa_attend_workspace_size_fp4(int64_t rows, int64_t num_requests, int64_t
  * sums are FP32.
  * Keys a row may not see do not reach its output.  A visible scale that is NaN
  * makes what it enters NaN: a key's the whole row, a value's its 16 output columns.
- * Queries are finite (else the rows of the tile's head are unspecified).  Keys of
- * a page outside the pool are skipped (DSA_STATUS_BAD_PAGE).
+ * Queries are finite (else the rows of the tile's head are unspecified), and scores
+ * (scale q . k log2(e)) within FP32's range.  Keys of a page outside the pool are
+ * skipped (DSA_STATUS_BAD_PAGE).
+ *
+ * What the host knows chooses the kernels, for speed alone.  max_query_len is best the
+ * largest row count of this call: one above it takes higher row tiles than the rows
+ * fill, and one that allows more than 64 rows by query heads of a key head takes two
+ * launches for small batches too; one below it may leave a long request to few SMs.
+ * Small batches run in one launch where max_pages stays below some hundred pages (384
+ * for one request of up to 8 rows by heads), so a table is best cut to the longest request.
  */
 int dsa_attend_paged_fp4(const dsa_kv_cache_fp4* cache, int32_t dtype, const void* q, int64_t q_row_stride,
                          int64_t q_head_stride, int64_t heads, const int32_t* block_table, int64_t bt_stride,

@@ -102,7 +102,9 @@ class DecodeAttention:
                    positions: torch.Tensor, starts: torch.Tensor, row_ends: torch.Tensor,
                    prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0) -> torch.Tensor:
         """Append, then attention over the shared prefix (16-bit caches; requests of a 4-bit cache list its pages in
-        their own tables) and all own keys below ``row_ends``."""
+        their own tables) and all own keys below ``row_ends``.  The layer's ``max_query_len`` and the block table's
+        width go into the call as they are: a 4-bit layer of short requests is faster with both no larger than it
+        needs."""
         if self.kv_format is not None:
             if prefix_len != 0:
                 raise ValueError("a shared prefix is read from a 16-bit cache only")

@@ -23,14 +23,18 @@
 // a cycle on one SM); the matrix products of 8 rows hide behind that, 16 rows bring a
 // unit to 435 cycles, 32 to 670.  Measured: 413, 653 and 712 cycles.  So up to 8 rows
 // the memory bounds (64 requests of 4096 to 8192 keys, 32 heads over 8: 82 us, 82 % of
-// the copy rate with 5 us until the first unit), past them the pipes (128 requests of 1
-// to 4 rows, 64 heads over 8, 64 to 8192 keys: 243 us, 11 of them the join).
+// the copy rate with 5 us until the first unit), under 32 the pipes, the matrix products
+// alone with 512 cycles (128 requests of 1 to 4 rows, 64 heads over 8, 64 to 8192 keys: 243
+// us, 11 of them the join).  Under 16 rows no pipe that was counted is active more than 31 % of
+// the time, and what the 218 cycles past the count go into is not known (8 x 131071 keys,
+// 16 heads over 1: 50 us).
 //
-// tcgen05 was built for 9 to 32 rows and taken back: operands made by some warps and put
+// tcgen05 was tried for 9 to 32 rows and not kept: operands made by some warps and put
 // into tensor memory, products issued by another, the softmax in four more.  It was right
-// and slower (8 x 131071 keys under 16 rows 95 us against 52, the 128 requests 555
-// against 257): 1190 instructions an SMSP for 128 keys, as many cycles as mma.sync
-// takes altogether, at 37 % issue.  The conversions are what costs, and they are the same.
+// and slower as far as it got (8 x 131071 keys under 16 rows 95 us against 52, the 128
+// requests 555 against 257): 1190 instructions an SMSP for 128 keys at 37 % issue, most
+// stalls for instructions to be fetched.  That is no bound of the form; the codes'
+// conversions are the same in both.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -60,6 +64,10 @@ constexpr int kBitmapKeys = 1 << 20;    // positions that a list is put in order
 // Listed sections' bytes from which lists are put in order first (a launch, 6 to 7 us).
 // Lists of 2048 of 4096 to 8192 positions, 8 heads, in order and not: 18 MB 28.3 and
 // 25.2 us, 36 MB 36.5 and 37.5, 72 MB 48.8 and 57, 144 MB 66 and 91, 576 MB 163 and 303.
+// The rule does not know how dense a list is, and sparse ones gain less: 151 MB of lists of
+// 2048 of 8192 positions 52 and 76, of 32768 69 and 84, of 131072 88 and 88; 75 MB of 8192
+// 37 and 42, of 65536 50 and 49, of 131072 56 and 50.  Nor do lists of four rows a request
+// that share its keys, 59 MB of 2000 of 8192 positions and 4 heads of 64: 38 and 31.
 constexpr int64_t kPackBytes = 32 << 20;
 constexpr float kLog2e4 = 1.4426950408889634f;
 constexpr float kLn2_4 = 0.6931471805599453f;
@@ -1370,6 +1378,8 @@ __global__ void __launch_bounds__((Shape4<kForm, kRows>::kWarps * 32), 1) attend
 // at once, as far as the GPU has room for them (15 of eight CTAs; a second turn took 14.4
 // us for 8.5 with four), and a warp has at most kClusterUnits units: there the two meet (10
 // requests of 6000 keys 24.8 and 24.6, 4 of 12000 16.9 and 20.1), past it the axis shares them better.
+// Lengths are on the device, so the units are those of the block table's width (or of the
+// list): under a table of 2048 pages one request of 1000 keys takes the axis, 10.9 us for 6.9.
 constexpr int kCluster = 8;        // CTAs of a cluster at most
 constexpr int kClusterUnits = 4;   // units of a warp at most
 // A request's row tiles take turns in its cluster, 11 to 25 us each, while the axis spreads
@@ -1778,11 +1788,11 @@ static int check_attend4(const dsa_kv_cache_fp4* cache, int32_t dtype, const voi
     if (dtype != DSA_BF16 && dtype != DSA_FP16) return DSA_ERR_UNSUPPORTED;
     if (heads < 1 || rows < 0 || num_requests < 0 || max_pages < 0) return DSA_ERR_INVALID;
     if (heads % cache->heads) return DSA_ERR_INVALID;
+    // (rows by heads, and so a request's items, key heads by row tiles, are counted in 31 bits)
     if (!sizes4_ok(rows, num_requests, heads, cache->heads, cache->dim) || rows * heads > 0x7FFFFFFF)
         return DSA_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !isfinite(scale)) return DSA_ERR_INVALID;
     if (rows == 0) return DSA_OK;
-    // (an item's number in its request is counted in 31 bits: key heads by row tiles of 32, at least 4 rows of heads)
     if (max_pages > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
     if (!q || !out || !row_ends || !starts || !workspace) return DSA_ERR_INVALID;
     if (max_pages > 0 && num_requests > 0 && (!block_table || bt_stride < max_pages)) return DSA_ERR_INVALID;

@@ -5,7 +5,7 @@
 // E2M1(x / (s g)); a code c reads as (c s) g.  Both kernels move 16-bit elements
 // once on one side and 9/16 of a byte an element on the other and are bound by
 // memory: 16384 tokens of 32 query and 2 x 8 cache heads of 128 columns, appended and
-// read back, take 84 us (79 % of the copy rate), 65536 tokens of 2 x 8 heads read back 61
+// read back, take 79 us (84 % of the copy rate), 65536 tokens of 2 x 8 heads read back 61
 // (83 %).  Few tokens are bound by the launch and two loads that depend on each other.
 #include <math.h>
 
@@ -96,7 +96,9 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float six) {
 // an element: q0 = x inv(d) with the correctly rounded reciprocal, its remainder
 // (negated, so that the quotient of -0 stays -0) exactly by a fused multiply-add, one
 // correction (Markstein).  Under the largest scale |x| is first cut to 8 d, past the
-// largest code, so that nothing overflows; under the others |x| is not above 7 d.
+// largest code, so that nothing overflows; under the others |x| is not above 9 d (the
+// smallest scale stands for up to one and a half of itself), and what is past the
+// largest code becomes it.
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale_byte, float g) {
     const float d = __fmul_rn(half2_float2(e4m3x2_f16(scale_byte)).x, g);
     uint32_t w = 0;
