@@ -1484,7 +1484,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
     }
     if (bad && p.status) atomicOr(p.status, DSA_STATUS_BAD_GEOMETRY);
 
-    const int count = sharer < units ? (units - sharer + sharers - 1) / sharers : 0;
+    int count = sharer < units ? (units - sharer + sharers - 1) / sharers : 0;
     const int tiles = kSelected ? 1 : (all + p.cap - 1) / p.cap;
     int pos[2], page[2];
     auto copy = [&](int tile, int i) {   // unit i of the warp into its stage
@@ -1554,6 +1554,7 @@ attend_fp4_cluster_kernel(const Att4Params p) {
                             if (j % kStages == s) parity = (turns[s] - (j == i)) & 1;
                         mbar_drain(&desk.full[j % kStages], parity, deadline, p.status);
                     }
+                    count = 0;   // (no more copies: those of a later tile would have other parities than `turns`)
                     break;
                 }
             }
@@ -1565,7 +1566,8 @@ attend_fp4_cluster_kernel(const Att4Params p) {
             __syncwarp();
         }
         if (kSelected) cp_async_wait<0>();
-        if (!kSelected && tile == 0 && count == 0 && lane == 0 && first_page >= 0)   // the copy that was not needed
+        // (the copy that was not needed)
+        if (!kSelected && tile == 0 && sharer >= units && lane == 0 && first_page >= 0)
             mbar_drain(&desk.full[0], 0, globaltimer() + kWaitLimitNs, p.status);
         __syncwarp();
         // The warp's results take the place of its ring; the CTA's are joined in its first warp's, the cluster's from
